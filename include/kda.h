@@ -379,6 +379,116 @@ int kda_decode_layer_step(const void *xq, const void *xk, const void *xv, const 
                           int dk, int dv, float q_scale, float l2_eps, float norm_eps,
                           void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Latent attention over a paged cache: the hybrid model's other token mixer
+ * ("Kimi K3 -> TPU v7x feasibility", section 2: latent-attention layers
+ * without rotary positions between the KDA layers; section 4.2 lists its
+ * ragged paged kernel).  Per token the layer keeps one row of 576 bf16 for
+ * all heads,
+ *     row = [c (512, the latent) | r (64, a key part shared by the heads)],
+ * and head h's keys and values are expansions of it: k = [c Wk_h | r]
+ * (128 + 64), v = c Wv_h (128).  Two equal forms:
+ *   absorbed   q' = [q_nope Wk_h^T | q_pe] (576) attends to the rows as they
+ *              are, and o' (512) is multiplied by Wv_h afterwards
+ *              (kda_latent_decode: each cached row is read once for all heads)
+ *   expanded   keys and values are multiplied out first (kda_latent_prefill:
+ *              320 instead of 1,088 multiply-adds per query, key and head)
+ * The products with Wk and Wv are the caller's.
+ *
+ * The cache is [P, page, 576] bf16; page is a power of two, 16 to 1024, and
+ * P * page < 2^31.  block_table [N, max_pages] int32: entry i of row b is the
+ * page of sequence b's positions i * page .. (i + 1) * page - 1; entries
+ * behind the last needed one are not read into any result and may hold
+ * anything.  The device arrays seq_lens, cu_seqlens and block_table are not
+ * seen by the host; the kernels check them: a length below 0 or above
+ * max_pages * page, or offsets that decrease or leave [0, T], raise bit 0 of
+ * the device error word, a page index outside [0, P) raises bit 1 (its rows
+ * read as zeros, writes to it are dropped), and nothing outside the buffers
+ * is touched.  Rows of x, q and o that no sequence holds (t >= cu_seqlens[N])
+ * are neither read into a result nor written.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Write the rows of new tokens into the cache.  Token i of sequence b's n new
+ * ones (packed rows cu_seqlens[b] ..) goes to position seq_lens[b] - n + i.
+ *
+ *   x          [T, 576] bf16
+ *   cache      [P, page, 576] bf16, the new tokens' rows written
+ *   seq_lens   [N] int32: lengths with the new tokens counted in
+ *   cu_seqlens [N + 1] int32, or NULL: one new token a sequence (then T = N)
+ *   norm_w     [512] fp32, or NULL: with it the latent part is stored as
+ *              c / sqrt(mean_j c_j^2 + eps) * norm_w_j, rounded once; without
+ *              it, and for the shared part always, the bits of x are kept
+ *   eps        >= 0
+ * No two new tokens may have the same place.  Returns KDA_OK or a
+ * kda_status_t; T = 0 is a no-op.
+ */
+int kda_latent_append(const void *x, void *cache, const int32_t *block_table, const int32_t *seq_lens,
+                      const int32_t *cu_seqlens, const float *norm_w, float eps, int N, int64_t T,
+                      int64_t P, int page, int max_pages, int d_latent, int d_pe, void *stream);
+
+/*
+ * Read the first cu_seqlens[b + 1] - cu_seqlens[b] rows of every sequence b
+ * into out [T, 576] bf16, packed in order (the input of the expansion that
+ * kda_latent_prefill's keys and values come from).  Returns KDA_OK or a
+ * kda_status_t; T = 0 is a no-op.
+ */
+int kda_latent_gather(const void *cache, const int32_t *block_table, const int32_t *cu_seqlens,
+                      void *out, int N, int64_t T, int64_t P, int page, int max_pages, int d_latent,
+                      int d_pe, void *stream);
+
+/*
+ * Absorbed attention of one or a few new tokens a sequence over the cache
+ * that holds them already.  Token i of sequence b's n new ones sees positions
+ * 0 .. seq_lens[b] - n + i; for each of its heads
+ *     s_p = scale <q, row_p>,  o = sum_p softmax(s)_p c_p,  lse = ln sum_p e^{s_p}.
+ * A token that sees nothing (an empty sequence) gets o = 0 and lse = -inf.
+ *
+ *   q          [T, H, 576] bf16
+ *   seq_lens   [N] int32: lengths with the new tokens counted in
+ *   cu_seqlens [N + 1] int32, or NULL: one new token a sequence (then T = N)
+ *   scale      > 0, finite
+ *   o          [T, H, 512] bf16, written
+ *   lse        [T, H] fp32, written, or NULL
+ *   workspace  kda_latent_decode_workspace_bytes(N, T, H, ...) bytes of device
+ *              memory, 256-byte aligned, alive and unshared until the call's
+ *              kernels finish; nothing in it has to be initialised
+ * The rows of the positions that a token sees are finite (what lies behind a
+ * sequence's end in its last page may be anything).  Returns KDA_OK or a
+ * kda_status_t; T = 0 is a no-op.
+ */
+int kda_latent_decode(const void *q, const void *cache, const int32_t *block_table,
+                      const int32_t *seq_lens, const int32_t *cu_seqlens, float scale, void *o,
+                      float *lse, int N, int64_t T, int H, int64_t P, int page, int max_pages,
+                      int d_latent, int d_pe, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace of kda_latent_decode (0 for invalid sizes). */
+size_t kda_latent_decode_workspace_bytes(int N, int64_t T, int H, int d_latent, int d_pe);
+
+/*
+ * Expanded attention of new tokens over their sequence's keys and values.
+ * Sequence b has the queries cu_seqlens_q[b] .. and the keys cu_seqlens_k[b]
+ * .. (packed); its queries are its last tokens, so with causal = 1 query i of
+ * nq sees keys 0 .. nk - nq + i (none where that is negative: o = 0,
+ * lse = -inf).  With causal = 0 every query sees all nk keys; two such
+ * results over disjoint keys join by their lse.
+ *
+ *   q          [Tq, H, 192] bf16: 128 channels, then the 64 of the shared part
+ *   kv         [Tk, H, 256] bf16: key (128), then value (128), of each head
+ *   k_pe       bf16 rows of 64, k_pe_stride elements apart (a multiple of 8:
+ *              576 for the shared part of gathered cache rows), one a token
+ *   scale      > 0, finite
+ *   o          [Tq, H, 128] bf16, written
+ *   lse        [Tq, H] fp32, written, or NULL
+ *   d_nope, d_pe, dv   must be 128, 64, 128
+ * The keys and values of every sequence are finite.  Returns KDA_OK or a
+ * kda_status_t; Tq = 0 is a no-op.
+ */
+int kda_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t k_pe_stride,
+                       const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, float scale,
+                       int causal, void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
+                       int d_nope, int d_pe, int dv, void *stream);
+
 /*
  * Gives back the memory that the library's workspace pool on the current
  * device keeps between kda_prefill_chunked / _events / _gated /
@@ -400,9 +510,11 @@ int kda_workspace_release(void);
  *          tensor memory and exit.  Also set when cu_seqlens breaks its
  *          precondition (an entry below 0 or above T, or a decrease), by
  *          the prefill paths and the conv prologue, which then touch no
- *          memory outside their buffers.
+ *          memory outside their buffers; by the latent-attention calls
+ *          also for a sequence length outside its block table.
  *   Bit 1: a kda_decode_step_pool or kda_decode_layer_step slot index was
- *          past the end of the pool.
+ *          past the end of the pool, or a page index of a latent-attention
+ *          call was outside the cache.
  *   Bit 2: the tensor-core prefill saw a gate g outside [-5, 0] or a NaN
  *          (its decay folding is sized for the model's gate bound).
  *   Bit 3: debug builds only (libkda_gb300_debug.so, built with

@@ -20,11 +20,20 @@ RMSNorm after it):
     out, S_out, conv_out = prefill_layer(xq, xk, xv, conv_w, g, beta, gate, norm_w, cu_seqlens)
     out = decode_layer_step(xq, xk, xv, conv_w, conv_pool, g, beta, gate, norm_w, S_pool)
 
-Shapes (token-major): q, k, g [T, H, 128]; v [T, H, 128]; beta [T, H];
+The hybrid model's other token mixer, latent attention over a paged cache
+(bf16 rows of 512 latent + 64 shared key channels, [P, page, 576]):
+
+    latent_append(x, cache, block_table, seq_lens, cu_seqlens, norm_w=w)   # new tokens' rows
+    o, lse = latent_decode(q, cache, block_table, seq_lens, cu_seqlens)    # absorbed, over the pages
+    rows = latent_gather(cache, block_table, cu_seqlens_k, total)          # rows back, to expand
+    o, lse = latent_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k)       # expanded, causal
+
+Shapes of the recurrence (token-major): q, k, g [T, H, 128]; v [T, H, 128]; beta [T, H];
 S [N, H, 128, 128] fp32; q/k/v bf16 or fp32, g/beta fp32.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -34,7 +43,8 @@ import torch
 __all__ = ["prefill_chunked", "prefill_chunked_noalloc", "prefill_chunked_events",
            "prefill_workspace_bytes", "decode_step",
            "decode_step_pool", "conv_prologue", "prefill_chunked_gated", "prefill_layer",
-           "decode_layer_step", "device_error", "lib",
+           "decode_layer_step", "latent_append", "latent_gather", "latent_decode",
+           "latent_decode_workspace_bytes", "latent_prefill", "device_error", "lib",
            "KDAError", "KDA_BF16", "KDA_F32", "library_path"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -108,6 +118,19 @@ def lib() -> ctypes.CDLL:
         L.kda_decode_layer_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32,
                                             vp, i32, i32, i32, i32, f32, f32, f32, vp]
         L.kda_decode_layer_step.restype = i32
+        L.kda_latent_append.argtypes = [vp, vp, vp, vp, vp, vp, f32, i32, i64, i64, i32, i32, i32,
+                                        i32, vp]
+        L.kda_latent_append.restype = i32
+        L.kda_latent_gather.argtypes = [vp, vp, vp, vp, i32, i64, i64, i32, i32, i32, i32, vp]
+        L.kda_latent_gather.restype = i32
+        L.kda_latent_decode.argtypes = [vp, vp, vp, vp, vp, f32, vp, vp, i32, i64, i32, i64, i32,
+                                        i32, i32, i32, vp, ctypes.c_size_t, vp]
+        L.kda_latent_decode.restype = i32
+        L.kda_latent_decode_workspace_bytes.argtypes = [i32, i64, i32, i32, i32]
+        L.kda_latent_decode_workspace_bytes.restype = ctypes.c_size_t
+        L.kda_latent_prefill.argtypes = [vp, vp, vp, i64, vp, vp, f32, i32, vp, vp, i32, i64, i64,
+                                         i32, i32, i32, i32, vp]
+        L.kda_latent_prefill.restype = i32
         L.kda_workspace_release.argtypes = []
         L.kda_workspace_release.restype = i32
         L.kda_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
@@ -481,6 +504,185 @@ def decode_layer_step(xq: torch.Tensor, xk: torch.Tensor, xv: torch.Tensor, conv
     if rc != 0:
         raise KDAError(rc, "kda_decode_layer_step")
     return out
+
+
+# ------------------------------------------------------------ latent attention
+LATENT = 512                  # latent width of a cached row
+LATENT_PE = 64                # its key part shared by the heads
+LATENT_ROW = LATENT + LATENT_PE
+LATENT_SCALE = (DK + LATENT_PE) ** -0.5   # 1/sqrt(expanded key width)
+
+
+def _on(device: torch.device):
+    """The device's guard where it is not the current one (a launch goes to
+    the current device)."""
+    if device.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _check_cache(cache, block_table, N, dev):
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
+        raise ValueError("cache must be a [P, page, %d] tensor" % LATENT_ROW)
+    _check("cache", cache, torch.bfloat16, (cache.shape[0], cache.shape[1], LATENT_ROW), dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a [N, max_pages] tensor")
+    _check("block_table", block_table, torch.int32, (N, block_table.shape[1]), dev)
+
+
+def latent_append(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                  seq_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                  norm_w: Optional[torch.Tensor] = None, eps: float = NORM_EPS,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Write new tokens' rows into the paged latent cache (``kda_latent_append``).
+
+    x [T, 576] bf16; cache [P, page, 576] bf16, updated in place; block_table
+    [N, max_pages], seq_lens [N] (the new tokens counted in) and cu_seqlens
+    [N + 1] int32 (None: one new token a sequence).  With norm_w [512] fp32
+    the latent part is RMS-normalised.  Returns cache.
+    """
+    dev = x.device
+    T, N = x.shape[0], seq_lens.numel()
+    with _on(dev):
+        _check("x", x, torch.bfloat16, (T, LATENT_ROW), dev)
+        _check_cache(cache, block_table, N, dev)
+        _check("seq_lens", seq_lens, torch.int32, (N,), dev)
+        if cu_seqlens is not None:
+            _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
+        if norm_w is not None:
+            _check("norm_w", norm_w, torch.float32, (LATENT,), dev)
+        rc = lib().kda_latent_append(_p(x), _p(cache), _p(block_table), _p(seq_lens),
+                                     _p(cu_seqlens), _p(norm_w), float(eps), N, T, cache.shape[0],
+                                     cache.shape[1], block_table.shape[1], LATENT, LATENT_PE,
+                                     _stream(dev, stream))
+    if rc != 0:
+        raise KDAError(rc, "kda_latent_append")
+    return cache
+
+
+def latent_gather(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                  total: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Read every sequence's first rows back, packed by cu_seqlens
+    (``kda_latent_gather``).  total: the packed length cu_seqlens[N] (where
+    ``out`` [total, 576] bf16 is not given).  Returns out."""
+    dev = cache.device
+    N = cu_seqlens.numel() - 1
+    with _on(dev):
+        if out is None:
+            if total is None:
+                raise ValueError("give the packed length (total) or the output (out)")
+            with torch.cuda.stream(stream):
+                out = torch.empty((total, LATENT_ROW), dtype=torch.bfloat16, device=dev)
+        T = out.shape[0]
+        _check_cache(cache, block_table, N, dev)
+        _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
+        _check("out", out, torch.bfloat16, (T, LATENT_ROW), dev)
+        rc = lib().kda_latent_gather(_p(cache), _p(block_table), _p(cu_seqlens), _p(out), N, T,
+                                     cache.shape[0], cache.shape[1], block_table.shape[1], LATENT,
+                                     LATENT_PE, _stream(dev, stream))
+    if rc != 0:
+        raise KDAError(rc, "kda_latent_gather")
+    return out
+
+
+def latent_decode_workspace_bytes(N: int, T: int, H: int) -> int:
+    """Bytes of workspace of ``latent_decode`` (``kda_latent_decode_workspace_bytes``)."""
+    return int(lib().kda_latent_decode_workspace_bytes(int(N), int(T), int(H), LATENT, LATENT_PE))
+
+
+def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                  seq_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                  scale: float = LATENT_SCALE, o: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None
+                  ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Absorbed attention of one or a few new tokens a sequence over the paged
+    cache that holds them already (``kda_latent_decode``).
+
+    q [T, H, 576] bf16; cache [P, page, 576] bf16; block_table [N, max_pages],
+    seq_lens [N] and cu_seqlens [N + 1] int32 (None: one token a sequence).
+    Returns (o [T, H, 512] bf16, lse [T, H] fp32).  The workspace
+    (``latent_decode_workspace_bytes``) comes from torch's allocator unless
+    one is given.
+    """
+    dev = q.device
+    T, H, N = q.shape[0], q.shape[1], seq_lens.numel()
+    with _on(dev):
+        _check("q", q, torch.bfloat16, (T, H, LATENT_ROW), dev)
+        _check_cache(cache, block_table, N, dev)
+        _check("seq_lens", seq_lens, torch.int32, (N,), dev)
+        if cu_seqlens is not None:
+            _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
+        need = latent_decode_workspace_bytes(N, T, H)
+        with torch.cuda.stream(stream):       # memory of the stream that uses it
+            if o is None:
+                o = torch.empty((T, H, LATENT), dtype=torch.bfloat16, device=dev)
+            if lse is None:
+                lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+            if workspace is None and need > 0:
+                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        _check("o", o, torch.bfloat16, (T, H, LATENT), dev)
+        _check("lse", lse, torch.float32, (T, H), dev)
+        nbytes = 0
+        if workspace is not None:
+            if workspace.device != dev or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+            nbytes = workspace.numel() * workspace.element_size()
+        rc = lib().kda_latent_decode(_p(q), _p(cache), _p(block_table), _p(seq_lens),
+                                     _p(cu_seqlens), float(scale), _p(o), _p(lse), N, T, H,
+                                     cache.shape[0], cache.shape[1], block_table.shape[1], LATENT,
+                                     LATENT_PE, _p(workspace), nbytes, _stream(dev, stream))
+    if rc != 0:
+        raise KDAError(rc, "kda_latent_decode")
+    return o, lse
+
+
+def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seqlens: torch.Tensor,
+                   cu_seqlens_k: Optional[torch.Tensor] = None, scale: float = LATENT_SCALE,
+                   causal: bool = True, o: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Expanded attention of new tokens over their sequence's keys and values
+    (``kda_latent_prefill``).
+
+    q [Tq, H, 192] bf16; kv [Tk, H, 256] bf16 (key 128 | value 128); k_pe
+    [Tk, 64] bf16, its rows any multiple of 8 elements apart (so that
+    ``rows[:, 512:]`` of gathered cache rows is taken as it is); cu_seqlens
+    and cu_seqlens_k [N + 1] int32 (None: the same).  The queries of a
+    sequence are its last tokens.  Returns (o [Tq, H, 128] bf16, lse [Tq, H]
+    fp32).
+    """
+    dev = q.device
+    Tq, H, N, Tk = q.shape[0], q.shape[1], cu_seqlens.numel() - 1, kv.shape[0]
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens
+    with _on(dev):
+        _check("q", q, torch.bfloat16, (Tq, H, DK + LATENT_PE), dev)
+        _check("kv", kv, torch.bfloat16, (Tk, H, DK + DV), dev)
+        if (k_pe.device != dev or k_pe.dtype != torch.bfloat16 or tuple(k_pe.shape) != (Tk, LATENT_PE)
+                or (Tk > 0 and k_pe.stride(1) != 1)):
+            raise ValueError("k_pe must be [%d, %d] bfloat16 on %s with dense rows" % (Tk, LATENT_PE, dev))
+        # the stride of a dimension of one row means nothing
+        pe_stride = k_pe.stride(0) if Tk > 1 else LATENT_PE
+        _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
+        _check("cu_seqlens_k", cu_seqlens_k, torch.int32, (N + 1,), dev)
+        with torch.cuda.stream(stream):
+            if o is None:
+                o = torch.empty((Tq, H, DV), dtype=torch.bfloat16, device=dev)
+            if lse is None:
+                lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
+        _check("o", o, torch.bfloat16, (Tq, H, DV), dev)
+        _check("lse", lse, torch.float32, (Tq, H), dev)
+        rc = lib().kda_latent_prefill(_p(q), _p(kv), _p(k_pe), pe_stride, _p(cu_seqlens),
+                                      _p(cu_seqlens_k), float(scale), int(bool(causal)), _p(o),
+                                      _p(lse), N, Tq, Tk, H, DK, LATENT_PE, DV,
+                                      _stream(dev, stream))
+    if rc != 0:
+        raise KDAError(rc, "kda_latent_prefill")
+    return o, lse
 
 
 def device_error(reset: bool = True) -> int:

@@ -2,16 +2,27 @@
 // Declarations and the contract of each call are in include/kda.h.
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/kda.h"
 #include "kda_internal.h"
 
 namespace {
 
-constexpr int kVersion = 200;   // 0.2.0: caller-owned prefill workspace
+constexpr int kVersion = 300;   // 0.3.0: latent attention over a paged cache
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+
+// Sizes shared by the calls on a paged latent cache.
+int latent_cache_dims(int N, int64_t T, int64_t P, int page, int max_pages, int d_latent, int d_pe) {
+    if (d_latent != kda::kLatentDim || d_pe != kda::kLatentPeDim) return KDA_ERR_DIM;
+    if (N < 1 || T < 0 || T >= (int64_t(1) << 31) || P < 1 || max_pages < 1) return KDA_ERR_DIM;
+    if (page < 16 || page > 1024 || (page & (page - 1)) != 0) return KDA_ERR_DIM;
+    if (P * page >= (int64_t(1) << 31) || P >= (int64_t(1) << 31)) return KDA_ERR_DIM;
+    return KDA_OK;
+}
 
 }  // namespace
 
@@ -23,13 +34,13 @@ const char *kda_status_string(int status) {
     switch (status) {
         case KDA_OK: return "ok";
         case KDA_ERR_NULL: return "a required pointer is NULL";
-        case KDA_ERR_DIM: return "unsupported or inconsistent sizes (dk = dv = 128, N >= 1, H >= 1)";
+        case KDA_ERR_DIM: return "unsupported or inconsistent sizes (dk = dv = 128, N >= 1, H >= 1; latent rows 512 + 64, page a power of two)";
         case KDA_ERR_CHUNK: return "chunk must be 16, 32 or 64";
         case KDA_ERR_ALIGN: return "a pointer is not 16-byte aligned";
         case KDA_ERR_DTYPE: return "dtype must be KDA_BF16 or KDA_F32";
         case KDA_ERR_WORKSPACE: return "workspace could not be allocated or is too small";
         case KDA_ERR_CUDA: return "CUDA launch error";
-        case KDA_ERR_VALUE: return "a scalar argument is out of range (eps >= 0, finite q_scale)";
+        case KDA_ERR_VALUE: return "a scalar argument is out of range (eps >= 0, finite q_scale, scale > 0)";
         default: return "unknown status";
     }
 }
@@ -279,18 +290,101 @@ int kda_decode_layer_step(const void *xq, const void *xk, const void *xv, const 
                                                 static_cast<cudaStream_t>(stream)));
 }
 
+int kda_latent_append(const void *x, void *cache, const int32_t *block_table, const int32_t *seq_lens,
+                      const int32_t *cu_seqlens, const float *norm_w, float eps, int N, int64_t T,
+                      int64_t P, int page, int max_pages, int d_latent, int d_pe, void *stream) {
+    const int d = latent_cache_dims(N, T, P, page, max_pages, d_latent, d_pe);
+    if (d != KDA_OK) return d;
+    if (!cu_seqlens && T != N) return KDA_ERR_DIM;
+    if (!(eps >= 0.f)) return KDA_ERR_VALUE;
+    if (T == 0) return KDA_OK;
+    if (!x || !cache || !block_table || !seq_lens) return KDA_ERR_NULL;
+    const void *ptrs[] = {x, cache, block_table, seq_lens, cu_seqlens, norm_w};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_latent_append(x, cache, block_table, seq_lens, cu_seqlens, norm_w,
+                                                 eps, N, T, P, page, max_pages,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+int kda_latent_gather(const void *cache, const int32_t *block_table, const int32_t *cu_seqlens,
+                      void *out, int N, int64_t T, int64_t P, int page, int max_pages, int d_latent,
+                      int d_pe, void *stream) {
+    const int d = latent_cache_dims(N, T, P, page, max_pages, d_latent, d_pe);
+    if (d != KDA_OK) return d;
+    if (T == 0) return KDA_OK;
+    if (!cache || !block_table || !cu_seqlens || !out) return KDA_ERR_NULL;
+    const void *ptrs[] = {cache, block_table, cu_seqlens, out};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_latent_gather(cache, block_table, cu_seqlens, out, N, T, P, page,
+                                                 max_pages, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_latent_decode_workspace_bytes(int N, int64_t T, int H, int d_latent, int d_pe) {
+    if (d_latent != kda::kLatentDim || d_pe != kda::kLatentPeDim || N < 1 || T < 1 || H < 1 ||
+        T * H >= (int64_t(1) << 31))
+        return 0;
+    return kda::latent_decode_workspace_bytes(N, T, H);
+}
+
+int kda_latent_decode(const void *q, const void *cache, const int32_t *block_table,
+                      const int32_t *seq_lens, const int32_t *cu_seqlens, float scale, void *o,
+                      float *lse, int N, int64_t T, int H, int64_t P, int page, int max_pages,
+                      int d_latent, int d_pe, void *workspace, size_t ws_bytes, void *stream) {
+    const int d = latent_cache_dims(N, T, P, page, max_pages, d_latent, d_pe);
+    if (d != KDA_OK) return d;
+    if (H < 1 || T * H >= (int64_t(1) << 31) || (!cu_seqlens && T != N)) return KDA_ERR_DIM;
+    if (!(scale > 0.f) || scale - scale != 0.f) return KDA_ERR_VALUE;
+    if (T == 0) return KDA_OK;
+    if (!q || !cache || !block_table || !seq_lens || !o) return KDA_ERR_NULL;
+    const void *ptrs[] = {q, cache, block_table, seq_lens, cu_seqlens, o, lse};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_ALIGN;
+    const size_t need = kda::latent_decode_workspace_bytes(N, T, H);
+    if (need > 0 && (!workspace || ws_bytes < need)) return KDA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_latent_decode(q, cache, block_table, seq_lens, cu_seqlens, scale, o,
+                                                 lse, N, T, H, P, page, max_pages, workspace,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+int kda_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t k_pe_stride,
+                       const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, float scale,
+                       int causal, void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
+                       int d_nope, int d_pe, int dv, void *stream) {
+    if (d_nope != kda::kDK || d_pe != kda::kLatentPeDim || dv != kda::kDV) return KDA_ERR_DIM;
+    if (N < 1 || H < 1 || Tq < 0 || Tk < 0 || Tq * H >= (int64_t(1) << 31) ||
+        Tk * H >= (int64_t(1) << 31))
+        return KDA_ERR_DIM;
+    if (k_pe_stride < d_pe || k_pe_stride % 8 != 0 || k_pe_stride >= (int64_t(1) << 31)) return KDA_ERR_DIM;
+    if (!(scale > 0.f) || scale - scale != 0.f || (causal != 0 && causal != 1)) return KDA_ERR_VALUE;
+    if (Tq == 0) return KDA_OK;
+    if (!q || !cu_seqlens_q || !cu_seqlens_k || !o) return KDA_ERR_NULL;
+    if (Tk > 0 && (!kv || !k_pe)) return KDA_ERR_NULL;
+    const void *ptrs[] = {q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, o, lse};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_latent_prefill(q, kv, k_pe, k_pe_stride, cu_seqlens_q, cu_seqlens_k,
+                                                  scale, causal != 0, o, lse, N, Tq, Tk, H,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
 int kda_workspace_release(void) { return cuda_status(kda::release_workspace_pool()); }
 
 int kda_device_error(unsigned int *code, int reset) {
     if (!code) return KDA_ERR_NULL;
-    unsigned int a = 0, b = 0, c = 0, d = 0;
+    unsigned int a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
     const cudaError_t e1 = kda::read_device_error(&a, reset != 0);
     const cudaError_t e2 = kda::read_decode_error(&b, reset != 0);
     const cudaError_t e3 = kda::read_layer_error(&c, reset != 0);
     const cudaError_t e4 = kda::read_simt_error(&d, reset != 0);
-    *code = a | b | c | d;
-    const cudaError_t e = e1 != cudaSuccess ? e1 : (e2 != cudaSuccess ? e2 : (e3 != cudaSuccess ? e3 : e4));
-    return cuda_status(e);
+    const cudaError_t e5 = kda::read_latent_error(&f, reset != 0);
+    const cudaError_t e6 = kda::read_latent_prefill_error(&g, reset != 0);
+    *code = a | b | c | d | f | g;
+    for (const cudaError_t e : {e1, e2, e3, e4, e5, e6})
+        if (e != cudaSuccess) return cuda_status(e);
+    return KDA_OK;
 }
 
 }  // extern "C"

@@ -9,6 +9,8 @@ namespace kda {
 
 constexpr int kDK = 128;
 constexpr int kDV = 128;
+constexpr int kLatentDim = 512;    // latent part of a cached row (the absorbed value width)
+constexpr int kLatentPeDim = 64;   // its key part shared by the heads
 
 // Bits of the device error word (kda_device_error).
 constexpr unsigned kErrWait = 1u;        // a bounded wait gave up, or cu_seqlens broke the call's precondition
@@ -140,6 +142,30 @@ cudaError_t launch_decode_layer(const void *xq, const void *xk, const void *xv, 
                                 const int32_t *slots, int P, float *out, int B, int H,
                                 float q_scale, float l2_eps, float norm_eps, cudaStream_t stream);
 cudaError_t read_layer_error(unsigned int *code, bool reset);
+
+// Latent attention over a paged cache of [P, page, 576] bf16 rows
+// (kda_latent.cu): write new tokens' rows, read rows back in order, and
+// attend with queries already absorbed into the latent.  cu == nullptr: one
+// new token a sequence.
+cudaError_t launch_latent_append(const void *x, void *cache, const int32_t *table,
+                                 const int32_t *seq_lens, const int32_t *cu, const float *norm_w,
+                                 float eps, int N, int64_t T, int64_t P, int page, int max_pages,
+                                 cudaStream_t stream);
+cudaError_t launch_latent_gather(const void *cache, const int32_t *table, const int32_t *cu, void *out,
+                                 int N, int64_t T, int64_t P, int page, int max_pages,
+                                 cudaStream_t stream);
+size_t latent_decode_workspace_bytes(int N, int64_t T, int H);
+cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t *table,
+                                 const int32_t *seq_lens, const int32_t *cu, float scale, void *o,
+                                 float *lse, int N, int64_t T, int H, int64_t P, int page,
+                                 int max_pages, void *ws, cudaStream_t stream);
+cudaError_t read_latent_error(unsigned int *code, bool reset);
+// Attention with expanded keys and values (kda_latent_prefill.cu).
+cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t pe_stride,
+                                  const int32_t *cu_q, const int32_t *cu_k, float scale, bool causal,
+                                  void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
+                                  cudaStream_t stream);
+cudaError_t read_latent_prefill_error(unsigned int *code, bool reset);
 
 // The conv prologue's arithmetic, shared by the prologue kernel and the
 // layer prefill that fuses it: bf16 pairs (low half = even channel) to and

@@ -1,0 +1,247 @@
+// The paged latent cache: writing new tokens' rows (append), reading a
+// sequence's rows back in order (gather), and attention of one or a few new
+// tokens over the pages in latent space (decode).
+//
+// A cached row is [c | r], 512 latent and 64 shared key channels in bf16.
+// With the value and key expansions absorbed into q and into the caller's
+// output product, a (token, head) row x [576] attends as
+//   s_p = scale <x, row_p>,   o = sum_p softmax(s)_p c_p,   lse = ln sum_p e^{s_p}
+// over the positions p it may see: those up to its own.
+#include <math_constants.h>
+
+#include <algorithm>
+
+#include "kda_internal.h"
+#include "latent_common.cuh"
+
+namespace kda {
+
+// Error word of this file's kernels (bit 0: cu_seqlens or a length broke its
+// precondition; bit 1: a page index outside the cache).
+__device__ unsigned int g_kda_latent_error = 0;
+
+namespace {
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+
+// ---------------------------------------------------------------- append
+// A warp a token: the row's 72 16-byte pieces are read once (lane l holds
+// latent pieces l and 32 + l, lanes 0..7 one of the shared part), the sum of
+// squares is a warp reduction in fp32, each value is rounded to bf16 once.
+// Bound by HBM: 1,152 B in and out a token.
+constexpr int kAppendThreads = 256;
+
+__device__ __forceinline__ float sumsq8(uint4 u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = bf2_to_f2(w[e]);
+        s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
+    }
+    return s;
+}
+__device__ __forceinline__ uint4 scale8(uint4 u, float n, const float *w) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(w));
+    const float4 b = __ldg(reinterpret_cast<const float4 *>(w) + 1);
+    const float2 x0 = bf2_to_f2(u.x), x1 = bf2_to_f2(u.y), x2 = bf2_to_f2(u.z), x3 = bf2_to_f2(u.w);
+    return make_uint4(f2_to_bf2(make_float2(x0.x * n * a.x, x0.y * n * a.y)),
+                      f2_to_bf2(make_float2(x1.x * n * a.z, x1.y * n * a.w)),
+                      f2_to_bf2(make_float2(x2.x * n * b.x, x2.y * n * b.y)),
+                      f2_to_bf2(make_float2(x3.x * n * b.z, x3.y * n * b.w)));
+}
+
+__global__ void __launch_bounds__(kAppendThreads)
+latent_append_kernel(const uint4 *__restrict__ x, uint4 *__restrict__ cache, PagedRows pages,
+                     const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ cu,
+                     const float *__restrict__ norm_w, float eps, int N, int T) {
+    const int t = (int)((blockIdx.x * (unsigned)kAppendThreads + threadIdx.x) >> 5);
+    const int lane = threadIdx.x & 31;
+    if (t >= T) return;
+    // the row does not wait for the walk to its place
+    const uint4 *src = x + (size_t)t * kRowChunks;
+    uint4 a = __ldcs(src + lane), b = __ldcs(src + 32 + lane), c = make_uint4(0, 0, 0, 0);
+    if (lane < 8) c = __ldcs(src + 64 + lane);
+    const int s = seq_of_token(cu, N, t);
+    if (s < 0) return;                     // behind the last sequence
+    const int start = cu ? cu[s] : s, count = cu ? cu[s + 1] - start : 1;
+    const long long pos = (long long)seq_lens[s] - count + (t - start);
+    if (pos < 0 || pos >= pages.max_len()) {
+        if (lane == 0) atomicOr(&g_kda_latent_error, kErrWait);
+        return;
+    }
+    const int64_t row = pages.row(s, (int)pos);
+    if (row < 0) {
+        if (lane == 0) atomicOr(&g_kda_latent_error, kErrSlot);
+        return;
+    }
+    if (norm_w) {
+        const float ss = warp_sum(sumsq8(a) + sumsq8(b));
+        const float n = 1.f / sqrtf(ss * (1.f / kLatent) + eps);
+        a = scale8(a, n, norm_w + 8 * lane);
+        b = scale8(b, n, norm_w + 256 + 8 * lane);
+    }
+    uint4 *dst = cache + (size_t)row * kRowChunks;
+    dst[lane] = a;
+    dst[32 + lane] = b;
+    if (lane < 8) dst[64 + lane] = c;
+}
+
+// ---------------------------------------------------------------- gather
+// A warp copies four consecutive rows: 288 16-byte pieces, nine a lane, all
+// in flight at once; lanes 0..3 walk to the four source rows.  Bound by HBM:
+// 1,152 B in and out a row.
+constexpr int kGatherThreads = 256;
+
+__global__ void __launch_bounds__(kGatherThreads)
+latent_gather_kernel(const uint4 *__restrict__ cache, PagedRows pages, const int32_t *__restrict__ cu,
+                     uint4 *__restrict__ out, int N, int T) {
+    const int64_t t0 = 4 * (int64_t)((blockIdx.x * (unsigned)kGatherThreads + threadIdx.x) >> 5);
+    const int lane = threadIdx.x & 31;
+    if (t0 >= T) return;
+    // source row of output row t0 + lane; -2: no such row, -1: its page is bad
+    long long src = -2;
+    if (lane < 4 && t0 + lane < T) {
+        const int t = (int)t0 + lane;
+        const int s = seq_of_token(cu, N, t);
+        if (s >= 0) {
+            const int pos = t - cu[s];
+            if (pos < pages.max_len()) src = pages.row(s, pos);
+            else src = -1;
+            if (src < 0) atomicOr(&g_kda_latent_error, pos < pages.max_len() ? kErrSlot : kErrWait);
+        }
+    }
+    uint4 v[9];
+    long long from[9];
+#pragma unroll
+    for (int i = 0; i < 9; ++i) {
+        const int e = 32 * i + lane;
+        from[i] = __shfl_sync(0xffffffffu, src, e / kRowChunks);
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (from[i] >= 0) v[i] = __ldcs(cache + (size_t)from[i] * kRowChunks + e % kRowChunks);
+    }
+    uint4 *dst = out + (size_t)t0 * kRowChunks;
+#pragma unroll
+    for (int i = 0; i < 9; ++i)
+        if (from[i] > -2) dst[32 * i + lane] = v[i];
+}
+
+// ---------------------------------------------------------------- decode
+// A block a (token, head) row: positions in tiles of 64, a warp a position
+// at a time for the scores, a running maximum and sum, two latent columns a
+// thread for the output.
+constexpr int kDecThreads = 256;
+constexpr int kDecTile = 64;
+
+__global__ void __launch_bounds__(kDecThreads)
+latent_decode_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ cache,
+                     PagedRows pages, const int32_t *__restrict__ seq_lens,
+                     const int32_t *__restrict__ cu, float scale, __nv_bfloat16 *__restrict__ o,
+                     float *__restrict__ lse, int N, int T, int H) {
+    const int t = (int)(blockIdx.x / (unsigned)H);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int s = seq_of_token(cu, N, t);
+    if (s < 0) return;
+    const int start = cu ? cu[s] : s, count = cu ? cu[s + 1] - start : 1;
+    int L = seq_lens[s];
+    if (L < 0 || L > pages.max_len()) {
+        if (tid == 0) atomicOr(&g_kda_latent_error, kErrWait);
+        L = max(0, min(L, pages.max_len()));
+    }
+    const int seen = max(0, L - count + (t - start) + 1);
+    __shared__ float sq[kLatentRow], sc[kDecTile];
+    __shared__ long long srow[kDecTile];
+    const size_t row = blockIdx.x;
+    for (int i = tid; i < kLatentRow; i += kDecThreads) sq[i] = __bfloat162float(q[row * kLatentRow + i]);
+    float m = -CUDART_INF_F, l = 0.f, o0 = 0.f, o1 = 0.f;
+    for (int p0 = 0; p0 < seen; p0 += kDecTile) {
+        const int n = min(kDecTile, seen - p0);
+        __syncthreads();
+        if (tid < n) {
+            srow[tid] = pages.row(s, p0 + tid);
+            if (srow[tid] < 0) atomicOr(&g_kda_latent_error, kErrSlot);
+        }
+        __syncthreads();
+        for (int j = warp; j < n; j += kDecThreads / 32) {
+            float d = 0.f;
+            if (srow[j] >= 0)
+                for (int i = lane; i < kLatentRow; i += 32)
+                    d = fmaf(sq[i], __bfloat162float(cache[(size_t)srow[j] * kLatentRow + i]), d);
+            d = warp_sum(d);
+            if (lane == 0) sc[j] = d * scale;
+        }
+        __syncthreads();
+        float mt = m;
+        for (int j = 0; j < n; ++j) mt = fmaxf(mt, sc[j]);
+        const float a = m == -CUDART_INF_F ? 0.f : expf(m - mt);
+        l *= a; o0 *= a; o1 *= a;
+        m = mt;
+        for (int j = 0; j < n; ++j) {
+            const float p = expf(sc[j] - m);
+            l += p;
+            if (srow[j] >= 0) {
+                const float2 c = bf2_to_f2(reinterpret_cast<const uint32_t *>(cache + (size_t)srow[j] * kLatentRow)[tid]);
+                o0 = fmaf(p, c.x, o0);
+                o1 = fmaf(p, c.y, o1);
+            }
+        }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    reinterpret_cast<uint32_t *>(o + row * kLatent)[tid] = f2_to_bf2(make_float2(o0 * inv, o1 * inv));
+    if (lse && tid == 0) lse[row] = l > 0.f ? m + logf(l) : -CUDART_INF_F;
+}
+
+PagedRows paged(const int32_t *table, int64_t P, int page, int max_pages) {
+    int lg = 0;
+    while ((1 << lg) < page) ++lg;
+    return PagedRows{table, P, lg, max_pages};
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const void *x, void *cache, const int32_t *table,
+                                 const int32_t *seq_lens, const int32_t *cu, const float *norm_w,
+                                 float eps, int N, int64_t T, int64_t P, int page, int max_pages,
+                                 cudaStream_t stream) {
+    const unsigned blocks = (unsigned)((T * 32 + kAppendThreads - 1) / kAppendThreads);
+    latent_append_kernel<<<blocks, kAppendThreads, 0, stream>>>(
+        static_cast<const uint4 *>(x), static_cast<uint4 *>(cache), paged(table, P, page, max_pages),
+        seq_lens, cu, norm_w, eps, N, (int)T);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_latent_gather(const void *cache, const int32_t *table, const int32_t *cu, void *out,
+                                 int N, int64_t T, int64_t P, int page, int max_pages,
+                                 cudaStream_t stream) {
+    const unsigned blocks = (unsigned)(((T + 3) / 4 * 32 + kGatherThreads - 1) / kGatherThreads);
+    latent_gather_kernel<<<blocks, kGatherThreads, 0, stream>>>(
+        static_cast<const uint4 *>(cache), paged(table, P, page, max_pages), cu,
+        static_cast<uint4 *>(out), N, (int)T);
+    return cudaGetLastError();
+}
+
+size_t latent_decode_workspace_bytes(int, int64_t, int) { return 0; }
+
+cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t *table,
+                                 const int32_t *seq_lens, const int32_t *cu, float scale, void *o,
+                                 float *lse, int N, int64_t T, int H, int64_t P, int page,
+                                 int max_pages, void *, cudaStream_t stream) {
+    latent_decode_kernel<<<(unsigned)(T * H), kDecThreads, 0, stream>>>(
+        static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(cache),
+        paged(table, P, page, max_pages), seq_lens, cu, scale, static_cast<__nv_bfloat16 *>(o), lse, N,
+        (int)T, H);
+    return cudaGetLastError();
+}
+
+cudaError_t read_latent_error(unsigned int *code, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_kda_latent_error, sizeof(unsigned int));
+    if (e != cudaSuccess || !reset) return e;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_kda_latent_error, &zero, sizeof(unsigned int));
+}
+
+}  // namespace kda

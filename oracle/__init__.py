@@ -21,9 +21,12 @@ Contents
                 norm before it, per-head RMSNorm + sigmoid gate after it
                 ("Colibri Kimi K3 Metal backend", sections 8.3 and 8.4), and
                 the whole-layer prefill and decode compositions.
+  latent.py     latent attention over a paged cache: the rows written, read
+                and attended to, in the absorbed and the expanded form.
 
 Parity pins: every function here is pinned by the CPU tests in
-``tests/test_oracle_pins.py`` and ``tests/test_oracle_layer_pins.py``
+``tests/test_oracle_pins.py``, ``tests/test_oracle_layer_pins.py`` and
+``tests/test_oracle_latent_pins.py``
 (closed forms, exact retrieval, brute force, hand-worked examples, numpy's
 convolution, the chunked restatement, invariants).
 """

@@ -1,0 +1,543 @@
+"""GPU parity of latent attention over the paged cache, through the public
+calls, against the fp64 oracle: rows written (``latent_append``) and read
+back (``latent_gather``), absorbed attention over the pages
+(``latent_decode``), expanded attention (``latent_prefill``), and the layer
+as they make it together."""
+import numpy as np
+import pytest
+
+from oracle import latent as ol
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 192 ** -0.5
+HALF = 2.0 ** -8            # half a bf16 step, relative
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from kda_linear_attention_gb300 import build
+    build.build()
+    _kda().device_error(reset=True)
+    yield
+
+
+def _kda():
+    import kda_linear_attention_gb300 as kda
+    return kda
+
+
+def _rng(seed):
+    return np.random.Generator(np.random.PCG64(seed))
+
+
+def _bf(a):
+    """fp64 numpy -> (bf16 device tensor, its exact values as fp64)."""
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(torch.bfloat16)
+    return t.cuda(), t.double().numpy()
+
+
+def _i32(a):
+    import torch
+    return torch.tensor(np.asarray(a), dtype=torch.int32).cuda()
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _clear(want=0):
+    import torch
+    torch.cuda.synchronize()
+    assert _kda().device_error(reset=True) == want
+
+
+def check(o, lse, r, what):
+    """o and lse against the oracle's result, element by element.
+
+    A score is an fp32 sum of at most 36 products of 16 terms each, exact
+    before they are added; an addition is off by at most two units of 2^-23 of
+    the row's largest sum |x||k| scale (r.mag), so a score by d = 80 2^-23 mag
+    and a probability by the factor 1 +- (2 d + 2^-20) (its own score, the sum
+    it is divided by, exponential and reciprocal).  Each probability is then
+    rounded to bf16 for its product with the values: independent errors of at
+    most HALF p |v|, whose sum exceeds 7 sqrt(sum (HALF p v)^2) with
+    probability below 2 e^-24.5 (Hoeffding).  The sum is rounded to bf16
+    once.  lse is not touched by the rounded probabilities."""
+    o, lse = _np(o), _np(lse)
+    d = 80 * 2.0 ** -23 * r.mag
+    assert np.array_equal(np.isneginf(lse), np.isneginf(r.lse)), what + ": rows that see nothing"
+    live = ~np.isneginf(r.lse)
+    err = np.abs(lse[live] - r.lse[live])
+    lim = d[live] + 2.0 ** -20 * (1 + np.abs(r.lse[live]))
+    assert (err <= lim).all(), "%s: lse off by %.3g (allowed %.3g)" % (what, err.max(), lim[err.argmax()])
+    err = np.abs(o - r.o)
+    lim = (HALF * np.abs(r.o) + 7 * HALF * r.sqsum) * (1 + HALF) + (2 * d + 2.0 ** -20)[..., None] * r.absum
+    bad = ~(err <= lim)
+    assert not bad.any(), "%s: %d of %d outputs off, first at %s: %.6g for %.6g (allowed %.3g)" % (
+        what, bad.sum(), bad.size, np.argwhere(bad)[0], o[bad][0], r.o[bad][0], lim[bad][0])
+
+
+class Paged:
+    """A cache of random rows with NaN wherever no sequence has a row."""
+
+    def __init__(self, seed, lens, page, nan=True):
+        self.rng = _rng(seed)
+        self.lens, self.page = list(lens), page
+        self.table, self.P = ol.ragged_pages(self.rng, self.lens, page)
+        rows = self.rng.normal(size=(self.P, page, ol.ROW))
+        self.dev, self.ref = _bf(rows)
+        if nan:
+            held = np.zeros((self.P, page), dtype=bool)
+            for b, n in enumerate(self.lens):
+                p = np.arange(n)
+                held[self.table[b, p // page], p % page] = True
+            import torch
+            self.dev[torch.from_numpy(~held).cuda()] = float("nan")
+        self.table_dev = _i32(self.table)
+        self.lens_dev = _i32(self.lens)
+
+    def q(self, tokens, H, scale=1.0):
+        return _bf(self.rng.normal(size=(tokens, H, ol.ROW)) * scale)
+
+
+# ------------------------------------------------------------------ append, gather
+LENS = [0, 1, 15, 16, 17, 64, 200, 129]
+
+
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("norm", [False, True])
+def test_append_ragged(page, norm):
+    import torch
+    kda = _kda()
+    c = Paged(11, LENS, page, nan=False)
+    news = [0, 1, 15, 3, 0, 64, 130, 2]
+    cu = np.cumsum([0] + news)
+    x, xr = _bf(c.rng.normal(size=(cu[-1] + 2, ol.ROW)) * 3)      # two tokens behind the last sequence
+    w = torch.from_numpy(c.rng.normal(size=512)).float().cuda() if norm else None
+    want = ol.append(xr[:cu[-1]], c.ref, c.table, c.lens, cu, None if w is None else _np(w), 1e-6)
+    got = kda.latent_append(x, c.dev, c.table_dev, c.lens_dev, _i32(cu), norm_w=w, eps=1e-6)
+    assert got is c.dev
+    _clear()
+    got = _np(got)
+    if not norm:
+        assert np.array_equal(got, want)
+        return
+    assert np.array_equal(got[..., 512:], want[..., 512:])
+    # one rounding to bf16 of a value computed in a few fp32 steps (2^-20)
+    assert (np.abs(got - want) <= (HALF + 2.0 ** -20) * np.abs(want)).all()
+
+
+def test_append_one_token_a_sequence_equals_the_packed_call():
+    import torch
+    kda = _kda()
+    lens = [1, 16, 17, 100]
+    c = Paged(12, lens, 16, nan=False)
+    x, _ = _bf(c.rng.normal(size=(4, ol.ROW)))
+    w = torch.ones(512, device="cuda")
+    a = kda.latent_append(x, c.dev.clone(), c.table_dev, c.lens_dev, norm_w=w)
+    b = kda.latent_append(x, c.dev.clone(), c.table_dev, c.lens_dev, _i32([0, 1, 2, 3, 4]), norm_w=w)
+    _clear()
+    assert torch.equal(a, b) and not torch.equal(a, c.dev)
+
+
+def test_append_flags_bad_places_and_writes_none_of_them():
+    import torch
+    kda = _kda()
+    c = Paged(13, [20, 20, 20, 20], 16, nan=False)
+    x, _ = _bf(c.rng.normal(size=(4, ol.ROW)))
+    table = c.table.copy()
+    table[0, 1], table[1, 1] = -1, c.P                              # positions 19 of sequences 0 and 1
+    before = c.dev.clone()
+    kda.latent_append(x, c.dev, _i32(table), c.lens_dev)
+    _clear(2)
+    keep = torch.ones((c.P, 16), dtype=torch.bool)
+    for b in (2, 3):
+        row = int(table[b, 1])
+        assert torch.equal(c.dev[row, 3].cpu(), x[b].cpu())
+        keep[row, 3] = False
+    assert torch.equal(c.dev[keep.cuda()], before[keep.cuda()])
+    c.dev.copy_(before)                                             # lengths outside the table
+    kda.latent_append(x, c.dev, c.table_dev, _i32([0, -5, 16 * c.table.shape[1] + 1, 2 ** 31 - 1]))
+    _clear(1)
+    assert torch.equal(c.dev, before)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_gather_ragged(page):
+    import torch
+    kda = _kda()
+    c = Paged(14, LENS, page)
+    cu = np.cumsum([0] + [n // 2 for n in LENS[:4]] + LENS[4:])
+    out = torch.full((cu[-1] + 5, ol.ROW), 7.0, dtype=torch.bfloat16, device="cuda")
+    kda.latent_gather(c.dev, c.table_dev, _i32(cu), out=out)
+    _clear()
+    want = np.concatenate([ol.sequence_rows(c.ref, c.table[b], 0, cu[b + 1] - cu[b]) for b in range(len(LENS))])
+    assert np.array_equal(_np(out[:cu[-1]]), want)
+    assert (out[cu[-1]:] == 7.0).all()                             # rows behind the last sequence
+    again = kda.latent_gather(c.dev, c.table_dev, _i32(cu), total=int(cu[-1]))
+    assert torch.equal(again, out[:cu[-1]])
+
+
+def test_gather_reads_zeros_for_a_bad_page():
+    import torch
+    kda = _kda()
+    c = Paged(15, [40], 16)
+    table = c.table.copy()
+    table[0, 1] = c.P + 3
+    out = kda.latent_gather(c.dev, _i32(table), _i32([0, 40]), total=40)
+    _clear(2)
+    want = ol.sequence_rows(c.ref, c.table[0], 0, 40).copy()
+    want[16:32] = 0
+    assert np.array_equal(_np(out), want)
+
+
+# ------------------------------------------------------------------ decode
+def _decode(c, q, cu, **kw):
+    return _kda().latent_decode(q, c.dev, c.table_dev, c.lens_dev, None if cu is None else _i32(cu), **kw)
+
+
+@pytest.mark.parametrize("H", [1, 3, 16, 40, 96, 128])
+@pytest.mark.parametrize("page", [16, 64])
+def test_decode_one_token(H, page):
+    lens = [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 300, 1000]
+    c = Paged(21, lens, page)
+    q, qr = c.q(len(lens), H)
+    o, lse = _decode(c, q, None)
+    _clear()
+    r = ol.decode(qr, c.ref, c.table, lens, np.arange(len(lens) + 1), SCALE)
+    check(o, lse, r, "decode H=%d" % H)
+
+
+@pytest.mark.parametrize("H", [1, 5, 16, 96])
+def test_decode_ragged_new_tokens(H):
+    lens = [5, 130, 0, 64, 257, 3, 128, 140]
+    news = [5, 3, 0, 1, 33, 0, 64, 7]
+    c = Paged(22, lens, 32)
+    cu = np.cumsum([0] + news)
+    q, qr = c.q(cu[-1] + 1, H)                                      # one row behind the last sequence
+    import torch
+    o = torch.full((cu[-1] + 1, H, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((cu[-1] + 1, H), 7.0, device="cuda")
+    _decode(c, q, cu, o=o, lse=lse)
+    _clear()
+    assert (o[-1] == 7.0).all() and (lse[-1] == 7.0).all()
+    r = ol.decode(qr[:-1], c.ref, c.table, lens, cu, SCALE)
+    check(o[:-1], lse[:-1], r, "ragged decode H=%d" % H)
+
+
+def test_decode_more_new_tokens_than_positions():
+    """A length shorter than the new tokens: the first ones see nothing."""
+    c = Paged(23, [2, 70], 16)
+    q, qr = c.q(5 + 3, 4)
+    o, lse = _decode(c, q, [0, 5, 8])
+    _clear()
+    check(o, lse, ol.decode(qr, c.ref, c.table, c.lens, [0, 5, 8], SCALE), "short sequence")
+    assert (o[:3] == 0).all() and np.isneginf(_np(lse)[:3]).all()
+
+
+@pytest.mark.parametrize("lens,H,page", [([5000, 1, 2049], 16, 128), ([9001], 64, 16), ([300] * 200, 8, 64)])
+def test_decode_split_over_positions(lens, H, page):
+    """Few long sequences (each split over the SMs) and many short ones."""
+    c = Paged(24, lens, page)
+    q, qr = c.q(len(lens), H)
+    o, lse = _decode(c, q, None)
+    _clear()
+    check(o, lse, ol.decode(qr, c.ref, c.table, lens, np.arange(len(lens) + 1), SCALE), "split")
+
+
+@pytest.mark.parametrize("kind", ["rising", "falling", "spike", "tiny", "flat"])
+def test_decode_score_ranges(kind):
+    """Scores that rise or fall by hundreds over the positions, one position
+    that takes all, and none that stands out: the running maximum moves often,
+    once, or never."""
+    lens, H = [700, 129], 16
+    c = Paged(25, lens, 64, nan=False)
+    ref = c.ref.copy()
+    u = np.zeros(ol.ROW)
+    u[7] = 1.0
+    for b, n in enumerate(lens):
+        p = np.arange(n)
+        ramp = {"rising": p * 2.0, "falling": -p * 2.0, "spike": (p == n // 2) * 3000.0, "tiny": p * 0.0,
+                "flat": p * 0.0 + 500.0}[kind]
+        ref[c.table[b, p // 64], p % 64, 7] = ramp
+    c.dev, c.ref = _bf(ref)
+    q, qr = c.q(2, H, scale=1e-3 if kind == "tiny" else 1.0)
+    qr = qr.copy()
+    qr[:, :, 7] = 13.0
+    q, qr = _bf(qr)
+    o, lse = _decode(c, q, None)
+    _clear()
+    check(o, lse, ol.decode(qr, c.ref, c.table, lens, np.arange(3), SCALE), kind)
+
+
+def test_decode_is_reproducible_and_takes_a_workspace():
+    import torch
+    kda = _kda()
+    c = Paged(26, [3000, 40, 777], 64)
+    q, _ = c.q(3, 96)
+    o, lse = _decode(c, q, None)
+    n = kda.latent_decode_workspace_bytes(3, 3, 96)
+    ws = torch.full((max(n, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        o2, lse2 = _decode(c, q, None, workspace=ws)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    _clear()
+
+
+def test_decode_bad_pages_read_as_zeros():
+    kda = _kda()
+    c = Paged(27, [300, 100], 64)
+    table = c.table.copy()
+    table[0, 1], table[1, 0] = -7, 2 ** 31 - 1
+    q, qr = c.q(2, 8)
+    o, lse = kda.latent_decode(q, c.dev, _i32(table), c.lens_dev)
+    _clear(2)
+    ref = np.concatenate([c.ref, np.zeros((1, 64, ol.ROW))])        # a page of zeros in their place
+    table[0, 1] = table[1, 0] = c.P
+    check(o, lse, ol.decode(qr, ref, table, c.lens, np.arange(3), SCALE), "bad pages")
+
+
+def test_decode_lengths_outside_the_table_are_flagged():
+    kda = _kda()
+    c = Paged(28, [64, 64], 64)
+    q, qr = c.q(2, 4)
+    o, lse = kda.latent_decode(q, c.dev, c.table_dev[:, :1].contiguous(), _i32([65, -1]))
+    _clear(1)
+    r = ol.decode(qr, c.ref, c.table, [64, 0], np.arange(3), SCALE)
+    check(o, lse, r, "clamped lengths")
+
+
+def test_decode_shared_pages():
+    """Two sequences whose first pages are the same ones."""
+    kda = _kda()
+    c = Paged(29, [200, 90], 16, nan=False)
+    table = c.table.copy()
+    table[1, :4] = table[0, :4]
+    q, qr = c.q(2, 16)
+    o, lse = kda.latent_decode(q, c.dev, _i32(table), c.lens_dev)
+    _clear()
+    check(o, lse, ol.decode(qr, c.ref, table, c.lens, np.arange(3), SCALE), "shared pages")
+
+
+# ------------------------------------------------------------------ prefill
+def _prefill_inputs(seed, nq, nk, H, extra=0):
+    rng = _rng(seed)
+    cu, cuk = np.cumsum([0] + list(nq)), np.cumsum([0] + list(nk))
+    q, qr = _bf(rng.normal(size=(cu[-1] + extra, H, 192)))
+    kv, kvr = _bf(rng.normal(size=(cuk[-1] + extra, H, 256)))
+    pe, per = _bf(rng.normal(size=(cuk[-1] + extra, 64)))
+    return cu, cuk, (q, kv, pe), (qr, kvr, per)
+
+
+@pytest.mark.parametrize("H", [1, 3])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_ragged(H, causal):
+    kda = _kda()
+    lens = [0, 1, 2, 17, 63, 64, 65, 127, 128, 129, 0, 200, 257, 300]
+    cu, _, (q, kv, pe), (qr, kvr, per) = _prefill_inputs(31, lens, lens, H)
+    o, lse = kda.latent_prefill(q, kv, pe, _i32(cu), causal=causal)
+    _clear()
+    check(o, lse, ol.prefill(qr, kvr, per, cu, cu, SCALE, causal), "prefill H=%d" % H)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_behind_a_context(causal):
+    """New tokens behind contexts, more queries than keys, no keys at all; NaN
+    behind the last sequence in every input, and output rows there untouched."""
+    import torch
+    kda = _kda()
+    nq, nk, H = [3, 130, 1, 64, 5, 4, 300], [200, 131, 700, 64, 2, 0, 300], 2
+    cu, cuk, (q, kv, pe), (qr, kvr, per) = _prefill_inputs(32, nq, nk, H, extra=3)
+    for t, n in ((q, cu[-1]), (kv, cuk[-1]), (pe, cuk[-1])):
+        t[int(n):] = float("nan")
+    o = torch.full((q.shape[0], H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((q.shape[0], H), 7.0, device="cuda")
+    kda.latent_prefill(q, kv, pe, _i32(cu), _i32(cuk), causal=causal, o=o, lse=lse)
+    _clear()
+    n = int(cu[-1])
+    assert (o[n:] == 7.0).all() and (lse[n:] == 7.0).all()
+    check(o[:n], lse[:n], ol.prefill(qr[:n], kvr, per, cu, cuk, SCALE, causal), "context")
+
+
+def test_prefill_sequences_do_not_reach_into_each_other():
+    """A neighbour of infinities and NaN changes nothing."""
+    kda = _kda()
+    lens = [70, 90, 140]
+    cu, _, (q, kv, pe), (qr, kvr, per) = _prefill_inputs(33, lens, lens, 2)
+    for t in (q, kv, pe):
+        t[70:160] = float("nan")
+        t[100:110] = float("inf")
+    o, lse = kda.latent_prefill(q, kv, pe, _i32(cu))
+    _clear()
+    r = ol.prefill(qr, kvr, per, cu, cu, SCALE)
+    for a, b in ((0, 70), (160, 300)):
+        part = ol.Result((b - a, 2), 128)
+        part.o, part.lse, part.absum, part.sqsum, part.mag = (getattr(r, n)[a:b] for n in
+                                                              ("o", "lse", "absum", "sqsum", "mag"))
+        check(o[a:b], lse[a:b], part, "rows %d.." % a)
+
+
+@pytest.mark.parametrize("kind", ["rising", "falling", "spike"])
+def test_prefill_score_ranges(kind):
+    kda = _kda()
+    n, H = 400, 2
+    cu, _, (q, kv, pe), (qr, kvr, per) = _prefill_inputs(34, [n], [n], H)
+    p = np.arange(n)
+    qr, per = qr.copy(), per.copy()
+    qr[:, :, 128] = 13.0
+    per[:, 0] = {"rising": p * 2.0, "falling": -p * 2.0, "spike": (p == 37) * 3000.0}[kind]
+    q, qr = _bf(qr)
+    pe, per = _bf(per)
+    o, lse = kda.latent_prefill(q, kv, pe, _i32(cu))
+    _clear()
+    check(o, lse, ol.prefill(qr, kvr, per, cu, cu, SCALE), kind)
+
+
+def test_prefill_takes_strided_shared_keys():
+    import torch
+    kda = _kda()
+    cu, _, (q, kv, pe), _ = _prefill_inputs(35, [150, 20], [150, 20], 2)
+    rows = torch.full((170, ol.ROW), float("nan"), dtype=torch.bfloat16, device="cuda")
+    rows[:, 512:] = pe
+    a, la = kda.latent_prefill(q, kv, pe, _i32(cu))
+    b, lb = kda.latent_prefill(q, kv, rows[:, 512:], _i32(cu))
+    _clear()
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    with pytest.raises(kda.KDAError):
+        kda.latent_prefill(q, kv, torch.zeros((170, 68), dtype=torch.bfloat16, device="cuda")[:, :64], _i32(cu))
+
+
+def test_prefill_flags_bad_offsets():
+    kda = _kda()
+    cu, _, (q, kv, pe), _ = _prefill_inputs(36, [40], [40], 1)
+    for bad in ([0, 41], [-1, 40], [30, 20]):
+        kda.latent_prefill(q, kv, pe, _i32([0, 40]), _i32(bad))
+        _clear(1)
+
+
+# ------------------------------------------------------------------ together
+def _layer(seed, H):
+    rng = _rng(seed)
+    (wk, wkr), (wv, wvr) = (_bf(rng.normal(size=(H, 512, 128)) / 16) for _ in range(2))
+    return rng, wk, wkr, wv, wvr
+
+
+def test_layer_chunked_prefill_then_decode_both_forms():
+    """A prompt in two chunks and three decode steps through the cache, each
+    chunk attended to in the expanded form (rows gathered, expanded, prefill)
+    and in the absorbed one (decode over the pages): the two agree to the
+    roundings between them, and the cache holds what was written."""
+    import torch
+    kda = _kda()
+    H, page, N = 4, 16, 3
+    rng, wk, wkr, wv, wvr = _layer(41, H)
+    total = [90, 33, 200]
+    table, P = ol.ragged_pages(rng, [n + 3 for n in total], page)
+    table_dev = _i32(table)
+    cache = torch.full((P, page, ol.ROW), float("nan"), dtype=torch.bfloat16, device="cuda")
+    norm_w = torch.from_numpy(1 + 0.1 * rng.normal(size=512)).float().cuda()
+    have = [0, 0, 0]
+    for news in ([60, 33, 128], [30, 0, 72], [1, 1, 1], [1, 1, 1], [1, 1, 1]):
+        have = [a + b for a, b in zip(have, news)]
+        cu, cuk = _i32(np.cumsum([0] + news)), _i32(np.cumsum([0] + have))
+        lens = _i32(have)
+        x, _ = _bf(rng.normal(size=(sum(news), ol.ROW)))
+        q, _ = _bf(rng.normal(size=(sum(news), H, 192)))
+        kda.latent_append(x, cache, table_dev, lens, cu, norm_w=norm_w)
+        rows = kda.latent_gather(cache, table_dev, cuk, total=sum(have))
+        kv = torch.cat([torch.einsum("nc,hcd->nhd", rows[:, :512].float(), w.float()) for w in (wk, wv)], 2)
+        oe, le = kda.latent_prefill(q, kv.to(torch.bfloat16).contiguous(), rows[:, 512:], cu, cuk)
+        qa = torch.cat([torch.einsum("thd,hcd->thc", q[..., :128].float(), wk.float()), q[..., 128:].float()], 2)
+        oa, la = kda.latent_decode(qa.to(torch.bfloat16).contiguous(), cache, table_dev, lens, cu)
+        oa = torch.einsum("thc,hcd->thd", oa.float(), wv.float())
+        _clear()
+        # the roundings to bf16 between the forms (q absorbed; keys and values expanded): errors of a
+        # score of at most 2^-8 scale (|qa| . |row| + |q| . |k|), here below 2^-8 * 90, as random signs
+        # (7 sqrt(n) instead of n of them): both sides' scores agree to 0.15
+        assert (le - la).abs().max() < 0.15
+        rel = ((oe.float() - oa).norm() / oa.norm()).item()
+        assert rel < 0.03, rel
+    assert torch.isnan(cache).any()                                 # what no token owns was never touched
+
+
+def test_layer_captured_and_replayed():
+    """A decode step (append, then attention) captured into a graph and
+    replayed with new inputs in place."""
+    import torch
+    kda = _kda()
+    lens = [130, 64, 1, 500]
+    c = Paged(42, lens, 64)
+    x, _ = _bf(c.rng.normal(size=(4, ol.ROW)))
+    q, _ = c.q(4, 16)
+    n = kda.latent_decode_workspace_bytes(4, 4, 16)
+    ws = torch.empty((max(n, 1),), dtype=torch.uint8, device="cuda")
+    o = torch.empty((4, 16, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((4, 16), device="cuda")
+
+    def step():
+        kda.latent_append(x, c.dev, c.table_dev, c.lens_dev)
+        kda.latent_decode(q, c.dev, c.table_dev, c.lens_dev, o=o, lse=lse, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for k in range(3):
+        nx, nq = _bf(c.rng.normal(size=(4, ol.ROW)))[0], c.q(4, 16)[0]
+        x.copy_(nx)
+        q.copy_(nq)
+        c.lens_dev.copy_(_i32([m - k % 2 if m > 1 else m for m in lens]))
+        g.replay()
+        _clear()
+        got = o.clone(), lse.clone()
+        step()
+        _clear()
+        assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+
+
+def test_calls_on_another_stream():
+    import torch
+    kda = _kda()
+    c = Paged(43, [2000, 300], 64)
+    q, _ = c.q(2, 16)
+    want = _decode(c, q, None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [_decode(c, q, None, stream=s) for _ in range(4)]
+    s.synchronize()
+    _clear()
+    for o, lse in got:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_binding_refuses_wrong_tensors():
+    import torch
+    kda = _kda()
+    c = Paged(44, [20], 16)
+    q, _ = c.q(1, 4)
+    two, _ = c.q(2, 4)
+    with pytest.raises(TypeError):
+        kda.latent_decode(q.float(), c.dev, c.table_dev, c.lens_dev)
+    with pytest.raises(TypeError):
+        kda.latent_decode(q, c.dev, c.table_dev.long(), c.lens_dev)
+    with pytest.raises(ValueError):
+        kda.latent_decode(q, c.dev[:, :, :512], c.table_dev, c.lens_dev)
+    with pytest.raises(ValueError):
+        kda.latent_decode(q, c.dev, c.table_dev, _i32([20, 20]))
+    with pytest.raises(ValueError):
+        kda.latent_decode(two.transpose(0, 1), c.dev, c.table_dev, c.lens_dev)
+    with pytest.raises(ValueError):
+        kda.latent_gather(c.dev, c.table_dev, _i32([0, 20]))
+    with pytest.raises(kda.KDAError):
+        kda.latent_decode(q, c.dev.view(-1, 8, 576), c.table_dev, c.lens_dev)
+    with pytest.raises(kda.KDAError):
+        kda.latent_decode(q, c.dev, c.table_dev, c.lens_dev, scale=-1.0)
