@@ -374,15 +374,16 @@ int kda_workspace_release(void) { return cuda_status(kda::release_workspace_pool
 
 int kda_device_error(unsigned int *code, int reset) {
     if (!code) return KDA_ERR_NULL;
-    unsigned int a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
+    unsigned int a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0;
     const cudaError_t e1 = kda::read_device_error(&a, reset != 0);
     const cudaError_t e2 = kda::read_decode_error(&b, reset != 0);
     const cudaError_t e3 = kda::read_layer_error(&c, reset != 0);
     const cudaError_t e4 = kda::read_simt_error(&d, reset != 0);
     const cudaError_t e5 = kda::read_latent_error(&f, reset != 0);
     const cudaError_t e6 = kda::read_latent_prefill_error(&g, reset != 0);
-    *code = a | b | c | d | f | g;
-    for (const cudaError_t e : {e1, e2, e3, e4, e5, e6})
+    const cudaError_t e7 = kda::read_latent_decode_error(&h, reset != 0);
+    *code = a | b | c | d | f | g | h;
+    for (const cudaError_t e : {e1, e2, e3, e4, e5, e6, e7})
         if (e != cudaSuccess) return cuda_status(e);
     return KDA_OK;
 }

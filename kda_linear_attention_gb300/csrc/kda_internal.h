@@ -143,10 +143,10 @@ cudaError_t launch_decode_layer(const void *xq, const void *xk, const void *xv, 
                                 float q_scale, float l2_eps, float norm_eps, cudaStream_t stream);
 cudaError_t read_layer_error(unsigned int *code, bool reset);
 
-// Latent attention over a paged cache of [P, page, 576] bf16 rows
-// (kda_latent.cu): write new tokens' rows, read rows back in order, and
-// attend with queries already absorbed into the latent.  cu == nullptr: one
-// new token a sequence.
+// Latent attention over a paged cache of [P, page, 576] bf16 rows: write new
+// tokens' rows and read rows back in order (kda_latent.cu), attend with
+// queries already absorbed into the latent (kda_latent_decode.cu; `ws` of
+// latent_decode_workspace_bytes).  cu == nullptr: one new token a sequence.
 cudaError_t launch_latent_append(const void *x, void *cache, const int32_t *table,
                                  const int32_t *seq_lens, const int32_t *cu, const float *norm_w,
                                  float eps, int N, int64_t T, int64_t P, int page, int max_pages,
@@ -160,6 +160,7 @@ cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t
                                  float *lse, int N, int64_t T, int H, int64_t P, int page,
                                  int max_pages, void *ws, cudaStream_t stream);
 cudaError_t read_latent_error(unsigned int *code, bool reset);
+cudaError_t read_latent_decode_error(unsigned int *code, bool reset);
 // Attention with expanded keys and values (kda_latent_prefill.cu).
 cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t pe_stride,
                                   const int32_t *cu_q, const int32_t *cu_k, float scale, bool causal,

@@ -1,16 +1,6 @@
-// The paged latent cache: writing new tokens' rows (append), reading a
-// sequence's rows back in order (gather), and attention of one or a few new
-// tokens over the pages in latent space (decode).
-//
-// A cached row is [c | r], 512 latent and 64 shared key channels in bf16.
-// With the value and key expansions absorbed into q and into the caller's
-// output product, a (token, head) row x [576] attends as
-//   s_p = scale <x, row_p>,   o = sum_p softmax(s)_p c_p,   lse = ln sum_p e^{s_p}
-// over the positions p it may see: those up to its own.
-#include <math_constants.h>
-
-#include <algorithm>
-
+// The paged latent cache: writing new tokens' rows (append) and reading a
+// sequence's rows back in order (gather).  A cached row is [c | r], 512
+// latent and 64 shared key channels in bf16.
 #include "kda_internal.h"
 #include "latent_common.cuh"
 
@@ -130,77 +120,6 @@ latent_gather_kernel(const uint4 *__restrict__ cache, PagedRows pages, const int
         if (from[i] > -2) dst[32 * i + lane] = v[i];
 }
 
-// ---------------------------------------------------------------- decode
-// A block a (token, head) row: positions in tiles of 64, a warp a position
-// at a time for the scores, a running maximum and sum, two latent columns a
-// thread for the output.
-constexpr int kDecThreads = 256;
-constexpr int kDecTile = 64;
-
-__global__ void __launch_bounds__(kDecThreads)
-latent_decode_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ cache,
-                     PagedRows pages, const int32_t *__restrict__ seq_lens,
-                     const int32_t *__restrict__ cu, float scale, __nv_bfloat16 *__restrict__ o,
-                     float *__restrict__ lse, int N, int T, int H) {
-    const int t = (int)(blockIdx.x / (unsigned)H);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int s = seq_of_token(cu, N, t);
-    if (s < 0) return;
-    const int start = cu ? cu[s] : s, count = cu ? cu[s + 1] - start : 1;
-    int L = seq_lens[s];
-    if (L < 0 || L > pages.max_len()) {
-        if (tid == 0) atomicOr(&g_kda_latent_error, kErrWait);
-        L = max(0, min(L, pages.max_len()));
-    }
-    const int seen = max(0, L - count + (t - start) + 1);
-    __shared__ float sq[kLatentRow], sc[kDecTile];
-    __shared__ long long srow[kDecTile];
-    const size_t row = blockIdx.x;
-    for (int i = tid; i < kLatentRow; i += kDecThreads) sq[i] = __bfloat162float(q[row * kLatentRow + i]);
-    float m = -CUDART_INF_F, l = 0.f, o0 = 0.f, o1 = 0.f;
-    for (int p0 = 0; p0 < seen; p0 += kDecTile) {
-        const int n = min(kDecTile, seen - p0);
-        __syncthreads();
-        if (tid < n) {
-            srow[tid] = pages.row(s, p0 + tid);
-            if (srow[tid] < 0) atomicOr(&g_kda_latent_error, kErrSlot);
-        }
-        __syncthreads();
-        for (int j = warp; j < n; j += kDecThreads / 32) {
-            float d = 0.f;
-            if (srow[j] >= 0)
-                for (int i = lane; i < kLatentRow; i += 32)
-                    d = fmaf(sq[i], __bfloat162float(cache[(size_t)srow[j] * kLatentRow + i]), d);
-            d = warp_sum(d);
-            if (lane == 0) sc[j] = d * scale;
-        }
-        __syncthreads();
-        float mt = m;
-        for (int j = 0; j < n; ++j) mt = fmaxf(mt, sc[j]);
-        const float a = m == -CUDART_INF_F ? 0.f : expf(m - mt);
-        l *= a; o0 *= a; o1 *= a;
-        m = mt;
-        for (int j = 0; j < n; ++j) {
-            const float p = expf(sc[j] - m);
-            l += p;
-            if (srow[j] >= 0) {
-                const float2 c = bf2_to_f2(reinterpret_cast<const uint32_t *>(cache + (size_t)srow[j] * kLatentRow)[tid]);
-                o0 = fmaf(p, c.x, o0);
-                o1 = fmaf(p, c.y, o1);
-            }
-        }
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    reinterpret_cast<uint32_t *>(o + row * kLatent)[tid] = f2_to_bf2(make_float2(o0 * inv, o1 * inv));
-    if (lse && tid == 0) lse[row] = l > 0.f ? m + logf(l) : -CUDART_INF_F;
-}
-
-PagedRows paged(const int32_t *table, int64_t P, int page, int max_pages) {
-    int lg = 0;
-    while ((1 << lg) < page) ++lg;
-    return PagedRows{table, P, lg, max_pages};
-}
-
 }  // namespace
 
 cudaError_t launch_latent_append(const void *x, void *cache, const int32_t *table,
@@ -209,7 +128,7 @@ cudaError_t launch_latent_append(const void *x, void *cache, const int32_t *tabl
                                  cudaStream_t stream) {
     const unsigned blocks = (unsigned)((T * 32 + kAppendThreads - 1) / kAppendThreads);
     latent_append_kernel<<<blocks, kAppendThreads, 0, stream>>>(
-        static_cast<const uint4 *>(x), static_cast<uint4 *>(cache), paged(table, P, page, max_pages),
+        static_cast<const uint4 *>(x), static_cast<uint4 *>(cache), paged_rows(table, P, page, max_pages),
         seq_lens, cu, norm_w, eps, N, (int)T);
     return cudaGetLastError();
 }
@@ -219,21 +138,8 @@ cudaError_t launch_latent_gather(const void *cache, const int32_t *table, const 
                                  cudaStream_t stream) {
     const unsigned blocks = (unsigned)(((T + 3) / 4 * 32 + kGatherThreads - 1) / kGatherThreads);
     latent_gather_kernel<<<blocks, kGatherThreads, 0, stream>>>(
-        static_cast<const uint4 *>(cache), paged(table, P, page, max_pages), cu,
+        static_cast<const uint4 *>(cache), paged_rows(table, P, page, max_pages), cu,
         static_cast<uint4 *>(out), N, (int)T);
-    return cudaGetLastError();
-}
-
-size_t latent_decode_workspace_bytes(int, int64_t, int) { return 0; }
-
-cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t *table,
-                                 const int32_t *seq_lens, const int32_t *cu, float scale, void *o,
-                                 float *lse, int N, int64_t T, int H, int64_t P, int page,
-                                 int max_pages, void *, cudaStream_t stream) {
-    latent_decode_kernel<<<(unsigned)(T * H), kDecThreads, 0, stream>>>(
-        static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(cache),
-        paged(table, P, page, max_pages), seq_lens, cu, scale, static_cast<__nv_bfloat16 *>(o), lse, N,
-        (int)T, H);
     return cudaGetLastError();
 }
 

@@ -1,0 +1,732 @@
+// Absorbed latent attention of one or a few new tokens a sequence over the
+// paged cache, on the tensor cores.
+//
+// A sequence's n new tokens and H heads are n H rows x [576] that attend to
+// the same cached rows [c | r] (512 + 64), so a tile of 128 positions is read
+// once for up to 64 of them.  Both products run with the positions or the
+// latent channels on the 128 TMEM lanes and the rows as columns, so a few
+// rows cost a few columns:
+//   S^T [128 positions x rows]   = K [128 x 576] X^T           (36 K-steps)
+//   O^T [512 x rows]            += c^T [512 x 128] P^T         (4 blocks of 128 channels, 8 K-steps)
+// K's tile is both products' A operand, K-major for the first, MN-major for
+// the second.  P = exp2(S scale log2 e - m) in bf16 (fp32 sums of the
+// unrounded values): its rounding, 2^-9 of each probability at most, is of
+// the kind that the bf16 output has anyway.  m is a row's running maximum,
+// moved only when a score passes it by more than 8 (a factor 256, which fp32
+// sums and bf16 probabilities hold without loss); then O^T and the sums are
+// rescaled in TMEM and registers.
+//
+// Work is cut in units of (sequence, row tile, 128 positions); CTA c of G
+// (one an SM) takes units c W / G .. (c + 1) W / G, so every SM has the same
+// number of units whatever the lengths are.  A CTA's first and last row tile
+// may be pieces of longer ones: pieces are written normalised in fp32 with
+// their log2-sum-exp into the workspace, and a second kernel joins them in the
+// order of the positions (no atomics: the same bits every time).
+//
+// Roles: a copy warp (TMA boxes of one page each, and L2 prefetch of the next
+// tile's pages, whose rows are contiguous), an MMA thread, two groups of four
+// softmax warps that each take half of the rows (columns).  Shared memory: X
+// (NR x 1152 B), a ring of 32 KB slots (128 positions x 128 channels) and the
+// 16 KB slots of the shared key part, which hold P once the scores are done.
+#include <algorithm>
+
+#include "latent_tc.cuh"
+
+namespace kda {
+
+using namespace tc;
+
+// Error word of this file's kernels (bit 0: a bounded wait gave up, or
+// cu_seqlens or a length broke its precondition; bit 1: a page index outside
+// the cache).
+__device__ unsigned int g_kda_latent_decode_error = 0;
+
+namespace {
+
+constexpr int kTile = 128;                // positions a unit
+constexpr int kMaxCtas = 160;             // grid bound (one CTA an SM; 152 SMs)
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = 32 * (kSoftWarps + 2);
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr uint32_t kPair = 32768;         // 128 positions x 128 channels
+constexpr uint32_t kRope = 16384;         // 128 positions x 64 channels; later P [128][64]
+constexpr float kMoveAt = 8.f;            // log2 of the factor a score may pass the maximum by
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t TM_S = 0, TM_O = 64;   // S^T: 64 columns; O^T: 4 blocks of 64
+
+// What a CTA leaves for the joining kernel: the row tile that starts in its
+// units and goes on behind them.
+struct Split {
+    int32_t row;                          // first row (flat over [T * H])
+    int32_t rows;                         // rows of the tile; 0: nothing
+    int32_t last;                         // the CTA that holds the last piece
+    int32_t pad;
+};
+
+template <int NR>
+struct Cfg {
+    static constexpr int NP = NR == 64 || NR == 48 ? 4 : 5;   // 32 KB slots
+    static constexpr int NQ = NR == 16 || NR == 48 ? 2 : 1;   // 16 KB slots
+    static constexpr uint32_t X = 0;
+    static constexpr uint32_t PAIR = NR * 1152u;
+    static constexpr uint32_t ROPE = PAIR + NP * kPair;
+    static constexpr uint32_t MISC = ROPE + NQ * kRope;
+    static constexpr uint32_t BYTES = MISC + 4096;
+    static_assert(BYTES + 1024 <= 232448, "shared memory of an SM");
+};
+
+struct Misc {
+    uint64_t full_p[5], empty_p[5], full_r[2], empty_r[2];
+    uint64_t x_full, x_empty, s_full, p_full, o_full, done;
+    uint32_t tmem;
+    int fail;
+    int b0, j0, t0;                       // first unit
+    int32_t units;                        // units of this CTA
+    int used;                             // CTAs with units
+    long long scan[kThreads / 32 + 1];
+    long long start, total;
+    // per column (row of the tile), by softmax group
+    float red[2][4][32];                  // cross-warp reductions
+    float m[2][32];                       // running maximum, log2 units
+    float f[2][32];                       // rescale factor, then 1 / sum
+    int seen[2][32];                      // positions it may see
+};
+static_assert(sizeof(Misc) <= 4096, "control block");
+
+struct Args {
+    PagedRows pages;
+    const int32_t *seq_lens, *cu;
+    int N, T, H;
+    float scale_log2;                     // scale * log2 e
+    __nv_bfloat16 *o;
+    float *lse;
+    Split *split;
+    float *ws_lse;                        // [2 G][NR]
+    float *ws_o;                          // [2 G][NR][512]
+};
+
+// A sequence as the kernel sees it (clamped to what its buffers hold).
+struct Seq {
+    int row0, rows;                       // flat rows over [T * H], of this sequence
+    int first;                            // positions its first new token sees (may be <= 0)
+    int len, tiles, row_tiles;
+};
+
+template <int NR>
+__device__ __forceinline__ Seq get_seq(const Args &a, int b, bool flag) {
+    Seq s;
+    int t0 = b, n = 1;
+    bool bad = false;
+    if (a.cu) {
+        t0 = a.cu[b];
+        const int t1 = a.cu[b + 1];
+        bad = t0 < 0 || t1 < t0 || t1 > a.T;
+        n = bad ? 0 : t1 - t0;
+        if (bad) t0 = 0;
+    }
+    int L = a.seq_lens[b];
+    const int most = a.pages.max_len();
+    if (L < 0 || L > most) {
+        bad = true;
+        L = max(0, min(L, most));
+    }
+    if (bad && flag) atomicOr(&g_kda_latent_decode_error, kErrWait);
+    s.row0 = t0 * a.H;
+    s.rows = n * a.H;
+    s.first = L - n + 1;
+    s.len = L;
+    s.tiles = max(1, (L + kTile - 1) / kTile);
+    s.row_tiles = (s.rows + NR - 1) / NR;
+    return s;
+}
+
+// One row tile over a range of positions.
+struct Item {
+    int b, row, rows;                     // sequence, first flat row, rows
+    int tile, n;                          // first tile of positions, tiles with anything to see
+    int len;                              // the sequence's length
+    int first_tok, row_in_seq;            // positions its first new token sees; row - row0
+    bool head, tail;                      // holds the row tile's first / last unit
+    long long unit;                       // the first unit here
+    int tiles;                            // units of the whole row tile
+};
+
+// Walks a CTA's units row tile by row tile; every role takes the same walk.
+template <int NR>
+struct Walk {
+    int b, j, t, left;
+    long long u;
+    Seq s;
+    __device__ __forceinline__ Walk(const Args &a, const Misc *m)
+        : b(m->b0), j(m->j0), t(m->t0), left(m->units), u(m->start) {
+        if (left > 0) s = get_seq<NR>(a, b, false);
+    }
+    __device__ __forceinline__ bool next(const Args &a, Item &it) {
+        if (left <= 0) return false;
+        while (j >= s.row_tiles) {        // units are left, so a sequence with rows follows
+            if (++b >= a.N) { left = 0; return false; }
+            s = get_seq<NR>(a, b, false);
+            j = t = 0;
+        }
+        const int units = min(s.tiles - t, left);
+        it.b = b;
+        it.row_in_seq = j * NR;
+        it.row = s.row0 + j * NR;
+        it.rows = min(NR, s.rows - j * NR);
+        it.len = s.len;
+        it.first_tok = s.first;
+        it.head = t == 0;
+        it.tail = t + units == s.tiles;
+        it.tile = t;
+        it.unit = u;
+        it.tiles = s.tiles;
+        // the last row sees the most positions
+        const int most = min(s.len, s.first + (it.row_in_seq + it.rows - 1) / a.H);
+        it.n = max(0, min(t + units, (max(0, most) + kTile - 1) / kTile) - t);
+        left -= units;
+        u += units;
+        t = 0;
+        ++j;
+        return true;
+    }
+};
+
+// Sum (or maximum) over the 32 lanes of each of NC values: lane l of the
+// result holds value l (l < NC), for NC a multiple of 8 up to 32.
+template <int NC, bool MAX>
+__device__ __forceinline__ float lanes_reduce(float (&v)[NC], int lane) {
+    float r = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; c += 8) {
+        // butterfly over 8 columns: after 3 halvings a lane holds one column
+        // over 4-lane strided groups, then two more exchanges finish it
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = v[c + i];
+#pragma unroll
+        for (int h = 4; h > 0; h >>= 1) {
+            const bool up = lane & h;
+#pragma unroll
+            for (int i = 0; i < h; ++i) {
+                const float keep = up ? w[i + h] : w[i], give = up ? w[i] : w[i + h];
+                const float got = __shfl_xor_sync(0xffffffffu, give, h);
+                w[i] = MAX ? fmaxf(keep, got) : keep + got;
+            }
+        }
+        // lane l holds column c + (l & 7) over the lanes with its low bits
+#pragma unroll
+        for (int h = 8; h < 32; h <<= 1) {
+            const float got = __shfl_xor_sync(0xffffffffu, w[0], h);
+            w[0] = MAX ? fmaxf(w[0], got) : w[0] + got;
+        }
+        if ((lane >> 3) == (c >> 3)) r = w[0];
+    }
+    return r;
+}
+
+template <int NR>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_c,
+                     const uint8_t *__restrict__ cache, const Args a) {
+    using F = Cfg<NR>;
+    constexpr int NC = NR / 2;                // columns of a softmax group
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Misc *M = reinterpret_cast<Misc *>(sm + F::MISC);
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int G = gridDim.x, cta = blockIdx.x;
+
+    // ---- this CTA's units: a block-wide scan of the sequences' units
+    {
+        const int per = (a.N + kThreads - 1) / kThreads;
+        const int b_lo = min(a.N, t * per), b_hi = min(a.N, b_lo + per);
+        long long mine = 0;
+        for (int b = b_lo; b < b_hi; ++b) {
+            const Seq s = get_seq<NR>(a, b, cta == 0);     // CTA 0 flags what is wrong with a sequence
+            mine += (long long)s.tiles * s.row_tiles;
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        if (lane == 31) M->scan[warp] = incl;
+        if (t == 0) {
+            M->fail = 0;
+            M->b0 = M->j0 = M->t0 = 0;
+            a.split[cta] = Split{0, 0, 0, 0};
+            for (int i = 0; i < F::NP; ++i) { mbar_init(&M->full_p[i], 1); mbar_init(&M->empty_p[i], 1); }
+            for (int i = 0; i < F::NQ; ++i) { mbar_init(&M->full_r[i], 1); mbar_init(&M->empty_r[i], 1); }
+            mbar_init(&M->x_full, 1);
+            mbar_init(&M->x_empty, 1);
+            mbar_init(&M->s_full, 1);
+            mbar_init(&M->p_full, kSoftThreads);
+            mbar_init(&M->o_full, 1);
+            mbar_init(&M->done, 1);
+            fence_mbar_init();
+        }
+        if (warp == kSoftWarps) tmem_alloc(&M->tmem, kTmemCols);
+        if (warp == kSoftWarps + 1 && lane == 0) {
+            prefetch_tmap(&map_x);
+            prefetch_tmap(&map_c);
+        }
+        __syncthreads();
+        long long before = incl - mine, total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += M->scan[w];
+            total += M->scan[w];
+        }
+        // no CTA between a row tile's pieces is without one: with fewer units than CTAs, one each
+        const int used = (int)min((long long)G, total);
+        const long long u0 = cta < used ? total * cta / used : total;
+        const long long u1 = cta < used ? total * (cta + 1) / used : total;
+        if (t == 0) {
+            M->used = used;
+            M->units = (int)(u1 - u0);
+            M->start = u0;
+            M->total = total;
+        }
+        if (u1 > u0 && u0 >= before && u0 < before + mine) {
+            for (int b = b_lo; b < b_hi; ++b) {
+                const Seq s = get_seq<NR>(a, b, false);
+                const long long n = (long long)s.tiles * s.row_tiles;
+                if (u0 < before + n) {
+                    M->b0 = b;
+                    M->j0 = (int)((u0 - before) / s.tiles);
+                    M->t0 = (int)((u0 - before) % s.tiles);
+                    break;
+                }
+                before += n;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = M->tmem;
+    volatile int *fail = &M->fail;
+
+    if (warp == kSoftWarps + 1) {
+        // ================================================= copies
+        Walk<NR> walk(a, M);
+        Item it;
+        uint32_t n_tile = 0, n_item = 0;          // tiles and items with tiles so far
+        const int page = 1 << a.pages.page_log2;
+        const int brows = min(page, kTile), boxes = kTile / brows;   // TMA boxes down a tile
+        bool ok = true;
+        while (ok && walk.next(a, it)) {
+            if (it.n == 0) continue;
+            // the flat cache row of box `lane` of tile `i` (P * page: past the end, reads zeros)
+            auto box_row = [&](int i, bool flag) -> int {
+                const int pos = (it.tile + i) * kTile + lane * brows;
+                if (lane >= boxes || pos >= it.len) return -1;
+                const int64_t r = a.pages.row(it.b, pos);
+                if (r < 0 && flag) atomicOr(&g_kda_latent_decode_error, kErrSlot);
+                return r < 0 ? (int)(a.pages.P << a.pages.page_log2) : (int)r;
+            };
+            int rows = box_row(0, true);
+            if (n_item > 0) ok = warp_wait(&M->x_empty, (n_item - 1) & 1, fail);
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&M->x_full, NR * 1152u);
+                for (int k = 0; k < 9; ++k)
+                    tma_load_2d(sm + F::X + k * NR * 128u, &map_x, &M->x_full, 64 * k, it.row);
+            }
+            for (int i = 0; ok && i < it.n; ++i, ++n_tile) {
+                const int live = __popc(__ballot_sync(0xffffffffu, rows >= 0));
+                const int next_rows = i + 1 < it.n ? box_row(i + 1, true) : -1;
+                // the next tile's rows toward L2 (a page's rows are contiguous)
+                if (next_rows >= 0 && next_rows < (a.pages.P << a.pages.page_log2))
+                    for (int e = 0; e < brows; e += 16)
+                        bulk_prefetch_l2(cache + ((size_t)next_rows + e) * 1152u, 16 * 1152u);
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t u = 4 * n_tile + j, slot = u % F::NP, use = u / F::NP;
+                    if (use > 0) ok = warp_wait(&M->empty_p[slot], (use - 1) & 1, fail);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&M->full_p[slot], (uint32_t)live * brows * 256u);
+                    __syncwarp();
+                    uint8_t *dst = sm + F::PAIR + slot * kPair;
+                    if (rows >= 0) {
+                        tma_load_2d(dst + lane * brows * 128u, &map_c, &M->full_p[slot], 128 * j, rows);
+                        tma_load_2d(dst + 16384u + lane * brows * 128u, &map_c, &M->full_p[slot], 128 * j + 64, rows);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                const uint32_t slot = n_tile % F::NQ, use = n_tile / F::NQ;
+                if (use > 0) ok = warp_wait(&M->empty_r[slot], (use - 1) & 1, fail);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&M->full_r[slot], (uint32_t)live * brows * 128u);
+                __syncwarp();
+                if (rows >= 0)
+                    tma_load_2d(sm + F::ROPE + slot * kRope + lane * brows * 128u, &map_c, &M->full_r[slot], kLatent, rows);
+                __syncwarp();
+                rows = next_rows;
+            }
+            ++n_item;
+        }
+    } else if (warp == kSoftWarps) {
+        // ================================================= matrix products
+        if (lane == 0) {
+            Walk<NR> walk(a, M);
+            Item it;
+            uint32_t n_tile = 0, n_item = 0;
+            bool ok = true;
+            constexpr uint32_t id_s = instr_desc(kFmtBF16, 128, NR, 0, 0);
+            constexpr uint32_t id_o = instr_desc(kFmtBF16, 128, NR, 1, 1);
+            while (ok && walk.next(a, it)) {
+                if (it.n == 0) continue;
+                ok = wait_or_fail(&M->x_full, n_item & 1, fail);
+                for (int i = 0; ok && i < it.n; ++i, ++n_tile) {
+                    // S^T: channels 0..511 from the pairs, 512..575 from the shared part
+                    for (int j = 0; ok && j < 4; ++j) {
+                        const uint32_t u = 4 * n_tile + j, slot = u % F::NP;
+                        ok = wait_or_fail(&M->full_p[slot], (u / F::NP) & 1, fail);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t ka = smem_u32(sm + F::PAIR + slot * kPair);
+                        const uint32_t xa = smem_u32(sm + F::X) + 2 * j * NR * 128u;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_bf16_ss(tmem + TM_S, smem_desc(ka + (k >> 2) * 16384u + (k & 3) * 32u, 16, 1024, kSwizzle128B),
+                                        smem_desc(xa + (k >> 2) * NR * 128u + (k & 3) * 32u, 16, 1024, kSwizzle128B),
+                                        id_s, j > 0 || k > 0);
+                    }
+                    const uint32_t rslot = n_tile % F::NQ;
+                    const uint32_t ra = smem_u32(sm + F::ROPE + rslot * kRope);
+                    if (ok) ok = wait_or_fail(&M->full_r[rslot], (n_tile / F::NQ) & 1, fail);
+                    if (!ok) break;
+                    tc_fence_after();
+                    {
+                        const uint32_t xa = smem_u32(sm + F::X) + 8 * NR * 128u;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_ss(tmem + TM_S, smem_desc(ra + k * 32u, 16, 1024, kSwizzle128B),
+                                        smem_desc(xa + k * 32u, 16, 1024, kSwizzle128B), id_s, 1);
+                    }
+                    mma_commit(&M->s_full);
+                    if (i + 1 == it.n) mma_commit(&M->x_empty);
+                    // O^T += c^T P^T, a slot released as soon as its block is done
+                    ok = wait_or_fail(&M->p_full, n_tile & 1, fail);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t slot = (4 * n_tile + j) % F::NP;
+                        const uint32_t va = smem_u32(sm + F::PAIR + slot * kPair);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_bf16_ss(tmem + TM_O + 64 * j, smem_desc(va + k * 2048u, 16384, 1024, kSwizzle128B),
+                                        smem_desc(ra + k * 2048u, 8192, 1024, kSwizzle128B), id_o, i > 0 || k > 0);
+                        mma_commit(&M->empty_p[slot]);
+                    }
+                    mma_commit(&M->empty_r[rslot]);
+                    if (i + 1 == it.n) mma_commit(&M->o_full);
+                }
+                ++n_item;
+            }
+            // nothing of this CTA's products is in flight when its TMEM goes
+            mma_commit(&M->done);
+            mbar_wait(&M->done, 0, kWaitLimit);
+        }
+    } else {
+        // ================================================= softmax, output
+        const int g = warp >> 2, quarter = warp & 3;
+        const int col0 = g * NC;                        // this group's columns
+        const uint32_t lane_base = (uint32_t)quarter << 21;   // 32 lanes a quarter, lane field at bit 16
+        const int bar = 1 + g;
+        const int pos_in_tile = quarter * 32 + lane;
+        Walk<NR> walk(a, M);
+        Item it;
+        uint32_t n_tile = 0, n_item = 0;
+        bool ok = true;
+        while (ok && walk.next(a, it)) {
+            float l[NC];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) l[c] = 0.f;
+            // (the barriers of the last item's output came after its last readers)
+            if (quarter == 0 && lane < NC) {
+                const int r = it.row_in_seq + col0 + lane;   // several new tokens differ in what they see
+                M->seen[g][lane] = min(it.len, it.first_tok + r / a.H);
+                M->m[g][lane] = -CUDART_INF_F;
+            }
+            bar_sync(bar, 128);
+            // from here on a tile needs masks: the first row's limit
+            const int all_see = min(it.len, it.first_tok + it.row_in_seq / a.H);
+            for (int i = 0; i < it.n; ++i, ++n_tile) {
+                const int p0 = (it.tile + i) * kTile;
+                ok = wait_or_fail(&M->s_full, n_tile & 1, fail);
+                tc_fence_after();
+                float s[NC];
+                tmem_ldn<NC>(tmem + lane_base + TM_S + col0, s);
+                tmem_wait_ld();
+                if (p0 + kTile > it.len) {
+                    // rows behind the end: whatever the cache holds there must not meet a zero weight
+                    const int from = it.len - p0;
+                    for (int e = t; e < (kTile - from) * 64; e += kSoftThreads) {
+                        const int r = from + (e >> 6), blk = (e >> 3) & 7, ch = e & 7;
+                        const uint32_t slot = (4 * n_tile + (blk >> 1)) % F::NP;
+                        *reinterpret_cast<uint4 *>(sm + F::PAIR + slot * kPair + (blk & 1) * 16384u + r * 128u + ch * 16u) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                }
+                const bool masked = p0 + kTile > all_see;
+                bool move = i == 0 || !ok;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    s[c] *= a.scale_log2;
+                    if (masked && p0 + pos_in_tile >= M->seen[g][c]) s[c] = -CUDART_INF_F;
+                    move |= s[c] - M->m[g][c] > kMoveAt;     // (-inf) - (-inf) is not
+                }
+                if (bar_any(bar, 128, move)) {
+                    // a new maximum for every column of the group
+                    const float mx = lanes_reduce<NC, true>(s, lane);
+                    if (lane < NC) M->red[g][quarter][lane] = mx;
+                    if (bar_any(bar, 128, !ok)) { ok = false; break; }
+                    if (quarter == 0 && lane < NC) {
+                        const float was = M->m[g][lane];
+                        float now = fmaxf(fmaxf(fmaxf(M->red[g][0][lane], M->red[g][1][lane]),
+                                                fmaxf(M->red[g][2][lane], M->red[g][3][lane])), was);
+                        // a row that sees nothing in its piece's first tile sees nothing in
+                        // the later ones either: any finite maximum serves it
+                        if (now == -CUDART_INF_F) now = 0.f;
+                        M->m[g][lane] = now;
+                        M->f[g][lane] = ex2_approx(was - now);
+                    }
+                    bar_sync(bar, 128);
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) l[c] *= M->f[g][c];
+                    if (i > 0) {                       // the products before this tile are done (s_full)
+#pragma unroll 1
+                        for (int j = 0; j < 4; ++j) {
+#pragma unroll 1
+                            for (int c0 = 0; c0 < NC; c0 += 8) {
+                                const uint32_t at = tmem + lane_base + TM_O + 64 * j + col0 + c0;
+                                float ov[8];
+                                tmem_ldn<8>(at, ov);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) ov[c] *= M->f[g][c0 + c];
+                                tmem_stn<8>(at, ov);
+                            }
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                uint8_t *pr = sm + F::ROPE + (n_tile % F::NQ) * kRope + pos_in_tile * 128u;
+#pragma unroll
+                for (int c = 0; c < NC; c += 8) {
+                    float p[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        p[e] = ex2_approx(s[c + e] - M->m[g][c + e]);
+                        l[c + e] += p[e];
+                    }
+                    *reinterpret_cast<uint4 *>(pr + ((((col0 + c) >> 3) ^ (pos_in_tile & 7)) << 4)) = pack_bf8(p);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(&M->p_full);
+            }
+            if (!ok) break;
+            // ---- the row tile's (piece's) output
+            const bool whole = it.head && it.tail;
+            const int slot = 2 * cta + (it.head ? 1 : 0);      // a piece that starts here goes on behind
+            if (it.n > 0) {
+                ok = wait_or_fail(&M->o_full, n_item & 1, fail);
+                if (bar_any(bar, 128, !ok)) { ok = false; break; }
+                tc_fence_after();
+                ++n_item;
+            }
+            const float part = lanes_reduce<NC, false>(l, lane);
+            if (lane < NC) M->red[g][quarter][lane] = part;
+            bar_sync(bar, 128);
+            if (quarter == 0 && lane < NC) {
+                const float sum = (M->red[g][0][lane] + M->red[g][1][lane]) + (M->red[g][2][lane] + M->red[g][3][lane]);
+                const float lg = sum > 0.f ? M->m[g][lane] + log2f(sum) : -CUDART_INF_F;
+                M->f[g][lane] = sum > 0.f ? 1.f / sum : 0.f;
+                if (col0 + lane < it.rows) {
+                    if (!whole) a.ws_lse[slot * NR + col0 + lane] = lg;
+                    else if (a.lse) a.lse[it.row + col0 + lane] = lg * 0.6931471805599453f;
+                }
+            }
+            bar_sync(bar, 128);
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                float ov[NC];
+                if (it.n > 0) {
+                    tmem_ldn<NC>(tmem + lane_base + TM_O + 64 * j + col0, ov);
+                    tmem_wait_ld();
+                }
+                const int ch = 128 * j + pos_in_tile;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) ov[c] = it.n > 0 ? ov[c] * M->f[g][c] : 0.f;
+                if (!whole) {
+                    float *dst = a.ws_o + ((size_t)slot * NR + col0) * kLatent + ch;
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        if (col0 + c < it.rows) dst[(size_t)c * kLatent] = ov[c];
+                } else {
+                    // pairs of channels: even lanes store column c, odd lanes column c + 1
+                    __nv_bfloat16 *dst = a.o + ((size_t)it.row + col0) * kLatent + (ch & ~1);
+                    const bool odd = lane & 1;
+#pragma unroll
+                    for (int c = 0; c < NC; c += 2) {
+                        const float got = __shfl_xor_sync(0xffffffffu, odd ? ov[c] : ov[c + 1], 1);
+                        const uint32_t two = odd ? pack_bf2(got, ov[c + 1]) : pack_bf2(ov[c], got);
+                        if (col0 + c + odd < it.rows)
+                            *reinterpret_cast<uint32_t *>(dst + (size_t)(c + odd) * kLatent) = two;
+                    }
+                }
+            }
+            tc_fence_before();
+            // the tile that starts here and goes on: who holds its last piece
+            if (t == 0 && it.head && !it.tail) {
+                // CTA c holds unit u when c W / G <= u < (c + 1) W / G (rounded down), so the
+                // last c with c W / G < u + 1
+                const long long last = it.unit + it.tiles - 1;
+                a.split[cta] = Split{it.row, it.rows, (int)(((last + 1) * M->used - 1) / M->total), 0};
+            }
+        }
+        if (!ok && t == 0) atomicOr(&g_kda_latent_decode_error, kErrWait);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSoftWarps) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the pieces of the row tile that starts in CTA c = blockIdx.x and goes
+// on behind it: o = sum_k 2^(lse_k - lse) o_k, in the order of the positions.
+// A block a row, four channels a thread; bound by the pieces' bytes, which
+// the first kernel has just left in L2.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = 8;              // blocks a row tile
+
+__global__ void __launch_bounds__(kJoinThreads)
+latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws_lse,
+                   const float *__restrict__ ws_o, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
+                   int NR) {
+    const int c = blockIdx.x, t = threadIdx.x, lane = t & 31;
+    const Split sp = split[c];
+    __shared__ float w[kMaxCtas];
+    const int n = sp.last - c + 1;
+    for (int r = blockIdx.y; r < sp.rows; r += kJoinRows) {
+        auto slot = [&](int k) { return k == 0 ? 2 * c + 1 : 2 * (c + k); };
+        // every warp finds the maximum and the sum by itself
+        float v[(kMaxCtas + 31) / 32], mx = -CUDART_INF_F, sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < (kMaxCtas + 31) / 32; ++e) {
+            const int k = 32 * e + lane;
+            v[e] = k < n ? ws_lse[slot(k) * NR + r] : -CUDART_INF_F;
+            mx = fmaxf(mx, v[e]);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+#pragma unroll
+        for (int e = 0; e < (kMaxCtas + 31) / 32; ++e) {
+            v[e] = mx == -CUDART_INF_F ? 0.f : ex2_approx(v[e] - mx);
+            sum += v[e];
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        __syncthreads();                  // the last row's weights are read
+        if (t < 32) {
+#pragma unroll
+            for (int e = 0; e < (kMaxCtas + 31) / 32; ++e)
+                if (32 * e + lane < n) w[32 * e + lane] = sum > 0.f ? v[e] / sum : 0.f;
+        }
+        __syncthreads();
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float4 x = *reinterpret_cast<const float4 *>(ws_o + ((size_t)slot(k) * NR + r) * kLatent + 4 * t);
+            const float wk = w[k];
+            acc.x = fmaf(wk, x.x, acc.x);
+            acc.y = fmaf(wk, x.y, acc.y);
+            acc.z = fmaf(wk, x.z, acc.z);
+            acc.w = fmaf(wk, x.w, acc.w);
+        }
+        const size_t row = (size_t)sp.row + r;
+        *reinterpret_cast<uint2 *>(o + row * kLatent + 4 * t) = make_uint2(pack_bf2(acc.x, acc.y), pack_bf2(acc.z, acc.w));
+        if (lse && t == 0) lse[row] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -CUDART_INF_F;
+    }
+}
+
+// Rows of a tile: the average sequence's rows in as few tiles of at most 64
+// as hold them, in steps of 16 (the products' column step).
+int rows_of_tile(int N, int64_t T, int H) {
+    const int64_t rows = (T + N - 1) / N * H;
+    const int64_t tiles = (rows + 63) / 64;
+    return (int)std::min<int64_t>(64, ((rows + tiles - 1) / tiles + 15) / 16 * 16);
+}
+
+constexpr size_t kSplitBytes = 4096, kLseBytes = 2 * kMaxCtas * 64 * sizeof(float);
+static_assert(kSplitBytes >= kMaxCtas * sizeof(Split), "records of the split row tiles");
+
+template <int NR>
+cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const void *cache, const Args &a, int G,
+                   cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)(Cfg<NR>::BYTES + 1024));
+    if (e != cudaSuccess) return e;
+    latent_decode_kernel<NR><<<G, kThreads, Cfg<NR>::BYTES + 1024, stream>>>(
+        mx, mc, static_cast<const uint8_t *>(cache), a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    latent_join_kernel<<<dim3(G, kJoinRows), kJoinThreads, 0, stream>>>(a.split, a.ws_lse, a.ws_o, a.o, a.lse, NR);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Workspace: the split records, the pieces' log2-sum-exp, the pieces.
+size_t latent_decode_workspace_bytes(int N, int64_t T, int H) {
+    return kSplitBytes + kLseBytes + (size_t)2 * kMaxCtas * rows_of_tile(N, T, H) * kLatent * sizeof(float);
+}
+
+cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t *table,
+                                 const int32_t *seq_lens, const int32_t *cu, float scale, void *o,
+                                 float *lse, int N, int64_t T, int H, int64_t P, int page,
+                                 int max_pages, void *ws, cudaStream_t stream) {
+    const int NR = rows_of_tile(N, T, H);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    CUtensorMap mx, mc;
+    if (!make_map_rows(&mx, q, kLatentRow, T * H, kLatentRow, (uint32_t)NR) ||
+        !make_map_rows(&mc, cache, kLatentRow, P * page, kLatentRow, (uint32_t)std::min(page, kTile)))
+        return cudaErrorInvalidValue;
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    Args a;
+    a.pages = paged_rows(table, P, page, max_pages);
+    a.seq_lens = seq_lens;
+    a.cu = cu;
+    a.N = N;
+    a.T = (int)T;
+    a.H = H;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.o = static_cast<__nv_bfloat16 *>(o);
+    a.lse = lse;
+    a.split = reinterpret_cast<Split *>(w);
+    a.ws_lse = reinterpret_cast<float *>(w + kSplitBytes);
+    a.ws_o = reinterpret_cast<float *>(w + kSplitBytes + kLseBytes);
+    const int G = std::min(sms, kMaxCtas);
+    switch (NR) {
+        case 16: return launch<16>(mx, mc, cache, a, G, stream);
+        case 32: return launch<32>(mx, mc, cache, a, G, stream);
+        case 48: return launch<48>(mx, mc, cache, a, G, stream);
+        default: return launch<64>(mx, mc, cache, a, G, stream);
+    }
+}
+
+cudaError_t read_latent_decode_error(unsigned int *code, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_kda_latent_decode_error, sizeof(unsigned int));
+    if (e != cudaSuccess || !reset) return e;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_kda_latent_decode_error, &zero, sizeof(unsigned int));
+}
+
+}  // namespace kda

@@ -24,7 +24,7 @@ struct PagedRows {
 
     __device__ __forceinline__ int max_len() const {
         const long long m = (long long)max_pages << page_log2;
-        return m > 0x7fffffffLL ? 0x7fffffff : (int)m;
+        return m > 0x7ffff000LL ? 0x7ffff000 : (int)m;   // sums with a tile stay in 32 bits
     }
     // Flat cache row of position `pos` of sequence `b`, or -1 (page index
     // outside the cache).  0 <= pos < max_len().
@@ -34,6 +34,12 @@ struct PagedRows {
         return ((int64_t)pg << page_log2) + (pos & ((1 << page_log2) - 1));
     }
 };
+
+inline PagedRows paged_rows(const int32_t *table, int64_t P, int page, int max_pages) {
+    int lg = 0;
+    while ((1 << lg) < page) ++lg;
+    return PagedRows{table, P, lg, max_pages};
+}
 
 // The sequence that holds packed token t: the largest b with cu[b] <= t.
 // cu == nullptr: one token a sequence.  Returns -1 for a token that no
