@@ -87,9 +87,10 @@ struct Misc {
     long long start, total;
     // per column (row of the tile), by softmax group
     float red[2][4][32];                  // cross-warp reductions
-    float m[2][32];                       // running maximum, log2 units
-    float f[2][32];                       // rescale factor, then 1 / sum
-    int seen[2][32];                      // positions it may see
+    alignas(16) float neg_m[2][32];       // minus the running maximum, log2 units
+    alignas(16) float shift[2][32];       // how far the maximum moves
+    alignas(16) float f[2][32];           // rescale factor, then 1 / sum
+    alignas(16) int seen[2][32];                      // positions it may see
 };
 static_assert(sizeof(Misc) <= 4096, "control block");
 
@@ -368,67 +369,76 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         }
     } else if (warp == kSoftWarps) {
         // ================================================= matrix products
-        if (lane == 0) {
-            Walk<NR> walk(a, M);
-            Item it;
-            uint32_t n_tile = 0, n_item = 0;
-            bool ok = true;
-            constexpr uint32_t id_s = instr_desc(kFmtBF16, 128, NR, 0, 0);
-            constexpr uint32_t id_o = instr_desc(kFmtBF16, 128, NR, 1, 1);
-            while (ok && walk.next(a, it)) {
-                if (it.n == 0) continue;
-                ok = wait_or_fail(&M->x_full, n_item & 1, fail);
-                for (int i = 0; ok && i < it.n; ++i, ++n_tile) {
-                    // S^T: channels 0..511 from the pairs, 512..575 from the shared part
-                    for (int j = 0; ok && j < 4; ++j) {
-                        const uint32_t u = 4 * n_tile + j, slot = u % F::NP;
-                        ok = wait_or_fail(&M->full_p[slot], (u / F::NP) & 1, fail);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t ka = smem_u32(sm + F::PAIR + slot * kPair);
-                        const uint32_t xa = smem_u32(sm + F::X) + 2 * j * NR * 128u;
+        // the whole warp walks and waits, one lane issues
+        Walk<NR> walk(a, M);
+        Item it;
+        uint32_t n_tile = 0, n_item = 0;
+        bool ok = true;
+        constexpr uint32_t id_s = instr_desc(kFmtBF16, 128, NR, 0, 0);
+        constexpr uint32_t id_o = instr_desc(kFmtBF16, 128, NR, 1, 1);
+        const uint64_t x_desc = smem_desc(smem_u32(sm + F::X), 16, 1024, kSwizzle128B);
+        const uint64_t k_desc = smem_desc(smem_u32(sm + F::PAIR), 16, 1024, kSwizzle128B);
+        const uint64_t v_desc = smem_desc(smem_u32(sm + F::PAIR), 16384, 1024, kSwizzle128B);
+        const uint64_t r_desc = smem_desc(smem_u32(sm + F::ROPE), 16, 1024, kSwizzle128B);
+        while (ok && walk.next(a, it)) {
+            if (it.n == 0) continue;
+            ok = warp_wait(&M->x_full, n_item & 1, fail);
+            for (int i = 0; ok && i < it.n; ++i, ++n_tile) {
+                // S^T: channels 0..511 from the pairs, 512..575 from the shared part
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t u = 4 * n_tile + j, slot = u % F::NP;
+                    ok = ok && warp_wait(&M->full_p[slot], (u / F::NP) & 1, fail);
+                    tc_fence_after();
+                    const uint64_t kd = desc_add(k_desc, slot * kPair);
+                    if (ok && elect_one()) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_bf16_ss(tmem + TM_S, smem_desc(ka + (k >> 2) * 16384u + (k & 3) * 32u, 16, 1024, kSwizzle128B),
-                                        smem_desc(xa + (k >> 2) * NR * 128u + (k & 3) * 32u, 16, 1024, kSwizzle128B),
-                                        id_s, j > 0 || k > 0);
+                            mma_bf16_ss(tmem + TM_S, desc_add(kd, (k >> 2) * 16384u + (k & 3) * 32u),
+                                        desc_add(x_desc, (2 * j + (k >> 2)) * NR * 128u + (k & 3) * 32u), id_s,
+                                        j > 0 || k > 0);
                     }
-                    const uint32_t rslot = n_tile % F::NQ;
-                    const uint32_t ra = smem_u32(sm + F::ROPE + rslot * kRope);
-                    if (ok) ok = wait_or_fail(&M->full_r[rslot], (n_tile / F::NQ) & 1, fail);
-                    if (!ok) break;
-                    tc_fence_after();
-                    {
-                        const uint32_t xa = smem_u32(sm + F::X) + 8 * NR * 128u;
+                    __syncwarp();
+                }
+                const uint32_t rslot = n_tile % F::NQ;
+                const uint64_t rd = desc_add(r_desc, rslot * kRope);
+                ok = ok && warp_wait(&M->full_r[rslot], (n_tile / F::NQ) & 1, fail);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16_ss(tmem + TM_S, smem_desc(ra + k * 32u, 16, 1024, kSwizzle128B),
-                                        smem_desc(xa + k * 32u, 16, 1024, kSwizzle128B), id_s, 1);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16_ss(tmem + TM_S, desc_add(rd, k * 32u), desc_add(x_desc, 8 * NR * 128u + k * 32u), id_s, 1);
                     mma_commit(&M->s_full);
                     if (i + 1 == it.n) mma_commit(&M->x_empty);
-                    // O^T += c^T P^T, a slot released as soon as its block is done
-                    ok = wait_or_fail(&M->p_full, n_tile & 1, fail);
-                    if (!ok) break;
-                    tc_fence_after();
+                }
+                __syncwarp();
+                // O^T += c^T P^T, a slot released as soon as its block is done (P's rows are one
+                // 128-byte atom wide, so the shared part's descriptor serves it, 16 rows a step)
+                ok = warp_wait(&M->p_full, n_tile & 1, fail);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t slot = (4 * n_tile + j) % F::NP;
-                        const uint32_t va = smem_u32(sm + F::PAIR + slot * kPair);
+                        const uint64_t vd = desc_add(v_desc, slot * kPair);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
-                            mma_bf16_ss(tmem + TM_O + 64 * j, smem_desc(va + k * 2048u, 16384, 1024, kSwizzle128B),
-                                        smem_desc(ra + k * 2048u, 8192, 1024, kSwizzle128B), id_o, i > 0 || k > 0);
+                            mma_bf16_ss(tmem + TM_O + 64 * j, desc_add(vd, k * 2048u), desc_add(rd, k * 2048u), id_o,
+                                        i > 0 || k > 0);
                         mma_commit(&M->empty_p[slot]);
                     }
                     mma_commit(&M->empty_r[rslot]);
                     if (i + 1 == it.n) mma_commit(&M->o_full);
                 }
-                ++n_item;
+                __syncwarp();
             }
-            // nothing of this CTA's products is in flight when its TMEM goes
-            mma_commit(&M->done);
-            mbar_wait(&M->done, 0, kWaitLimit);
+            ++n_item;
         }
+        // nothing of this CTA's products is in flight when its TMEM goes
+        if (elect_one()) mma_commit(&M->done);
+        warp_wait(&M->done, 0, fail);
     } else {
         // ================================================= softmax, output
         const int g = warp >> 2, quarter = warp & 3;
@@ -441,14 +451,14 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         uint32_t n_tile = 0, n_item = 0;
         bool ok = true;
         while (ok && walk.next(a, it)) {
-            float l[NC];
+            float2 l[NC / 2];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) l[c] = 0.f;
+            for (int c = 0; c < NC / 2; ++c) l[c] = make_float2(0.f, 0.f);
             // (the barriers of the last item's output came after its last readers)
             if (quarter == 0 && lane < NC) {
                 const int r = it.row_in_seq + col0 + lane;   // several new tokens differ in what they see
                 M->seen[g][lane] = min(it.len, it.first_tok + r / a.H);
-                M->m[g][lane] = -CUDART_INF_F;
+                M->neg_m[g][lane] = 0.f;
             }
             bar_sync(bar, 128);
             // from here on a tile needs masks: the first row's limit
@@ -470,32 +480,49 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                             make_uint4(0, 0, 0, 0);
                     }
                 }
-                const bool masked = p0 + kTile > all_see;
-                bool move = i == 0 || !ok;
+                // s <- s scale log2 e - m
+                const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    s[c] *= a.scale_log2;
-                    if (masked && p0 + pos_in_tile >= M->seen[g][c]) s[c] = -CUDART_INF_F;
-                    move |= s[c] - M->m[g][c] > kMoveAt;     // (-inf) - (-inf) is not
+                for (int c = 0; c < NC; c += 4) {
+                    const float4 nm = *reinterpret_cast<const float4 *>(&M->neg_m[g][c]);
+                    const float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), sc2, make_float2(nm.x, nm.y));
+                    const float2 y = __ffma2_rn(make_float2(s[c + 2], s[c + 3]), sc2, make_float2(nm.z, nm.w));
+                    s[c] = x.x; s[c + 1] = x.y; s[c + 2] = y.x; s[c + 3] = y.y;
                 }
-                if (bar_any(bar, 128, move)) {
+                if (p0 + kTile > all_see) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        if (p0 + pos_in_tile >= M->seen[g][c]) s[c] = -CUDART_INF_F;
+                }
+                float top = s[0];
+#pragma unroll
+                for (int c = 1; c < NC; ++c) top = fmaxf(top, s[c]);
+                if (bar_any(bar, 128, top > kMoveAt || i == 0 || !ok)) {
                     // a new maximum for every column of the group
                     const float mx = lanes_reduce<NC, true>(s, lane);
                     if (lane < NC) M->red[g][quarter][lane] = mx;
                     if (bar_any(bar, 128, !ok)) { ok = false; break; }
                     if (quarter == 0 && lane < NC) {
-                        const float was = M->m[g][lane];
-                        float now = fmaxf(fmaxf(fmaxf(M->red[g][0][lane], M->red[g][1][lane]),
-                                                fmaxf(M->red[g][2][lane], M->red[g][3][lane])), was);
-                        // a row that sees nothing in its piece's first tile sees nothing in
-                        // the later ones either: any finite maximum serves it
-                        if (now == -CUDART_INF_F) now = 0.f;
-                        M->m[g][lane] = now;
-                        M->f[g][lane] = ex2_approx(was - now);
+                        float up = fmaxf(fmaxf(M->red[g][0][lane], M->red[g][1][lane]),
+                                         fmaxf(M->red[g][2][lane], M->red[g][3][lane]));
+                        // the first tile sets the maximum, later ones only raise it.  A row that
+                        // sees nothing in its piece's first tile sees nothing in the later ones
+                        // either: any finite maximum serves it
+                        up = i > 0 ? fmaxf(up, 0.f) : up == -CUDART_INF_F ? 0.f : up;
+                        const float was = M->neg_m[g][lane], now = was - up;
+                        up = was - now;                // what the rounded maximum really moves by
+                        M->neg_m[g][lane] = now;
+                        M->shift[g][lane] = up;
+                        M->f[g][lane] = i > 0 ? ex2_approx(-up) : 1.f;
                     }
                     bar_sync(bar, 128);
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) l[c] *= M->f[g][c];
+                    for (int c = 0; c < NC; ++c) s[c] -= M->shift[g][c];
+#pragma unroll
+                    for (int c = 0; c < NC / 2; ++c) {
+                        l[c].x *= M->f[g][2 * c];
+                        l[c].y *= M->f[g][2 * c + 1];
+                    }
                     if (i > 0) {                       // the products before this tile are done (s_full)
 #pragma unroll 1
                         for (int j = 0; j < 4; ++j) {
@@ -518,10 +545,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 for (int c = 0; c < NC; c += 8) {
                     float p[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        p[e] = ex2_approx(s[c + e] - M->m[g][c + e]);
-                        l[c + e] += p[e];
-                    }
+                    for (int e = 0; e < 8; ++e) p[e] = ex2_approx(s[c + e]);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2)
+                        l[(c + e) / 2] = __fadd2_rn(l[(c + e) / 2], make_float2(p[e], p[e + 1]));
                     *reinterpret_cast<uint4 *>(pr + ((((col0 + c) >> 3) ^ (pos_in_tile & 7)) << 4)) = pack_bf8(p);
                 }
                 fence_proxy_async_smem();
@@ -538,12 +565,15 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 tc_fence_after();
                 ++n_item;
             }
-            const float part = lanes_reduce<NC, false>(l, lane);
+            float ls[NC];
+#pragma unroll
+            for (int c = 0; c < NC / 2; ++c) { ls[2 * c] = l[c].x; ls[2 * c + 1] = l[c].y; }
+            const float part = lanes_reduce<NC, false>(ls, lane);
             if (lane < NC) M->red[g][quarter][lane] = part;
             bar_sync(bar, 128);
             if (quarter == 0 && lane < NC) {
                 const float sum = (M->red[g][0][lane] + M->red[g][1][lane]) + (M->red[g][2][lane] + M->red[g][3][lane]);
-                const float lg = sum > 0.f ? M->m[g][lane] + log2f(sum) : -CUDART_INF_F;
+                const float lg = sum > 0.f ? log2f(sum) - M->neg_m[g][lane] : -CUDART_INF_F;
                 M->f[g][lane] = sum > 0.f ? 1.f / sum : 0.f;
                 if (col0 + lane < it.rows) {
                     if (!whole) a.ws_lse[slot * NR + col0 + lane] = lg;
@@ -599,25 +629,31 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
 
 // Joins the pieces of the row tile that starts in CTA c = blockIdx.x and goes
 // on behind it: o = sum_k 2^(lse_k - lse) o_k, in the order of the positions.
-// A block a row, four channels a thread; bound by the pieces' bytes, which
-// the first kernel has just left in L2.
-constexpr int kJoinThreads = 128;
-constexpr int kJoinRows = 8;              // blocks a row tile
+// With few pieces a warp takes a row by itself; with many (few long
+// sequences, so few such tiles) a block shares a row's pieces among its warps
+// and adds the warps' sums in order.  Bound by the pieces' bytes, which the
+// first kernel has just left in L2, and by the latency of its few loads.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinBlocks = 32;           // blocks a row tile
+constexpr int kJoinAlone = 8;             // pieces a warp takes by itself
 
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(32 * kJoinWarps)
 latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws_lse,
                    const float *__restrict__ ws_o, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
                    int NR) {
-    const int c = blockIdx.x, t = threadIdx.x, lane = t & 31;
+    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Split sp = split[c];
-    __shared__ float w[kMaxCtas];
     const int n = sp.last - c + 1;
-    for (int r = blockIdx.y; r < sp.rows; r += kJoinRows) {
-        auto slot = [&](int k) { return k == 0 ? 2 * c + 1 : 2 * (c + k); };
+    const bool alone = n <= kJoinAlone;
+    const int r0 = alone ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
+    const int step = alone ? kJoinBlocks * kJoinWarps : kJoinBlocks;
+    __shared__ float4 part[kJoinWarps][kLatent / 4];
+    auto slot = [&](int k) { return k == 0 ? 2 * c + 1 : 2 * (c + k); };
+    for (int r = r0; r < sp.rows; r += step) {
         // every warp finds the maximum and the sum by itself
-        float v[(kMaxCtas + 31) / 32], mx = -CUDART_INF_F, sum = 0.f;
+        float v[kMaxCtas / 32], mx = -CUDART_INF_F, sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < (kMaxCtas + 31) / 32; ++e) {
+        for (int e = 0; e < kMaxCtas / 32; ++e) {
             const int k = 32 * e + lane;
             v[e] = k < n ? ws_lse[slot(k) * NR + r] : -CUDART_INF_F;
             mx = fmaxf(mx, v[e]);
@@ -625,32 +661,57 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
 #pragma unroll
-        for (int e = 0; e < (kMaxCtas + 31) / 32; ++e) {
+        for (int e = 0; e < kMaxCtas / 32; ++e) {
             v[e] = mx == -CUDART_INF_F ? 0.f : ex2_approx(v[e] - mx);
             sum += v[e];
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        __syncthreads();                  // the last row's weights are read
-        if (t < 32) {
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        float4 acc[4];
 #pragma unroll
-            for (int e = 0; e < (kMaxCtas + 31) / 32; ++e)
-                if (32 * e + lane < n) w[32 * e + lane] = sum > 0.f ? v[e] / sum : 0.f;
-        }
-        __syncthreads();
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-            const float4 x = *reinterpret_cast<const float4 *>(ws_o + ((size_t)slot(k) * NR + r) * kLatent + 4 * t);
-            const float wk = w[k];
-            acc.x = fmaf(wk, x.x, acc.x);
-            acc.y = fmaf(wk, x.y, acc.y);
-            acc.z = fmaf(wk, x.z, acc.z);
-            acc.w = fmaf(wk, x.w, acc.w);
+        for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < kMaxCtas / 32; ++e) {
+            if (32 * e >= n) break;
+            const int hi = min(32, n - 32 * e);
+#pragma unroll 2
+            for (int k = alone ? 0 : warp; k < hi; k += alone ? 1 : kJoinWarps) {
+                const float w = __shfl_sync(0xffffffffu, v[e], k) * inv;
+                const float4 *src = reinterpret_cast<const float4 *>(ws_o + ((size_t)slot(32 * e + k) * NR + r) * kLatent);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float4 x = src[32 * q + lane];
+                    acc[q].x = fmaf(w, x.x, acc[q].x);
+                    acc[q].y = fmaf(w, x.y, acc[q].y);
+                    acc[q].z = fmaf(w, x.z, acc[q].z);
+                    acc[q].w = fmaf(w, x.w, acc[q].w);
+                }
+            }
         }
         const size_t row = (size_t)sp.row + r;
-        *reinterpret_cast<uint2 *>(o + row * kLatent + 4 * t) = make_uint2(pack_bf2(acc.x, acc.y), pack_bf2(acc.z, acc.w));
-        if (lse && t == 0) lse[row] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -CUDART_INF_F;
+        uint2 *dst = reinterpret_cast<uint2 *>(o + row * kLatent);
+        if (alone) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                dst[32 * q + lane] = make_uint2(pack_bf2(acc[q].x, acc[q].y), pack_bf2(acc[q].z, acc[q].w));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) part[warp][32 * q + lane] = acc[q];
+            __syncthreads();
+            if (threadIdx.x < kLatent / 4) {
+                float4 x = part[0][threadIdx.x];
+#pragma unroll
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    const float4 y = part[w][threadIdx.x];
+                    x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                }
+                dst[threadIdx.x] = make_uint2(pack_bf2(x.x, x.y), pack_bf2(x.z, x.w));
+            }
+            __syncthreads();
+        }
+        if (lse && lane == 0 && (alone || warp == 0))
+            lse[row] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -CUDART_INF_F;
     }
 }
 
@@ -675,7 +736,7 @@ cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const void *cac
         mx, mc, static_cast<const uint8_t *>(cache), a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    latent_join_kernel<<<dim3(G, kJoinRows), kJoinThreads, 0, stream>>>(a.split, a.ws_lse, a.ws_o, a.o, a.lse, NR);
+    latent_join_kernel<<<dim3(G, kJoinBlocks), 32 * kJoinWarps, 0, stream>>>(a.split, a.ws_lse, a.ws_o, a.o, a.lse, NR);
     return cudaGetLastError();
 }
 

@@ -40,6 +40,21 @@ __device__ __forceinline__ void tmem_stn(uint32_t taddr, const float (&v)[N]) {
     for (int c = 0; c < N; c += 8) tmem_st8p(taddr + c, v + c);
 }
 
+// One lane of a converged warp, the same every time: what it guards is known
+// to the compiler as warp-uniform, so descriptors stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+// A descriptor `bytes` further on (no carry out of its 14 address bits:
+// shared memory ends below 2^18).
+__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
 // A bounded wait that also ends when another role of the block has given up.
 __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, volatile int *fail) {
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
