@@ -1,79 +1,498 @@
-// Causal attention of many new tokens with expanded keys and values: the
-// prefill side of latent attention.
+// Causal attention of many new tokens with expanded keys and values, on the
+// tensor cores: the prefill side of latent attention.
 //
 // Head h of token j has the key [kv[j][h][0:128] | k_pe[j]] and the value
 // kv[j][h][128:256]; the last 64 key channels are one row a token for all
-// heads.  The queries of a sequence are its last tokens: query i of nq sees
-// keys 0 .. nk - nq + i.
+// heads and are read as such.  The queries of a sequence are its last tokens:
+// query i of nq sees keys 0 .. nk - nq + i.
 //   s = scale <q, k>,   o = softmax(s) v,   lse = ln sum e^s
-#include <math_constants.h>
+//
+// A CTA (one an SM) takes work tiles of 256 queries of one (sequence, head)
+// and runs over the keys 128 at a time, with two halves of 128 queries in
+// turn on the tensor cores, so that one half's products cover the other's
+// softmax:
+//   S_g [128 x 128] = Q_g K^T         12 K-steps, Q_g and K from shared memory
+//   O_g [128 x 128] += P_g V          8 K-steps, P_g (bf16) from TMEM, in S_g's place
+// A softmax thread owns a query: it keeps the row's maximum m, sum and nothing
+// else; p = exp2(s scale log2 e - m) with the m of the tile before, and only
+// when a score passes m by more than 8 (a factor 256, which fp32 sums and bf16
+// probabilities hold without loss) does the row take a new maximum, is O_g
+// rescaled in TMEM and the tile's p computed again.
+//
+// Roles: two groups of four softmax warps, an MMA warp, a copy warp that
+// feeds a ring of eight 16 KB slots (three a key tile, two a value tile: 1.6
+// tiles in flight).  TMEM: S_0, S_1, O_0, O_1, 128 columns each.
+#include <algorithm>
 
-#include "kda_internal.h"
-#include "latent_common.cuh"
+#include "latent_tc.cuh"
 
 namespace kda {
 
-// Error word of this file's kernels (bit 0: cu_seqlens broke its
-// precondition).
+using namespace tc;
+
+// Error word of this file's kernel (bit 0: a bounded wait gave up, or
+// cu_seqlens broke its precondition).
 __device__ unsigned int g_kda_latent_prefill_error = 0;
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kTile = 64;
+constexpr int kThreads = 320;             // 8 softmax warps, the MMA warp, the copy warp
+constexpr int kHalf = 128;                // queries a half
+constexpr int kTileQ = 2 * kHalf;
+constexpr int kTileK = 128;
+constexpr int kSlots = 8;
+constexpr uint32_t kSlot = 16384;
+constexpr uint32_t SM_Q = 0;              // [2 halves][3 blocks of 64 channels][128 rows x 128 B]
+constexpr uint32_t SM_RING = 6 * 16384;
+constexpr uint32_t SM_MISC = SM_RING + kSlots * kSlot;
+constexpr float kMoveAt = 8.f;            // log2 of the factor a score may pass the maximum by
+constexpr uint32_t TM_S = 0, TM_O = 256;
 
-// A block a (token, head) row: scores of 64 keys, two threads a key, then a
-// value column a thread.
-__global__ void __launch_bounds__(kThreads)
-latent_prefill_kernel(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__ kv,
-                      const __nv_bfloat16 *__restrict__ k_pe, int64_t pe_stride,
-                      const int32_t *__restrict__ cu_q, const int32_t *__restrict__ cu_k, float scale,
-                      int causal, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse, int N, int Tq,
-                      int Tk, int H) {
-    const int t = (int)(blockIdx.x / (unsigned)H), h = (int)(blockIdx.x % (unsigned)H);
-    const int tid = threadIdx.x;
-    const int s = seq_of_token(cu_q, N, t);
-    if (s < 0) return;
-    const int q0 = cu_q[s], nq = cu_q[s + 1] - q0;
-    int k0 = cu_k[s], nk = cu_k[s + 1] - k0;
-    if (k0 < 0 || nk < 0 || (int64_t)k0 + nk > Tk) {
-        if (tid == 0) atomicOr(&g_kda_latent_prefill_error, kErrWait);
-        nk = 0;
+struct Misc {
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], done;
+    uint32_t tmem;
+    int fail;
+    int tiles;                            // work tiles of all sequences (of one head)
+    int warp_sum[kThreads / 32];
+    int ahead[kThreads];                  // work tiles before thread t's sequences
+};
+constexpr uint32_t SM_BYTES = SM_MISC + sizeof(Misc);
+static_assert(SM_BYTES + 1024 <= 232448, "shared memory of an SM");
+
+struct Args {
+    const int32_t *cu_q, *cu_k;
+    int N, Tq, Tk, H;
+    bool causal;
+    float scale_log2;                     // scale * log2 e
+    __nv_bfloat16 *o;
+    float *lse;
+};
+
+__device__ __forceinline__ int queries_of(const Args &a, int b, bool flag) {
+    const int t0 = a.cu_q[b], t1 = a.cu_q[b + 1];
+    const bool bad = t0 < 0 || t1 < t0 || t1 > a.Tq;
+    if (flag) {
+        const int k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
+        if (bad || k0 < 0 || k1 < k0 || k1 > a.Tk) atomicOr(&g_kda_latent_prefill_error, kErrWait);
     }
-    const int seen = causal ? max(0, nk - nq + (t - q0) + 1) : nk;
-    __shared__ float sq[192], sc[kTile];
-    const size_t row = blockIdx.x;
-    for (int i = tid; i < 192; i += kThreads) sq[i] = __bfloat162float(q[row * 192 + i]);
-    float m = -CUDART_INF_F, l = 0.f, acc = 0.f;
-    for (int p0 = 0; p0 < seen; p0 += kTile) {
-        const int n = min(kTile, seen - p0);
-        __syncthreads();
-        const int j = tid >> 1, half = tid & 1;
-        float d = 0.f;
-        if (j < n) {
-            const size_t tok = (size_t)k0 + p0 + j;
-            const __nv_bfloat16 *kr = kv + (tok * H + h) * 256;
-            const __nv_bfloat16 *pr = k_pe + tok * pe_stride;
-            for (int i = half; i < 128; i += 2) d = fmaf(sq[i], __bfloat162float(kr[i]), d);
-            for (int i = half; i < 64; i += 2) d = fmaf(sq[128 + i], __bfloat162float(pr[i]), d);
-        }
-        d += __shfl_xor_sync(0xffffffffu, d, 1);
-        if (half == 0) sc[j] = d * scale;
-        __syncthreads();
-        float mt = m;
-        for (int i = 0; i < n; ++i) mt = fmaxf(mt, sc[i]);
-        const float a = m == -CUDART_INF_F ? 0.f : expf(m - mt);
-        l *= a;
-        acc *= a;
-        m = mt;
-        for (int i = 0; i < n; ++i) {
-            const float p = expf(sc[i] - m);
-            l += p;
-            acc = fmaf(p, __bfloat162float(kv[(((size_t)k0 + p0 + i) * H + h) * 256 + 128 + tid]), acc);
-        }
+    return bad ? 0 : t1 - t0;
+}
+
+struct Work {
+    int h, q0, nq, k0, nk;                // head; first token and tokens of the sequence's queries and keys
+    int i0;                               // first query of the tile
+    int rows[2];                          // queries of each half
+    int n[2];                             // key tiles each half sees any of
+    int first;                            // keys that the sequence's query 0 sees (may be <= 0)
+};
+
+// The r-th work tile of this CTA.  Tiles are listed head by head, in a head
+// from the last queries (which see the most keys) to the first; the CTAs take
+// them in rounds, every other round backwards, so that no stride between
+// them hits the long ones alone.
+__device__ __forceinline__ bool get_work(const Args &a, const Misc *M, int r, Work &w) {
+    const int G = gridDim.x, c = (r & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x;
+    const int64_t id = (int64_t)r * G + c;
+    const int tiles = M->tiles;
+    if (tiles == 0 || id >= (int64_t)tiles * a.H) return false;
+    w.h = (int)(id / tiles);
+    int k = tiles - 1 - (int)(id % tiles);
+    // the thread whose sequences hold tile k, then the sequence
+    int lo = 0, hi = kThreads;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (M->ahead[mid] <= k) lo = mid;
+        else hi = mid;
     }
-    o[row * 128 + tid] = __float2bfloat16_rn(l > 0.f ? acc / l : 0.f);
-    if (lse && tid == 0) lse[row] = l > 0.f ? m + logf(l) : -CUDART_INF_F;
+    k -= M->ahead[lo];
+    const int per = (a.N + kThreads - 1) / kThreads;
+    int b = lo * per, nq = queries_of(a, b, false);
+    while (k >= (nq + kTileQ - 1) / kTileQ) {
+        k -= (nq + kTileQ - 1) / kTileQ;
+        nq = queries_of(a, ++b, false);
+    }
+    w.nq = nq;
+    w.q0 = a.cu_q[b];
+    w.k0 = a.cu_k[b];
+    w.nk = a.cu_k[b + 1] - w.k0;
+    if (w.k0 < 0 || w.nk < 0 || w.k0 > a.Tk - w.nk) w.k0 = w.nk = 0;
+    w.i0 = k * kTileQ;
+    w.first = w.nk - nq + 1;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        w.rows[g] = max(0, min(kHalf, nq - w.i0 - g * kHalf));
+        const int sees = a.causal ? max(0, w.first + w.i0 + g * kHalf + w.rows[g] - 1) : w.nk;
+        w.n[g] = w.rows[g] > 0 ? (sees + kTileK - 1) / kTileK : 0;
+    }
+    return true;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
+        "%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_pe,
+                      const Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Misc *M = reinterpret_cast<Misc *>(sm + SM_MISC);
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+
+    // ---- work tiles ahead of each thread's sequences
+    {
+        const int per = (a.N + kThreads - 1) / kThreads;
+        const int b_lo = min(a.N, t * per), b_hi = min(a.N, b_lo + per);
+        int mine = 0;
+        for (int b = b_lo; b < b_hi; ++b)
+            mine += (queries_of(a, b, blockIdx.x == 0) + kTileQ - 1) / kTileQ;   // CTA 0 flags broken offsets
+        int incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        if (lane == 31) M->warp_sum[warp] = incl;
+        if (t == 0) {
+            M->fail = 0;
+            for (int i = 0; i < kSlots; ++i) { mbar_init(&M->full[i], 1); mbar_init(&M->empty[i], 1); }
+            mbar_init(&M->q_full, 1);
+            mbar_init(&M->q_empty, 1);
+            for (int g = 0; g < 2; ++g) {
+                mbar_init(&M->s_full[g], 1);
+                mbar_init(&M->p_full[g], kHalf);
+                mbar_init(&M->o_full[g], 1);
+            }
+            mbar_init(&M->done, 1);
+            fence_mbar_init();
+        }
+        if (warp == 8) tmem_alloc(&M->tmem, 512);
+        if (warp == 9 && lane == 0) {
+            prefetch_tmap(&map_q);
+            prefetch_tmap(&map_k);
+            prefetch_tmap(&map_v);
+            prefetch_tmap(&map_pe);
+        }
+        __syncthreads();
+        int before = incl - mine, total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += M->warp_sum[w];
+            total += M->warp_sum[w];
+        }
+        M->ahead[t] = before;
+        if (t == 0) M->tiles = total;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = M->tmem;
+    volatile int *fail = &M->fail;
+    Work w;
+
+    if (warp == 9) {
+        // ================================================= copies
+        uint32_t use = 0;                         // ring slots filled so far
+        bool ok = true;
+        uint32_t n_work = 0;
+        auto slot = [&](uint32_t bytes) -> uint8_t * {
+            const uint32_t s = use % kSlots, u = use / kSlots;
+            if (u > 0) ok = ok && warp_wait(&M->empty[s], (u - 1) & 1, fail);
+            if (ok && lane == 0) mbar_arrive_expect_tx(&M->full[s], bytes);
+            ++use;
+            return sm + SM_RING + s * kSlot;
+        };
+        for (int r = 0; ok && get_work(a, M, r, w); ++r) {
+            const int n = max(w.n[0], w.n[1]);
+            if (n == 0) continue;
+            if (n_work > 0) ok = warp_wait(&M->q_empty, (n_work - 1) & 1, fail);
+            if (!ok) break;
+            ++n_work;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&M->q_full, (w.n[0] > 0 ? 3 * kSlot : 0) + (w.n[1] > 0 ? 3 * kSlot : 0));
+                for (int g = 0; g < 2; ++g)
+                    for (int c = 0; w.n[g] > 0 && c < 3; ++c)
+                        tma_load_3d(sm + SM_Q + (3 * g + c) * kSlot, &map_q, &M->q_full, 64 * c, w.h,
+                                    w.q0 + w.i0 + g * kHalf);
+            }
+            for (int i = 0; ok && i < n; ++i) {
+                const int tok = w.k0 + i * kTileK;
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    uint64_t *bar = &M->full[use % kSlots];
+                    uint8_t *dst = slot(kSlot);
+                    if (ok && lane == 0) {
+                        if (c < 2) tma_load_3d(dst, &map_k, bar, 64 * c, w.h, tok);
+                        else tma_load_2d(dst, &map_pe, bar, 0, tok);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint64_t *bar = &M->full[use % kSlots];
+                    uint8_t *dst = slot(kSlot);
+                    if (ok && lane == 0) {
+                        tma_load_3d(dst, &map_v, bar, 128, w.h, tok + 64 * c);
+                        tma_load_3d(dst + 8192, &map_v, bar, 192, w.h, tok + 64 * c);
+                    }
+                }
+            }
+        }
+    } else if (warp == 8) {
+        // ================================================= matrix products
+        constexpr uint32_t id_s = instr_desc(kFmtBF16, 128, 128, 0, 0);
+        constexpr uint32_t id_o = instr_desc(kFmtBF16, 128, 128, 0, 1);
+        const uint64_t q_desc = smem_desc(smem_u32(sm + SM_Q), 16, 1024, kSwizzle128B);
+        const uint64_t k_desc = smem_desc(smem_u32(sm + SM_RING), 16, 1024, kSwizzle128B);
+        const uint64_t v_desc = smem_desc(smem_u32(sm + SM_RING), 8192, 1024, kSwizzle128B);
+        uint32_t u = 0;                           // key tiles so far: slots 5 u ..
+        uint32_t n_work = 0, cnt[2] = {0, 0};     // work tiles, tiles of each half
+        bool ok = true;
+        auto wait_slots = [&](uint32_t first, int count) {
+            for (int c = 0; c < count; ++c)
+                ok = ok && warp_wait(&M->full[(first + c) % kSlots], ((first + c) / kSlots) & 1, fail);
+            tc_fence_after();
+        };
+        auto scores = [&](int g, uint32_t tile) {
+            if (elect_one()) {
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    const uint64_t kd = desc_add(k_desc, ((5 * tile + c) % kSlots) * kSlot);
+                    const uint64_t qd = desc_add(q_desc, (3 * g + c) * kSlot);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16_ss(tmem + TM_S + 128 * g, desc_add(qd, k * 32u), desc_add(kd, k * 32u), id_s,
+                                    c > 0 || k > 0);
+                }
+                mma_commit(&M->s_full[g]);
+            }
+            __syncwarp();
+        };
+        auto free_slots = [&](uint32_t first, int count) {
+            if (elect_one())
+                for (int c = 0; c < count; ++c) mma_commit(&M->empty[(first + c) % kSlots]);
+            __syncwarp();
+        };
+        for (int r = 0; ok && get_work(a, M, r, w); ++r) {
+            const int n = max(w.n[0], w.n[1]);
+            if (n == 0) continue;
+            ok = warp_wait(&M->q_full, n_work & 1, fail);
+            ++n_work;
+            wait_slots(5 * u, 3);
+            if (!ok) break;
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+                if (w.n[g] > 0) scores(g, u);
+            free_slots(5 * u, 3);
+            if (n == 1 && elect_one()) mma_commit(&M->q_empty);
+            __syncwarp();
+            for (int i = 0; ok && i < n; ++i) {
+                wait_slots(5 * (u + i) + 3, 2);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (i < w.n[g]) {
+                        ok = ok && warp_wait(&M->p_full[g], cnt[g] & 1, fail);
+                        ++cnt[g];
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint64_t vd = desc_add(v_desc, ((5 * (u + i) + 3 + (k >> 2)) % kSlots) * kSlot);
+                                mma_bf16_ts(tmem + TM_O + 128 * g, tmem + TM_S + 128 * g + 8 * k,
+                                            desc_add(vd, (k & 3) * 2048u), id_o, i > 0 || k > 0);
+                            }
+                            if (i + 1 == w.n[g]) mma_commit(&M->o_full[g]);
+                        }
+                        __syncwarp();
+                    }
+                    // the next scores of this half follow its product, which reads P in their place
+                    if (g == 0 && i + 1 < n) wait_slots(5 * (u + i + 1), 3);
+                    if (ok && i + 1 < w.n[g]) scores(g, u + i + 1);
+                }
+                if (!ok) break;
+                free_slots(5 * (u + i) + 3, 2);
+                if (i + 1 < n) free_slots(5 * (u + i + 1), 3);
+                if (i + 2 == n && elect_one()) mma_commit(&M->q_empty);
+                __syncwarp();
+            }
+            u += n;
+        }
+        // nothing of this CTA's products is in flight when its TMEM goes
+        if (elect_one()) mma_commit(&M->done);
+        warp_wait(&M->done, 0, fail);
+    } else {
+        // ================================================= softmax, output
+        const int g = warp >> 2, quarter = warp & 3;
+        const int row = quarter * 32 + lane;              // query of the half
+        const uint32_t base = tmem + ((uint32_t)quarter << 21);
+        const uint32_t ts = base + TM_S + 128 * g, to = base + TM_O + 128 * g;
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+        uint32_t cnt = 0, n_out = 0, u = 0;
+        bool ok = true;
+        for (int r = 0; ok && get_work(a, M, r, w); ++r) {
+            const int rows = w.rows[g], n = w.n[g];
+            const int n_all = max(w.n[0], w.n[1]);
+            if (rows == 0) { u += n_all; continue; }
+            const int i_row = w.i0 + g * kHalf + row;     // query of the sequence
+            const int sees = a.causal ? min(w.nk, w.first + i_row) : w.nk;
+            const int all_see = a.causal ? min(w.nk, w.first + w.i0 + g * kHalf + quarter * 32) : w.nk;
+            float neg_m = 0.f, l = 0.f;
+            for (int i = 0; i < n; ++i, ++cnt) {
+                const int lim = sees - i * kTileK;        // columns from here on are masked
+                const bool masked = all_see - i * kTileK < kTileK;
+                ok = wait_or_fail(&M->s_full[g], cnt & 1, fail);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t p[64];
+                float top, sum;
+                // p and their sum from the row's present maximum; the largest exponent
+                auto weights = [&]() {
+                    const float2 nm2 = make_float2(neg_m, neg_m);
+                    float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+                    float tp = -CUDART_INF_F;
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t s[32];
+                        tmem_ld32(ts + 32 * ch, s);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            float2 d = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, nm2);
+                            if (masked) {
+                                if (32 * ch + c >= lim) d.x = -CUDART_INF_F;
+                                if (32 * ch + c + 1 >= lim) d.y = -CUDART_INF_F;
+                            }
+                            tp = fmaxf(tp, fmaxf(d.x, d.y));
+                            const float2 e = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+                            if (c & 2) acc1 = __fadd2_rn(acc1, e);
+                            else acc0 = __fadd2_rn(acc0, e);
+                            p[16 * ch + c / 2] = pack_bf2(e.x, e.y);
+                        }
+                    }
+                    top = tp;
+                    sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                };
+                // a new maximum: the first tile sets it, later ones raise it (and rescale O and
+                // the sum).  A row that sees nothing in the first tile sees nothing at all
+                auto move = [&]() {
+                    float mx = -CUDART_INF_F;
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t s[32];
+                        tmem_ld32(ts + 32 * ch, s);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float d = fmaf(__uint_as_float(s[c]), a.scale_log2, neg_m);
+                            mx = fmaxf(mx, masked && 32 * ch + c >= lim ? -CUDART_INF_F : d);
+                        }
+                    }
+                    float up = i > 0 ? fmaxf(mx, 0.f) : mx == -CUDART_INF_F ? 0.f : mx;
+                    const float now = neg_m - up;
+                    up = neg_m - now;                      // what the rounded maximum really moves by
+                    neg_m = now;
+                    if (i > 0) {                           // the products before this tile are done (s_full)
+                        const float f = ex2_approx(-up);
+                        l *= f;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 128; c0 += 16) {
+                            float ov[16];
+                            tmem_ld16(to + c0, ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) ov[c] *= f;
+                            tmem_st16(to + c0, ov);
+                        }
+                        tmem_wait_st();
+                    }
+                };
+                if (i == 0) move();
+                weights();
+                if (i > 0 && __any_sync(0xffffffffu, top > kMoveAt)) {
+                    move();
+                    weights();
+                }
+                l += sum;
+#pragma unroll
+                for (int c = 0; c < 64; c += 16) tmem_st16u(ts + c, p + c);
+                if ((i + 1) * kTileK > w.nk) {
+                    // value rows behind the sequence's end are its neighbour's: they must not meet
+                    // a zero weight
+                    const uint32_t first = 5 * (u + i) + 3;
+                    for (int c = 0; c < 2; ++c)
+                        ok = ok && wait_or_fail(&M->full[(first + c) % kSlots], ((first + c) / kSlots) & 1, fail);
+                    const int from = w.nk - i * kTileK;
+                    for (int e = row; ok && e < (kTileK - from) * 16; e += kHalf) {
+                        const int rr = from + (e >> 4), ch = e & 15;
+                        *reinterpret_cast<uint4 *>(sm + SM_RING + ((first + (rr >> 6)) % kSlots) * kSlot +
+                                                   (ch >> 3) * 8192u + (rr & 63) * 128u + (ch & 7) * 16u) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&M->p_full[g]);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            }
+            u += n_all;
+            if (!ok) break;
+            // ---- output
+            if (n > 0) {
+                ok = wait_or_fail(&M->o_full[g], n_out & 1, fail);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                ++n_out;
+                tc_fence_after();
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const size_t out = ((size_t)w.q0 + i_row) * a.H + w.h;
+#pragma unroll
+            for (int c0 = 0; c0 < 128; c0 += 32) {
+                uint32_t ov[32];
+                if (n > 0) {
+                    tmem_ld32(to + c0, ov);
+                    tmem_wait_ld();
+                }
+                if (row < rows) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(a.o + out * 128 + c0);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8) {
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = n > 0 ? __uint_as_float(ov[c + e]) * inv : 0.f;
+                        dst[c / 8] = l > 0.f ? pack_bf8(x) : make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            if (a.lse && row < rows)
+                a.lse[out] = l > 0.f ? (log2f(l) - neg_m) * 0.6931471805599453f : -CUDART_INF_F;
+            tc_fence_before();
+        }
+        if (!ok && lane == 0) atomicOr(&g_kda_latent_prefill_error, kErrWait);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
@@ -82,10 +501,24 @@ cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_p
                                   const int32_t *cu_q, const int32_t *cu_k, float scale, bool causal,
                                   void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
                                   cudaStream_t stream) {
-    latent_prefill_kernel<<<(unsigned)(Tq * H), kThreads, 0, stream>>>(
-        static_cast<const __nv_bfloat16 *>(q), static_cast<const __nv_bfloat16 *>(kv),
-        static_cast<const __nv_bfloat16 *>(k_pe), pe_stride, cu_q, cu_k, scale, causal ? 1 : 0,
-        static_cast<__nv_bfloat16 *>(o), lse, N, (int)Tq, (int)Tk, H);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(SM_BYTES + 1024));
+    if (e != cudaSuccess) return e;
+    CUtensorMap mq, mk, mv, mp;
+    if (!make_map_heads(&mq, q, 192, H, Tq, kHalf)) return cudaErrorInvalidValue;
+    mk = mv = mp = mq;                    // without keys none of the others is read through
+    if (Tk > 0 && (!make_map_heads(&mk, kv, 256, H, Tk, kTileK) || !make_map_heads(&mv, kv, 256, H, Tk, 64) ||
+                   !make_map_rows(&mp, k_pe, 64, Tk, pe_stride, kTileK)))
+        return cudaErrorInvalidValue;
+    const Args a{cu_q, cu_k, N, (int)Tq, (int)Tk, H, causal, scale * 1.4426950408889634f,
+                 static_cast<__nv_bfloat16 *>(o), lse};
+    const int64_t most = (Tq / kTileQ + N) * H;   // work tiles at most
+    latent_prefill_kernel<<<(unsigned)std::min<int64_t>(sms, most), kThreads, SM_BYTES + 1024, stream>>>(mq, mk, mv,
+                                                                                                    mp, a);
     return cudaGetLastError();
 }
 
