@@ -33,8 +33,8 @@ S [N, H, 128, 128] fp32; q/k/v bf16 or fp32, g/beta fp32.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -513,23 +513,45 @@ LATENT_ROW = LATENT + LATENT_PE
 LATENT_SCALE = (DK + LATENT_PE) ** -0.5   # 1/sqrt(expanded key width)
 
 
-def _on(device: torch.device):
-    """The device's guard where it is not the current one (a launch goes to
-    the current device)."""
-    if device.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# The calls below run once a layer and step with kernels of a few
+# microseconds, so their own checks cost less than the others': one chain of
+# cheap comparisons a tensor, and _check for the error's words.
+def _need(name, t, dtype, shape, dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == dev and t.is_contiguous()):
+        _check(name, t, dtype, shape, dev)
+    return t.data_ptr()
 
 
-def _check_cache(cache, block_table, N, dev):
+def _need_cache(cache, block_table, N, dev):
     if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
         raise ValueError("cache must be a [P, page, %d] tensor" % LATENT_ROW)
-    _check("cache", cache, torch.bfloat16, (cache.shape[0], cache.shape[1], LATENT_ROW), dev)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a [N, max_pages] tensor")
-    _check("block_table", block_table, torch.int32, (N, block_table.shape[1]), dev)
+    P, page, _ = cache.shape
+    pages = block_table.shape[1]
+    return (_need("cache", cache, torch.bfloat16, (P, page, LATENT_ROW), dev),
+            _need("block_table", block_table, torch.int32, (N, pages), dev), P, page, pages)
+
+
+def _elsewhere(t) -> bool:
+    """Whether the tensor's device is not the current one (a launch goes to
+    the current device)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("inputs must be CUDA tensors")
+    return t.get_device() != torch.cuda.current_device()
+
+
+def _raw_stream(dev, stream):
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _empty(shape, dtype, dev, stream):
+    """Memory of the stream that uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def latent_append(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
@@ -543,20 +565,18 @@ def latent_append(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     [N + 1] int32 (None: one new token a sequence).  With norm_w [512] fp32
     the latent part is RMS-normalised.  Returns cache.
     """
+    if _elsewhere(x):
+        with torch.cuda.device(x.device):
+            return latent_append(x, cache, block_table, seq_lens, cu_seqlens, norm_w, eps, stream)
     dev = x.device
     T, N = x.shape[0], seq_lens.numel()
-    with _on(dev):
-        _check("x", x, torch.bfloat16, (T, LATENT_ROW), dev)
-        _check_cache(cache, block_table, N, dev)
-        _check("seq_lens", seq_lens, torch.int32, (N,), dev)
-        if cu_seqlens is not None:
-            _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
-        if norm_w is not None:
-            _check("norm_w", norm_w, torch.float32, (LATENT,), dev)
-        rc = lib().kda_latent_append(_p(x), _p(cache), _p(block_table), _p(seq_lens),
-                                     _p(cu_seqlens), _p(norm_w), float(eps), N, T, cache.shape[0],
-                                     cache.shape[1], block_table.shape[1], LATENT, LATENT_PE,
-                                     _stream(dev, stream))
+    c, table, P, page, pages = _need_cache(cache, block_table, N, dev)
+    rc = lib().kda_latent_append(
+        _need("x", x, torch.bfloat16, (T, LATENT_ROW), dev), c, table,
+        _need("seq_lens", seq_lens, torch.int32, (N,), dev),
+        None if cu_seqlens is None else _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev),
+        None if norm_w is None else _need("norm_w", norm_w, torch.float32, (LATENT,), dev),
+        eps, N, T, P, page, pages, LATENT, LATENT_PE, _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_append")
     return cache
@@ -568,26 +588,27 @@ def latent_gather(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: to
     """Read every sequence's first rows back, packed by cu_seqlens
     (``kda_latent_gather``).  total: the packed length cu_seqlens[N] (where
     ``out`` [total, 576] bf16 is not given).  Returns out."""
+    if _elsewhere(cache):
+        with torch.cuda.device(cache.device):
+            return latent_gather(cache, block_table, cu_seqlens, total, out, stream)
     dev = cache.device
     N = cu_seqlens.numel() - 1
-    with _on(dev):
-        if out is None:
-            if total is None:
-                raise ValueError("give the packed length (total) or the output (out)")
-            with torch.cuda.stream(stream):
-                out = torch.empty((total, LATENT_ROW), dtype=torch.bfloat16, device=dev)
-        T = out.shape[0]
-        _check_cache(cache, block_table, N, dev)
-        _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
-        _check("out", out, torch.bfloat16, (T, LATENT_ROW), dev)
-        rc = lib().kda_latent_gather(_p(cache), _p(block_table), _p(cu_seqlens), _p(out), N, T,
-                                     cache.shape[0], cache.shape[1], block_table.shape[1], LATENT,
-                                     LATENT_PE, _stream(dev, stream))
+    c, table, P, page, pages = _need_cache(cache, block_table, N, dev)
+    if out is None:
+        if total is None:
+            raise ValueError("give the packed length (total) or the output (out)")
+        out = _empty((total, LATENT_ROW), torch.bfloat16, dev, stream)
+    T = out.shape[0]
+    rc = lib().kda_latent_gather(
+        c, table, _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev),
+        _need("out", out, torch.bfloat16, (T, LATENT_ROW), dev), N, T, P, page, pages, LATENT, LATENT_PE,
+        _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_gather")
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def latent_decode_workspace_bytes(N: int, T: int, H: int) -> int:
     """Bytes of workspace of ``latent_decode`` (``kda_latent_decode_workspace_bytes``)."""
     return int(lib().kda_latent_decode_workspace_bytes(int(N), int(T), int(H), LATENT, LATENT_PE))
@@ -608,33 +629,30 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     (``latent_decode_workspace_bytes``) comes from torch's allocator unless
     one is given.
     """
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return latent_decode(q, cache, block_table, seq_lens, cu_seqlens, scale, o, lse, workspace, stream)
     dev = q.device
     T, H, N = q.shape[0], q.shape[1], seq_lens.numel()
-    with _on(dev):
-        _check("q", q, torch.bfloat16, (T, H, LATENT_ROW), dev)
-        _check_cache(cache, block_table, N, dev)
-        _check("seq_lens", seq_lens, torch.int32, (N,), dev)
-        if cu_seqlens is not None:
-            _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
-        need = latent_decode_workspace_bytes(N, T, H)
-        with torch.cuda.stream(stream):       # memory of the stream that uses it
-            if o is None:
-                o = torch.empty((T, H, LATENT), dtype=torch.bfloat16, device=dev)
-            if lse is None:
-                lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-            if workspace is None and need > 0:
-                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        _check("o", o, torch.bfloat16, (T, H, LATENT), dev)
-        _check("lse", lse, torch.float32, (T, H), dev)
-        nbytes = 0
-        if workspace is not None:
-            if workspace.device != dev or not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-            nbytes = workspace.numel() * workspace.element_size()
-        rc = lib().kda_latent_decode(_p(q), _p(cache), _p(block_table), _p(seq_lens),
-                                     _p(cu_seqlens), float(scale), _p(o), _p(lse), N, T, H,
-                                     cache.shape[0], cache.shape[1], block_table.shape[1], LATENT,
-                                     LATENT_PE, _p(workspace), nbytes, _stream(dev, stream))
+    c, table, P, page, pages = _need_cache(cache, block_table, N, dev)
+    if o is None:
+        o = _empty((T, H, LATENT), torch.bfloat16, dev, stream)
+    if lse is None:
+        lse = _empty((T, H), torch.float32, dev, stream)
+    if workspace is None:
+        nbytes = latent_decode_workspace_bytes(N, T, H)
+        workspace = _empty((nbytes,), torch.uint8, dev, stream) if nbytes else None
+    else:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+        nbytes = workspace.numel() * workspace.element_size()
+    rc = lib().kda_latent_decode(
+        _need("q", q, torch.bfloat16, (T, H, LATENT_ROW), dev), c, table,
+        _need("seq_lens", seq_lens, torch.int32, (N,), dev),
+        None if cu_seqlens is None else _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev),
+        scale, _need("o", o, torch.bfloat16, (T, H, LATENT), dev), _need("lse", lse, torch.float32, (T, H), dev),
+        N, T, H, P, page, pages, LATENT, LATENT_PE,
+        None if workspace is None else workspace.data_ptr(), nbytes, _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_decode")
     return o, lse
@@ -655,31 +673,29 @@ def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seq
     sequence are its last tokens.  Returns (o [Tq, H, 128] bf16, lse [Tq, H]
     fp32).
     """
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return latent_prefill(q, kv, k_pe, cu_seqlens, cu_seqlens_k, scale, causal, o, lse, stream)
     dev = q.device
     Tq, H, N, Tk = q.shape[0], q.shape[1], cu_seqlens.numel() - 1, kv.shape[0]
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens
-    with _on(dev):
-        _check("q", q, torch.bfloat16, (Tq, H, DK + LATENT_PE), dev)
-        _check("kv", kv, torch.bfloat16, (Tk, H, DK + DV), dev)
-        if (k_pe.device != dev or k_pe.dtype != torch.bfloat16 or tuple(k_pe.shape) != (Tk, LATENT_PE)
-                or (Tk > 0 and k_pe.stride(1) != 1)):
-            raise ValueError("k_pe must be [%d, %d] bfloat16 on %s with dense rows" % (Tk, LATENT_PE, dev))
-        # the stride of a dimension of one row means nothing
-        pe_stride = k_pe.stride(0) if Tk > 1 else LATENT_PE
-        _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
-        _check("cu_seqlens_k", cu_seqlens_k, torch.int32, (N + 1,), dev)
-        with torch.cuda.stream(stream):
-            if o is None:
-                o = torch.empty((Tq, H, DV), dtype=torch.bfloat16, device=dev)
-            if lse is None:
-                lse = torch.empty((Tq, H), dtype=torch.float32, device=dev)
-        _check("o", o, torch.bfloat16, (Tq, H, DV), dev)
-        _check("lse", lse, torch.float32, (Tq, H), dev)
-        rc = lib().kda_latent_prefill(_p(q), _p(kv), _p(k_pe), pe_stride, _p(cu_seqlens),
-                                      _p(cu_seqlens_k), float(scale), int(bool(causal)), _p(o),
-                                      _p(lse), N, Tq, Tk, H, DK, LATENT_PE, DV,
-                                      _stream(dev, stream))
+    if not (isinstance(k_pe, torch.Tensor) and k_pe.device == dev and k_pe.dtype is torch.bfloat16
+            and k_pe.shape == (Tk, LATENT_PE) and (Tk == 0 or k_pe.stride(1) == 1)):
+        raise ValueError("k_pe must be [%d, %d] bfloat16 on %s with dense rows" % (Tk, LATENT_PE, dev))
+    # the stride of a dimension of one row means nothing
+    pe_stride = k_pe.stride(0) if Tk > 1 else LATENT_PE
+    if o is None:
+        o = _empty((Tq, H, DV), torch.bfloat16, dev, stream)
+    if lse is None:
+        lse = _empty((Tq, H), torch.float32, dev, stream)
+    rc = lib().kda_latent_prefill(
+        _need("q", q, torch.bfloat16, (Tq, H, DK + LATENT_PE), dev),
+        _need("kv", kv, torch.bfloat16, (Tk, H, DK + DV), dev), k_pe.data_ptr(), pe_stride,
+        _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev),
+        _need("cu_seqlens_k", cu_seqlens_k, torch.int32, (N + 1,), dev), scale, 1 if causal else 0,
+        _need("o", o, torch.bfloat16, (Tq, H, DV), dev), _need("lse", lse, torch.float32, (Tq, H), dev),
+        N, Tq, Tk, H, DK, LATENT_PE, DV, _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_prefill")
     return o, lse

@@ -727,11 +727,13 @@ constexpr size_t kSplitBytes = 4096, kLseBytes = 2 * kMaxCtas * 64 * sizeof(floa
 static_assert(kSplitBytes >= kMaxCtas * sizeof(Split), "records of the split row tiles");
 
 template <int NR>
-cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const void *cache, const Args &a, int G,
+cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const void *cache, const Args &a,
                    cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(Cfg<NR>::BYTES + 1024));
+    static KernelSetup setup;
+    int sms = 0;
+    cudaError_t e = setup.get(reinterpret_cast<const void *>(latent_decode_kernel<NR>), Cfg<NR>::BYTES + 1024, &sms);
     if (e != cudaSuccess) return e;
+    const int G = std::min(sms, kMaxCtas);
     latent_decode_kernel<NR><<<G, kThreads, Cfg<NR>::BYTES + 1024, stream>>>(
         mx, mc, static_cast<const uint8_t *>(cache), a);
     e = cudaGetLastError();
@@ -752,10 +754,6 @@ cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t
                                  float *lse, int N, int64_t T, int H, int64_t P, int page,
                                  int max_pages, void *ws, cudaStream_t stream) {
     const int NR = rows_of_tile(N, T, H);
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
     CUtensorMap mx, mc;
     if (!make_map_rows(&mx, q, kLatentRow, T * H, kLatentRow, (uint32_t)NR) ||
         !make_map_rows(&mc, cache, kLatentRow, P * page, kLatentRow, (uint32_t)std::min(page, kTile)))
@@ -774,12 +772,11 @@ cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t
     a.split = reinterpret_cast<Split *>(w);
     a.ws_lse = reinterpret_cast<float *>(w + kSplitBytes);
     a.ws_o = reinterpret_cast<float *>(w + kSplitBytes + kLseBytes);
-    const int G = std::min(sms, kMaxCtas);
     switch (NR) {
-        case 16: return launch<16>(mx, mc, cache, a, G, stream);
-        case 32: return launch<32>(mx, mc, cache, a, G, stream);
-        case 48: return launch<48>(mx, mc, cache, a, G, stream);
-        default: return launch<64>(mx, mc, cache, a, G, stream);
+        case 16: return launch<16>(mx, mc, cache, a, stream);
+        case 32: return launch<32>(mx, mc, cache, a, stream);
+        case 48: return launch<48>(mx, mc, cache, a, stream);
+        default: return launch<64>(mx, mc, cache, a, stream);
     }
 }
 

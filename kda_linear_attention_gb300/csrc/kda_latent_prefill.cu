@@ -501,12 +501,9 @@ cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_p
                                   const int32_t *cu_q, const int32_t *cu_k, float scale, bool causal,
                                   void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
                                   cudaStream_t stream) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(SM_BYTES + 1024));
+    static KernelSetup setup;
+    int sms = 0;
+    const cudaError_t e = setup.get(reinterpret_cast<const void *>(latent_prefill_kernel), SM_BYTES + 1024, &sms);
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv, mp;
     if (!make_map_heads(&mq, q, 192, H, Tq, kHalf)) return cudaErrorInvalidValue;

@@ -122,5 +122,46 @@ inline bool make_map_heads(CUtensorMap *m, const void *base, int64_t cols, int64
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// ---- host: a kernel's shared-memory limit and the device's SM count
+// Both cost a driver call of a microsecond or so; they hold for a device's
+// context, so they are asked for and set once in each (`id` of cuCtxGetId
+// tells a context made by a device reset from the one before it).
+struct KernelSetup {
+    static constexpr int kDevices = 64;
+    std::mutex mu;
+    unsigned long long ctx[kDevices] = {};
+    int sms[kDevices] = {};
+
+    cudaError_t get(const void *kernel, int smem_bytes, int *n_sms) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lk(mu);
+        unsigned long long id = context_id();
+        if (id == 0 || id != ctx[dev]) {
+            e = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+            if (e != cudaSuccess) return e;
+            ctx[dev] = context_id();
+        }
+        *n_sms = sms[dev];
+        return cudaSuccess;
+    }
+    static unsigned long long context_id() {
+        static PFN_cuCtxGetId_v12000 fn = [] {
+            cudaDriverEntryPointQueryResult q;
+            void *p = nullptr;
+            if (cudaGetDriverEntryPointByVersion("cuCtxGetId", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+                q != cudaDriverEntryPointSuccess)
+                p = nullptr;
+            return reinterpret_cast<PFN_cuCtxGetId_v12000>(p);
+        }();
+        unsigned long long id = 0;
+        return fn && fn(nullptr, &id) == CUDA_SUCCESS ? id : 0;
+    }
+};
+
 }  // namespace tc
 }  // namespace kda
