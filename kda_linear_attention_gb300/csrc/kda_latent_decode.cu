@@ -262,7 +262,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             mbar_init(&M->x_full, 1);
             mbar_init(&M->x_empty, 1);
             mbar_init(&M->s_full, 1);
-            mbar_init(&M->p_full, kSoftThreads);
+            mbar_init(&M->p_full, kSoftWarps);
             mbar_init(&M->o_full, 1);
             mbar_init(&M->done, 1);
             fence_mbar_init();
@@ -376,60 +376,65 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         bool ok = true;
         constexpr uint32_t id_s = instr_desc(kFmtBF16, 128, NR, 0, 0);
         constexpr uint32_t id_o = instr_desc(kFmtBF16, 128, NR, 1, 1);
-        const uint64_t x_desc = smem_desc(smem_u32(sm + F::X), 16, 1024, kSwizzle128B);
-        const uint64_t k_desc = smem_desc(smem_u32(sm + F::PAIR), 16, 1024, kSwizzle128B);
-        const uint64_t v_desc = smem_desc(smem_u32(sm + F::PAIR), 16384, 1024, kSwizzle128B);
-        const uint64_t r_desc = smem_desc(smem_u32(sm + F::ROPE), 16, 1024, kSwizzle128B);
+        const Operand x_op = operand(sm + F::X, 16, 1024), k_op = operand(sm + F::PAIR, 16, 1024);
+        const Operand v_op = operand(sm + F::PAIR, 16384, 1024), r_op = operand(sm + F::ROPE, 16, 1024);
+        const uint32_t full_p = smem_u32(M->full_p), empty_p = smem_u32(M->empty_p);
+        const uint32_t full_r = smem_u32(M->full_r), empty_r = smem_u32(M->empty_r);
+        const uint32_t s_full = smem_u32(&M->s_full), p_full = smem_u32(&M->p_full);
+        uint32_t slot = 0, lap = 0;               // next pair slot, its phase
         while (ok && walk.next(a, it)) {
             if (it.n == 0) continue;
-            ok = warp_wait(&M->x_full, n_item & 1, fail);
-            for (int i = 0; ok && i < it.n; ++i, ++n_tile) {
+            ok &= wait_or_fail(&M->x_full, n_item & 1, fail);
+            for (int i = 0; i < it.n; ++i, ++n_tile) {
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 // S^T: channels 0..511 from the pairs, 512..575 from the shared part
+                uint32_t at[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t u = 4 * n_tile + j, slot = u % F::NP;
-                    ok = ok && warp_wait(&M->full_p[slot], (u / F::NP) & 1, fail);
+                    at[j] = slot;
+                    ok &= wait_or_fail(full_p + 8 * slot, lap, fail);
+                    if (++slot == F::NP) { slot = 0; lap ^= 1; }
                     tc_fence_after();
-                    const uint64_t kd = desc_add(k_desc, slot * kPair);
-                    if (ok && elect_one()) {
+                    const Operand k = k_op + at[j] * kPair;
+                    if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_bf16_ss(tmem + TM_S, desc_add(kd, (k >> 2) * 16384u + (k & 3) * 32u),
-                                        desc_add(x_desc, (2 * j + (k >> 2)) * NR * 128u + (k & 3) * 32u), id_s,
-                                        j > 0 || k > 0);
+                        for (int e = 0; e < 8; ++e) {
+                            const Operand ke = k + ((e >> 2) * 16384u + (e & 3) * 32u);
+                            const Operand xe = x_op + ((2 * j + (e >> 2)) * NR * 128u + (e & 3) * 32u);
+                            if (j == 0 && e == 0) mma_ss<false>(tmem + TM_S, ke, xe, id_s, false);
+                            else mma_ss<true>(tmem + TM_S, ke, xe, id_s);
+                        }
                     }
                     __syncwarp();
                 }
                 const uint32_t rslot = n_tile % F::NQ;
-                const uint64_t rd = desc_add(r_desc, rslot * kRope);
-                ok = ok && warp_wait(&M->full_r[rslot], (n_tile / F::NQ) & 1, fail);
-                if (!ok) break;
+                const Operand rope = r_op + rslot * kRope;
+                ok &= wait_or_fail(full_r + 8 * rslot, (n_tile / F::NQ) & 1, fail);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16_ss(tmem + TM_S, desc_add(rd, k * 32u), desc_add(x_desc, 8 * NR * 128u + k * 32u), id_s, 1);
-                    mma_commit(&M->s_full);
+                    for (int e = 0; e < 4; ++e)
+                        mma_ss<true>(tmem + TM_S, rope + e * 32u, x_op + (8 * NR * 128u + e * 32u), id_s);
+                    commit(s_full);
                     if (i + 1 == it.n) mma_commit(&M->x_empty);
                 }
                 __syncwarp();
                 // O^T += c^T P^T, a slot released as soon as its block is done (P's rows are one
                 // 128-byte atom wide, so the shared part's descriptor serves it, 16 rows a step)
-                ok = warp_wait(&M->p_full, n_tile & 1, fail);
-                if (!ok) break;
+                ok &= wait_or_fail(p_full, n_tile & 1, fail);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint32_t slot = (4 * n_tile + j) % F::NP;
-                        const uint64_t vd = desc_add(v_desc, slot * kPair);
+                        const Operand v = v_op + at[j] * kPair;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_bf16_ss(tmem + TM_O + 64 * j, desc_add(vd, k * 2048u), desc_add(rd, k * 2048u), id_o,
-                                        i > 0 || k > 0);
-                        mma_commit(&M->empty_p[slot]);
+                        for (int e = 0; e < 8; ++e) {
+                            if (e == 0) mma_ss<false>(tmem + TM_O + 64 * j, v, rope, id_o, i > 0);
+                            else mma_ss<true>(tmem + TM_O + 64 * j, v + e * 2048u, rope + e * 2048u, id_o);
+                        }
+                        commit(empty_p + 8 * at[j]);
                     }
-                    mma_commit(&M->empty_r[rslot]);
+                    commit(empty_r + 8 * rslot);
                     if (i + 1 == it.n) mma_commit(&M->o_full);
                 }
                 __syncwarp();
@@ -465,7 +470,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             const int all_see = min(it.len, it.first_tok + it.row_in_seq / a.H);
             for (int i = 0; i < it.n; ++i, ++n_tile) {
                 const int p0 = (it.tile + i) * kTile;
-                ok = wait_or_fail(&M->s_full, n_tile & 1, fail);
+                ok = warp_wait(&M->s_full, n_tile & 1, fail);
                 tc_fence_after();
                 float s[NC];
                 tmem_ldn<NC>(tmem + lane_base + TM_S + col0, s);
@@ -553,14 +558,14 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(&M->p_full);
+                warp_arrive(&M->p_full);
             }
             if (!ok) break;
             // ---- the row tile's (piece's) output
             const bool whole = it.head && it.tail;
             const int slot = 2 * cta + (it.head ? 1 : 0);      // a piece that starts here goes on behind
             if (it.n > 0) {
-                ok = wait_or_fail(&M->o_full, n_item & 1, fail);
+                ok = warp_wait(&M->o_full, n_item & 1, fail);
                 if (bar_any(bar, 128, !ok)) { ok = false; break; }
                 tc_fence_after();
                 ++n_item;

@@ -49,7 +49,7 @@ constexpr float kMoveAt = 8.f;            // log2 of the factor a score may pass
 constexpr uint32_t TM_S = 0, TM_O = 256;
 
 struct Misc {
-    uint64_t full[kSlots], empty[kSlots];
+    uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];   // by key tile, even and odd
     uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], done;
     uint32_t tmem;
     int fail;
@@ -174,12 +174,17 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         if (lane == 31) M->warp_sum[warp] = incl;
         if (t == 0) {
             M->fail = 0;
-            for (int i = 0; i < kSlots; ++i) { mbar_init(&M->full[i], 1); mbar_init(&M->empty[i], 1); }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&M->k_full[i], 1);
+                mbar_init(&M->v_full[i], 1);
+                mbar_init(&M->k_empty[i], 1);
+                mbar_init(&M->v_empty[i], 1);
+            }
             mbar_init(&M->q_full, 1);
             mbar_init(&M->q_empty, 1);
             for (int g = 0; g < 2; ++g) {
                 mbar_init(&M->s_full[g], 1);
-                mbar_init(&M->p_full[g], kHalf);
+                mbar_init(&M->p_full[g], 4);      // warps of a group
                 mbar_init(&M->o_full[g], 1);
             }
             mbar_init(&M->done, 1);
@@ -210,16 +215,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
 
     if (warp == 9) {
         // ================================================= copies
-        uint32_t use = 0;                         // ring slots filled so far
+        // Key tile u fills ring slots 5 u .. 5 u + 2, its value tile 5 u + 3 and 5 u + 4 (modulo 8).
+        // The key slots were last the third of key tile u - 2 and both of its value tile, the value
+        // slots the first two of key tile u - 1; the MMA warp releases in the order of u.
+        uint32_t u = 0;
         bool ok = true;
         uint32_t n_work = 0;
-        auto slot = [&](uint32_t bytes) -> uint8_t * {
-            const uint32_t s = use % kSlots, u = use / kSlots;
-            if (u > 0) ok = ok && warp_wait(&M->empty[s], (u - 1) & 1, fail);
-            if (ok && lane == 0) mbar_arrive_expect_tx(&M->full[s], bytes);
-            ++use;
-            return sm + SM_RING + s * kSlot;
-        };
         for (int r = 0; ok && get_work(a, M, r, w); ++r) {
             const int n = max(w.n[0], w.n[1]);
             if (n == 0) continue;
@@ -233,107 +234,113 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                         tma_load_3d(sm + SM_Q + (3 * g + c) * kSlot, &map_q, &M->q_full, 64 * c, w.h,
                                     w.q0 + w.i0 + g * kHalf);
             }
-            for (int i = 0; ok && i < n; ++i) {
+            for (int i = 0; i < n; ++i, ++u) {
                 const int tok = w.k0 + i * kTileK;
+                auto slot = [&](int c) { return sm + SM_RING + ((5 * u + c) % kSlots) * kSlot; };
+                if (u >= 2) ok = warp_wait(&M->v_empty[u & 1], ((u >> 1) - 1) & 1, fail);
+                if (!ok) break;
+                if (lane == 0) {
+                    uint64_t *bar = &M->k_full[u & 1];
+                    mbar_arrive_expect_tx(bar, 3 * kSlot);
+                    tma_load_3d(slot(0), &map_k, bar, 0, w.h, tok);
+                    tma_load_3d(slot(1), &map_k, bar, 64, w.h, tok);
+                    tma_load_2d(slot(2), &map_pe, bar, 0, tok);
+                }
+                __syncwarp();
+                if (u >= 1) ok = warp_wait(&M->k_empty[(u - 1) & 1], ((u - 1) >> 1) & 1, fail);
+                if (!ok) break;
+                if (lane == 0) {
+                    uint64_t *bar = &M->v_full[u & 1];
+                    mbar_arrive_expect_tx(bar, 2 * kSlot);
 #pragma unroll
-                for (int c = 0; c < 3; ++c) {
-                    uint64_t *bar = &M->full[use % kSlots];
-                    uint8_t *dst = slot(kSlot);
-                    if (ok && lane == 0) {
-                        if (c < 2) tma_load_3d(dst, &map_k, bar, 64 * c, w.h, tok);
-                        else tma_load_2d(dst, &map_pe, bar, 0, tok);
+                    for (int c = 0; c < 2; ++c) {
+                        tma_load_3d(slot(3 + c), &map_v, bar, 128, w.h, tok + 64 * c);
+                        tma_load_3d(slot(3 + c) + 8192, &map_v, bar, 192, w.h, tok + 64 * c);
                     }
                 }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint64_t *bar = &M->full[use % kSlots];
-                    uint8_t *dst = slot(kSlot);
-                    if (ok && lane == 0) {
-                        tma_load_3d(dst, &map_v, bar, 128, w.h, tok + 64 * c);
-                        tma_load_3d(dst + 8192, &map_v, bar, 192, w.h, tok + 64 * c);
-                    }
-                }
+                __syncwarp();
             }
         }
     } else if (warp == 8) {
         // ================================================= matrix products
+        // The whole warp walks and waits, one lane issues.
         constexpr uint32_t id_s = instr_desc(kFmtBF16, 128, 128, 0, 0);
         constexpr uint32_t id_o = instr_desc(kFmtBF16, 128, 128, 0, 1);
-        const uint64_t q_desc = smem_desc(smem_u32(sm + SM_Q), 16, 1024, kSwizzle128B);
-        const uint64_t k_desc = smem_desc(smem_u32(sm + SM_RING), 16, 1024, kSwizzle128B);
-        const uint64_t v_desc = smem_desc(smem_u32(sm + SM_RING), 8192, 1024, kSwizzle128B);
-        uint32_t u = 0;                           // key tiles so far: slots 5 u ..
-        uint32_t n_work = 0, cnt[2] = {0, 0};     // work tiles, tiles of each half
+        const Operand q_op = operand(sm + SM_Q, 16, 1024), k_op = operand(sm + SM_RING, 16, 1024);
+        const Operand v_op = operand(sm + SM_RING, 8192, 1024);
+        const uint32_t k_full = smem_u32(M->k_full), v_full = smem_u32(M->v_full);
+        const uint32_t k_empty = smem_u32(M->k_empty), v_empty = smem_u32(M->v_empty);
+        const uint32_t s_full = smem_u32(M->s_full), p_full = smem_u32(M->p_full), o_full = smem_u32(M->o_full);
+        const uint32_t q_empty = smem_u32(&M->q_empty);
+        uint32_t u = 0, n_work = 0, cnt0 = 0, cnt1 = 0;   // key tiles, work tiles, tiles of each half
         bool ok = true;
-        auto wait_slots = [&](uint32_t first, int count) {
-            for (int c = 0; c < count; ++c)
-                ok = ok && warp_wait(&M->full[(first + c) % kSlots], ((first + c) / kSlots) & 1, fail);
-            tc_fence_after();
-        };
-        auto scores = [&](int g, uint32_t tile) {
-            if (elect_one()) {
+        auto scores = [&](int g, uint32_t tile) {         // one lane
 #pragma unroll
-                for (int c = 0; c < 3; ++c) {
-                    const uint64_t kd = desc_add(k_desc, ((5 * tile + c) % kSlots) * kSlot);
-                    const uint64_t qd = desc_add(q_desc, (3 * g + c) * kSlot);
+            for (int c = 0; c < 3; ++c) {
+                const Operand k = k_op + ((5 * tile + c) % kSlots) * kSlot, q = q_op + (3 * g + c) * kSlot;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16_ss(tmem + TM_S + 128 * g, desc_add(qd, k * 32u), desc_add(kd, k * 32u), id_s,
-                                    c > 0 || k > 0);
+                for (int e = 0; e < 4; ++e) {
+                    if (c == 0 && e == 0) mma_ss<false>(tmem + TM_S + 128 * g, q, k, id_s, false);
+                    else mma_ss<true>(tmem + TM_S + 128 * g, q + e * 32u, k + e * 32u, id_s);
                 }
-                mma_commit(&M->s_full[g]);
             }
-            __syncwarp();
+            commit(s_full + 8 * g);
         };
-        auto free_slots = [&](uint32_t first, int count) {
-            if (elect_one())
-                for (int c = 0; c < count; ++c) mma_commit(&M->empty[(first + c) % kSlots]);
-            __syncwarp();
+        auto product = [&](int g, uint32_t tile, bool acc) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const Operand v = v_op + ((5 * tile + 3 + c) % kSlots) * kSlot;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mma_ts(tmem + TM_O + 128 * g, tmem + TM_S + 128 * g + 32 * c + 8 * e, v + e * 2048u, id_o,
+                           acc || c > 0 || e > 0);
+            }
         };
         for (int r = 0; ok && get_work(a, M, r, w); ++r) {
-            const int n = max(w.n[0], w.n[1]);
+            const int n0 = w.n[0], n1 = w.n[1], n = max(n0, n1);
             if (n == 0) continue;
-            ok = warp_wait(&M->q_full, n_work & 1, fail);
+            ok &= wait_or_fail(&M->q_full, n_work & 1, fail);
             ++n_work;
-            wait_slots(5 * u, 3);
-            if (!ok) break;
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-                if (w.n[g] > 0) scores(g, u);
-            free_slots(5 * u, 3);
-            if (n == 1 && elect_one()) mma_commit(&M->q_empty);
+            ok &= wait_or_fail(k_full + 8 * (u & 1), (u >> 1) & 1, fail);
+            tc_fence_after();
+            if (elect_one()) {
+                if (n0 > 0) scores(0, u);
+                if (n1 > 0) scores(1, u);
+                commit(k_empty + 8 * (u & 1));
+                if (n == 1) commit(q_empty);
+            }
             __syncwarp();
-            for (int i = 0; ok && i < n; ++i) {
-                wait_slots(5 * (u + i) + 3, 2);
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    if (i < w.n[g]) {
-                        ok = ok && warp_wait(&M->p_full[g], cnt[g] & 1, fail);
-                        ++cnt[g];
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const uint64_t vd = desc_add(v_desc, ((5 * (u + i) + 3 + (k >> 2)) % kSlots) * kSlot);
-                                mma_bf16_ts(tmem + TM_O + 128 * g, tmem + TM_S + 128 * g + 8 * k,
-                                            desc_add(vd, (k & 3) * 2048u), id_o, i > 0 || k > 0);
-                            }
-                            if (i + 1 == w.n[g]) mma_commit(&M->o_full[g]);
-                        }
-                        __syncwarp();
-                    }
-                    // the next scores of this half follow its product, which reads P in their place
-                    if (g == 0 && i + 1 < n) wait_slots(5 * (u + i + 1), 3);
-                    if (ok && i + 1 < w.n[g]) scores(g, u + i + 1);
+            for (int i = 0; i < n; ++i, ++u) {
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                const uint32_t x = u + 1;
+                // half 0: its product, then its next scores (which follow the product in the pipe:
+                // it reads P in their place); then half 1
+                ok &= wait_or_fail(v_full + 8 * (u & 1), (u >> 1) & 1, fail);
+                if (i < n0) ok &= wait_or_fail(p_full, cnt0++ & 1, fail);
+                tc_fence_after();
+                if (i < n0 && elect_one()) {
+                    product(0, u, i > 0);
+                    if (i + 1 == n0) commit(o_full);
                 }
-                if (!ok) break;
-                free_slots(5 * (u + i) + 3, 2);
-                if (i + 1 < n) free_slots(5 * (u + i + 1), 3);
-                if (i + 2 == n && elect_one()) mma_commit(&M->q_empty);
+                __syncwarp();
+                if (i + 1 < n) ok &= wait_or_fail(k_full + 8 * (x & 1), (x >> 1) & 1, fail);
+                tc_fence_after();
+                if (i + 1 < n0 && elect_one()) scores(0, x);
+                __syncwarp();
+                if (i < n1) ok &= wait_or_fail(p_full + 8, cnt1++ & 1, fail);
+                tc_fence_after();
+                if (elect_one()) {
+                    if (i < n1) {
+                        product(1, u, i > 0);
+                        if (i + 1 == n1) commit(o_full + 8);
+                    }
+                    commit(v_empty + 8 * (u & 1));
+                    if (i + 1 < n1) scores(1, x);
+                    if (i + 1 < n) commit(k_empty + 8 * (x & 1));
+                    if (i + 2 == n) commit(q_empty);
+                }
                 __syncwarp();
             }
-            u += n;
         }
         // nothing of this CTA's products is in flight when its TMEM goes
         if (elect_one()) mma_commit(&M->done);
@@ -358,8 +365,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             for (int i = 0; i < n; ++i, ++cnt) {
                 const int lim = sees - i * kTileK;        // columns from here on are masked
                 const bool masked = all_see - i * kTileK < kTileK;
-                ok = wait_or_fail(&M->s_full[g], cnt & 1, fail);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                ok = warp_wait(&M->s_full[g], cnt & 1, fail);
+                if (!ok) break;
                 tc_fence_after();
                 uint32_t p[64];
                 float top, sum;
@@ -437,8 +444,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     // value rows behind the sequence's end are its neighbour's: they must not meet
                     // a zero weight
                     const uint32_t first = 5 * (u + i) + 3;
-                    for (int c = 0; c < 2; ++c)
-                        ok = ok && wait_or_fail(&M->full[(first + c) % kSlots], ((first + c) / kSlots) & 1, fail);
+                    ok = warp_wait(&M->v_full[(u + i) & 1], ((u + i) >> 1) & 1, fail);
                     const int from = w.nk - i * kTileK;
                     for (int e = row; ok && e < (kTileK - from) * 16; e += kHalf) {
                         const int rr = from + (e >> 4), ch = e & 15;
@@ -450,15 +456,15 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&M->p_full[g]);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                warp_arrive(&M->p_full[g]);
+                if (!ok) break;
             }
             u += n_all;
             if (!ok) break;
             // ---- output
             if (n > 0) {
-                ok = wait_or_fail(&M->o_full[g], n_out & 1, fail);
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                ok = warp_wait(&M->o_full[g], n_out & 1, fail);
+                if (!ok) break;
                 ++n_out;
                 tc_fence_after();
             }

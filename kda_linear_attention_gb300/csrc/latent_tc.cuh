@@ -51,23 +51,81 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(p));
     return p != 0;
 }
-// A descriptor `bytes` further on (no carry out of its 14 address bits:
-// shared memory ends below 2^18).
-__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+// A shared-memory operand as two words: the low one holds the address (14
+// bits of 16 bytes: shared memory ends below 2^18, so offsets add without a
+// carry) and the leading offset, the high one is constant over a kernel.  An
+// offset costs one 32-bit add, on a path that issues a product every 40 to 80
+// cycles.
+struct Operand {
+    uint32_t lo, hi;
+    __device__ __forceinline__ Operand operator+(uint32_t bytes) const { return Operand{lo + (bytes >> 4), hi}; }
+};
+__device__ __forceinline__ Operand operand(const void *p, uint32_t lbo, uint32_t sbo) {
+    const uint64_t d = smem_desc(smem_u32(p), lbo, sbo, kSwizzle128B);
+    return Operand{(uint32_t)d, (uint32_t)(d >> 32)};
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, Operand a, Operand b, uint32_t idesc, bool acc = true) {
+    if (ACC)
+        asm volatile(
+            "{\n\t.reg .b64 a, b;\n\t.reg .pred p;\n\t"
+            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.eq.u32 p, 0, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+            "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .b64 a, b;\n\t.reg .pred p;\n\t"
+            "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+            "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"((uint32_t)acc)
+            : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, Operand b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .b64 b;\n\t.reg .pred p;\n\t"
+        "mov.b64 b, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
 
 // A bounded wait that also ends when another role of the block has given up.
-__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, volatile int *fail) {
+// The first poll, which is the only one where the wait is over already, is a
+// handful of instructions: the MMA warp's time is its instructions'.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool poll_on(uint32_t bar, uint32_t parity, volatile int *fail) {
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (poll(bar, parity)) return true;
         if ((i & 63u) == 63u && *fail) return false;
     }
     *fail = 1;
     return false;
 }
-
+__device__ __forceinline__ bool wait_or_fail(uint32_t bar, uint32_t parity, volatile int *fail) {
+    return poll(bar, parity) || poll_on(bar, parity, fail);
+}
+__device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, volatile int *fail) {
+    return wait_or_fail(smem_u32(bar), parity, fail);
+}
 // The same by a whole warp, with one verdict.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *fail) {
     return __all_sync(0xffffffffu, wait_or_fail(bar, parity, fail));
+}
+// A warp's arrival: one for its 32 lanes, after what each of them did.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // Named barrier over `threads` threads; true if any of them passed `x`.
@@ -82,6 +140,9 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool x) {
         : "r"((uint32_t)x), "r"(id), "r"(threads)
         : "memory");
     return r != 0;
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
