@@ -302,6 +302,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             }
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -313,6 +314,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         Walk<NR> walk(a, M);
         Item it;
         uint32_t n_tile = 0, n_item = 0;          // tiles and items with tiles so far
+        uint32_t n_x = 0, n_pair = 0, n_rope = 0; // copies asked for, by barrier
         const int page = 1 << a.pages.page_log2;
         const int brows = min(page, kTile), boxes = kTile / brows;   // TMA boxes down a tile
         bool ok = true;
@@ -329,6 +331,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             int rows = box_row(0, true);
             if (n_item > 0) ok = warp_wait(&M->x_empty, (n_item - 1) & 1, fail);
             if (!ok) break;
+            ++n_x;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&M->x_full, NR * 1152u);
                 for (int k = 0; k < 9; ++k)
@@ -345,6 +348,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                     const uint32_t u = 4 * n_tile + j, slot = u % F::NP, use = u / F::NP;
                     if (use > 0) ok = warp_wait(&M->empty_p[slot], (use - 1) & 1, fail);
                     if (!ok) break;
+                    ++n_pair;
                     if (lane == 0) mbar_arrive_expect_tx(&M->full_p[slot], (uint32_t)live * brows * 256u);
                     __syncwarp();
                     uint8_t *dst = sm + F::PAIR + slot * kPair;
@@ -358,6 +362,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 const uint32_t slot = n_tile % F::NQ, use = n_tile / F::NQ;
                 if (use > 0) ok = warp_wait(&M->empty_r[slot], (use - 1) & 1, fail);
                 if (!ok) break;
+                ++n_rope;
                 if (lane == 0) mbar_arrive_expect_tx(&M->full_r[slot], (uint32_t)live * brows * 128u);
                 __syncwarp();
                 if (rows >= 0)
@@ -366,6 +371,16 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 rows = next_rows;
             }
             ++n_item;
+        }
+        if (!ok || *fail) {
+            // given up: what was asked for still has to land before the block may end
+            auto land = [&](uint64_t *bar, uint32_t uses, uint32_t bars) {
+                for (uint32_t i = uses > bars ? uses - bars : 0; i < uses; ++i)
+                    mbar_wait(bar + i % bars, (i / bars) & 1, kWaitLimit);
+            };
+            land(&M->x_full, n_x, 1);
+            land(M->full_p, n_pair, F::NP);
+            land(M->full_r, n_rope, F::NQ);
         }
     } else if (warp == kSoftWarps) {
         // ================================================= matrix products
@@ -647,6 +662,7 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
                    const float *__restrict__ ws_o, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
                    int NR) {
     const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces are written
     const Split sp = split[c];
     const int n = sp.last - c + 1;
     const bool alone = n <= kJoinAlone;
@@ -743,8 +759,18 @@ cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const void *cac
         mx, mc, static_cast<const uint8_t *>(cache), a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    latent_join_kernel<<<dim3(G, kJoinBlocks), 32 * kJoinWarps, 0, stream>>>(a.split, a.ws_lse, a.ws_o, a.o, a.lse, NR);
-    return cudaGetLastError();
+    // launched while the first kernel runs: its blocks wait for that one's end on the device
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(G, kJoinBlocks);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_join_kernel, (const Split *)a.split, (const float *)a.ws_lse,
+                              (const float *)a.ws_o, a.o, a.lse, NR);
 }
 
 }  // namespace

@@ -7,8 +7,10 @@
 // query i of nq sees keys 0 .. nk - nq + i.
 //   s = scale <q, k>,   o = softmax(s) v,   lse = ln sum e^s
 //
-// A CTA (one an SM) takes work tiles of 256 queries of one (sequence, head)
-// and runs over the keys 128 at a time, with two halves of 128 queries in
+// A work tile is 256 queries of one (sequence, head).  The grid has a CTA for
+// each; a CTA (one fits an SM) that is done with one takes over the next that
+// has not been launched, so its loads and products follow on without a gap.
+// It runs over the keys 128 at a time, with two halves of 128 queries in
 // turn on the tensor cores, so that one half's products cover the other's
 // softmax:
 //   S_g [128 x 128] = Q_g K^T         12 K-steps, Q_g and K from shared memory
@@ -47,10 +49,13 @@ constexpr uint32_t SM_RING = 6 * 16384;
 constexpr uint32_t SM_MISC = SM_RING + kSlots * kSlot;
 constexpr float kMoveAt = 8.f;            // log2 of the factor a score may pass the maximum by
 constexpr uint32_t TM_S = 0, TM_O = 256;
+constexpr int64_t kL2Bytes = 48 << 20;    // keys and values of the heads listed together
 
 struct Misc {
     uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];   // by key tile, even and odd
     uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], done;
+    uint64_t work_full[2], work_empty[2];
+    alignas(16) uint4 work[2];            // answers to the requests for a further work tile
     uint32_t tmem;
     int fail;
     int tiles;                            // work tiles of all sequences (of one head)
@@ -64,6 +69,8 @@ struct Args {
     const int32_t *cu_q, *cu_k;
     int N, Tq, Tk, H;
     bool causal;
+    int heads_together;                   // heads whose work tiles are listed together
+    bool o_aligned32;
     float scale_log2;                     // scale * log2 e
     __nv_bfloat16 *o;
     float *lse;
@@ -87,17 +94,18 @@ struct Work {
     int first;                            // keys that the sequence's query 0 sees (may be <= 0)
 };
 
-// The r-th work tile of this CTA.  Tiles are listed head by head, in a head
-// from the last queries (which see the most keys) to the first; the CTAs take
-// them in rounds, every other round backwards, so that no stride between
-// them hits the long ones alone.
-__device__ __forceinline__ bool get_work(const Args &a, const Misc *M, int r, Work &w) {
-    const int G = gridDim.x, c = (r & 1) ? G - 1 - (int)blockIdx.x : (int)blockIdx.x;
-    const int64_t id = (int64_t)r * G + c;
+// Work tile `id` of the grid.  Heads are listed in groups whose keys and
+// values fit in L2 together; in a group, from the tiles of the last queries
+// (which see the most keys) to those of the first, so that what is handed out
+// last is short.
+__device__ __forceinline__ bool get_work(const Args &a, const Misc *M, unsigned id, Work &w) {
     const int tiles = M->tiles;
-    if (tiles == 0 || id >= (int64_t)tiles * a.H) return false;
-    w.h = (int)(id / tiles);
-    int k = tiles - 1 - (int)(id % tiles);
+    if (id >= (unsigned)tiles * (unsigned)a.H) return false;
+    const unsigned group = id / ((unsigned)tiles * a.heads_together);
+    const int h0 = group * a.heads_together, heads = min(a.heads_together, a.H - h0);
+    const int in = (int)(id - group * tiles * a.heads_together);
+    w.h = h0 + in % heads;
+    int k = tiles - 1 - in / heads;
     // the thread whose sequences hold tile k, then the sequence
     int lo = 0, hi = kThreads;
     while (hi - lo > 1) {
@@ -139,6 +147,53 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
           "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
+}
+// Asks for a work tile that no CTA has begun: the grid has a CTA for each, and
+// a running one takes over the next that has not been launched.  The answer
+// (16 bytes) comes to shared memory like a copy.
+__device__ __forceinline__ void ask_work(uint4 *answer, uint64_t *bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// The block index taken over, or -1 (none was left).
+__device__ __forceinline__ int taken_work(const uint4 *answer) {
+    uint32_t ok, x = 0;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return ok ? (int)x : -1;
+}
+// One role's walk over the CTA's work tiles, by whole warps: its own block
+// index first, then what the copy warp's requests bring.
+struct Tiles {
+    uint32_t r = 0;
+    int id;
+    __device__ __forceinline__ Tiles() : id((int)blockIdx.x) {}
+    __device__ __forceinline__ void step(Misc *M, bool &ok, volatile int *fail) {
+        const uint32_t at = r & 1;
+        ok = ok && warp_wait(&M->work_full[at], (r >> 1) & 1, fail);
+        id = ok ? taken_work(&M->work[at]) : -1;
+        fence_proxy_async_smem();         // read before a later request writes there
+        warp_arrive(&M->work_empty[at]);
+        ++r;
+    }
+};
+
+__device__ __forceinline__ void st_global32(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *r) {
     asm volatile(
@@ -188,6 +243,10 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 mbar_init(&M->o_full[g], 1);
             }
             mbar_init(&M->done, 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&M->work_full[i], 1);
+                mbar_init(&M->work_empty[i], kThreads / 32);
+            }
             fence_mbar_init();
         }
         if (warp == 8) tmem_alloc(&M->tmem, 512);
@@ -212,16 +271,23 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     const uint32_t tmem = M->tmem;
     volatile int *fail = &M->fail;
     Work w;
+    Tiles tiles;
 
     if (warp == 9) {
         // ================================================= copies
         // Key tile u fills ring slots 5 u .. 5 u + 2, its value tile 5 u + 3 and 5 u + 4 (modulo 8).
         // The key slots were last the third of key tile u - 2 and both of its value tile, the value
         // slots the first two of key tile u - 1; the MMA warp releases in the order of u.
-        uint32_t u = 0;
+        uint32_t u = 0;                           // key tiles asked for
+        uint32_t n_v = 0, n_work = 0, asked = 0;  // value tiles, Q tiles, further work tiles
         bool ok = true;
-        uint32_t n_work = 0;
-        for (int r = 0; ok && get_work(a, M, r, w); ++r) {
+        for (; ok && tiles.id >= 0 && get_work(a, M, tiles.id, w); tiles.step(M, ok, fail)) {
+            // the next work tile's request; its answer is there long before this one is done
+            if (tiles.r >= 2) ok = warp_wait(&M->work_empty[tiles.r & 1], ((tiles.r >> 1) - 1) & 1, fail);
+            if (!ok) break;
+            if (lane == 0) ask_work(&M->work[tiles.r & 1], &M->work_full[tiles.r & 1]);
+            ++asked;
+            __syncwarp();
             const int n = max(w.n[0], w.n[1]);
             if (n == 0) continue;
             if (n_work > 0) ok = warp_wait(&M->q_empty, (n_work - 1) & 1, fail);
@@ -234,9 +300,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                         tma_load_3d(sm + SM_Q + (3 * g + c) * kSlot, &map_q, &M->q_full, 64 * c, w.h,
                                     w.q0 + w.i0 + g * kHalf);
             }
-            for (int i = 0; i < n; ++i, ++u) {
+            for (int i = 0; i < n; ++i) {
                 const int tok = w.k0 + i * kTileK;
-                auto slot = [&](int c) { return sm + SM_RING + ((5 * u + c) % kSlots) * kSlot; };
+                auto slot = [&](int c) { return sm + SM_RING + ((5 * n_v + c) % kSlots) * kSlot; };
                 if (u >= 2) ok = warp_wait(&M->v_empty[u & 1], ((u >> 1) - 1) & 1, fail);
                 if (!ok) break;
                 if (lane == 0) {
@@ -247,10 +313,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     tma_load_2d(slot(2), &map_pe, bar, 0, tok);
                 }
                 __syncwarp();
-                if (u >= 1) ok = warp_wait(&M->k_empty[(u - 1) & 1], ((u - 1) >> 1) & 1, fail);
+                ++u;
+                if (n_v >= 1) ok = warp_wait(&M->k_empty[(n_v - 1) & 1], ((n_v - 1) >> 1) & 1, fail);
                 if (!ok) break;
                 if (lane == 0) {
-                    uint64_t *bar = &M->v_full[u & 1];
+                    uint64_t *bar = &M->v_full[n_v & 1];
                     mbar_arrive_expect_tx(bar, 2 * kSlot);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -259,7 +326,19 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     }
                 }
                 __syncwarp();
+                ++n_v;
             }
+        }
+        if (!__all_sync(0xffffffffu, ok) || *fail) {
+            // given up: what was asked for still has to land before the block may end
+            auto land = [&](uint64_t *bar, uint32_t uses, uint32_t bars) {
+                for (uint32_t i = uses > bars ? uses - bars : 0; i < uses; ++i)
+                    mbar_wait(bar + i % bars, (i / bars) & 1, kWaitLimit);
+            };
+            land(&M->q_full, n_work, 1);
+            land(M->k_full, u, 2);
+            land(M->v_full, n_v, 2);
+            land(M->work_full, asked, 2);
         }
     } else if (warp == 8) {
         // ================================================= matrix products
@@ -296,7 +375,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                            acc || c > 0 || e > 0);
             }
         };
-        for (int r = 0; ok && get_work(a, M, r, w); ++r) {
+        for (; ok && tiles.id >= 0 && get_work(a, M, tiles.id, w); tiles.step(M, ok, fail)) {
             const int n0 = w.n[0], n1 = w.n[1], n = max(n0, n1);
             if (n == 0) continue;
             ok &= wait_or_fail(&M->q_full, n_work & 1, fail);
@@ -354,7 +433,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
         uint32_t cnt = 0, n_out = 0, u = 0;
         bool ok = true;
-        for (int r = 0; ok && get_work(a, M, r, w); ++r) {
+        for (; ok && tiles.id >= 0 && get_work(a, M, tiles.id, w); tiles.step(M, ok, fail)) {
             const int rows = w.rows[g], n = w.n[g];
             const int n_all = max(w.n[0], w.n[1]);
             if (rows == 0) { u += n_all; continue; }
@@ -472,19 +551,28 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             const size_t out = ((size_t)w.q0 + i_row) * a.H + w.h;
 #pragma unroll
             for (int c0 = 0; c0 < 128; c0 += 32) {
-                uint32_t ov[32];
+                uint32_t ov[32] = {};
                 if (n > 0) {
                     tmem_ld32(to + c0, ov);
                     tmem_wait_ld();
                 }
                 if (row < rows) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.o + out * 128 + c0);
+                    // a lane stores its own row: whole 32-byte sectors halve the store unit's work
+                    __nv_bfloat16 *dst = a.o + out * 128 + c0;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 8) {
-                        float x[8];
+                    for (int c = 0; c < 32; c += 16) {
+                        uint32_t x[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = n > 0 ? __uint_as_float(ov[c + e]) * inv : 0.f;
-                        dst[c / 8] = l > 0.f ? pack_bf8(x) : make_uint4(0, 0, 0, 0);
+                        for (int e = 0; e < 8; ++e)
+                            x[e] = l > 0.f ? pack_bf2(__uint_as_float(ov[c + 2 * e]) * inv,
+                                                      __uint_as_float(ov[c + 2 * e + 1]) * inv)
+                                           : 0u;
+                        if (a.o_aligned32) {
+                            st_global32(dst + c, x);
+                        } else {
+                            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+                        }
                     }
                 }
             }
@@ -508,7 +596,7 @@ cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_p
                                   void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
                                   cudaStream_t stream) {
     static KernelSetup setup;
-    int sms = 0;
+    int sms = 0;                          // not needed: the grid is the work's
     const cudaError_t e = setup.get(reinterpret_cast<const void *>(latent_prefill_kernel), SM_BYTES + 1024, &sms);
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv, mp;
@@ -517,11 +605,13 @@ cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_p
     if (Tk > 0 && (!make_map_heads(&mk, kv, 256, H, Tk, kTileK) || !make_map_heads(&mv, kv, 256, H, Tk, 64) ||
                    !make_map_rows(&mp, k_pe, 64, Tk, pe_stride, kTileK)))
         return cudaErrorInvalidValue;
-    const Args a{cu_q, cu_k, N, (int)Tq, (int)Tk, H, causal, scale * 1.4426950408889634f,
+    const int together = (int)std::min<int64_t>(H, std::max<int64_t>(1, kL2Bytes / (std::max<int64_t>(Tk, 1) * 512)));
+    const Args a{cu_q, cu_k, N, (int)Tq, (int)Tk, H, causal, together,
+                 (reinterpret_cast<uintptr_t>(o) & 31u) == 0, scale * 1.4426950408889634f,
                  static_cast<__nv_bfloat16 *>(o), lse};
-    const int64_t most = (Tq / kTileQ + N) * H;   // work tiles at most
-    latent_prefill_kernel<<<(unsigned)std::min<int64_t>(sms, most), kThreads, SM_BYTES + 1024, stream>>>(mq, mk, mv,
-                                                                                                    mp, a);
+    // a CTA for each work tile there can be: a sequence's last tile may be part of one
+    const int64_t most = std::min<int64_t>(Tq, Tq / kTileQ + N) * H;
+    latent_prefill_kernel<<<(unsigned)most, kThreads, SM_BYTES + 1024, stream>>>(mq, mk, mv, mp, a);
     return cudaGetLastError();
 }
 
