@@ -647,30 +647,62 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
     if (warp == kSoftWarps) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the pieces of the row tile that starts in CTA c = blockIdx.x and goes
-// on behind it: o = sum_k 2^(lse_k - lse) o_k, in the order of the positions.
-// With few pieces a warp takes a row by itself; with many (few long
-// sequences, so few such tiles) a block shares a row's pieces among its warps
-// and adds the warps' sums in order.  Bound by the pieces' bytes, which the
-// first kernel has just left in L2, and by the latency of its few loads.
+// Joins the pieces of the row tiles that start in one CTA and go on behind
+// it: o = sum_k 2^(lse_k - lse) o_k, in the order of the positions.  Every
+// block lists all such tiles (at most one a CTA) and takes every gridDim-th
+// unit of them: eight rows of a tile with few pieces, a warp a row, or one row
+// of a tile with many (few long sequences, so few such tiles), whose pieces
+// its warps share and whose warps' sums are added in order.  Bound by the
+// latency of its few loads, from L2, where the first kernel has just left the
+// pieces; a grid of a block a (tile, row) costs more in empty blocks.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinBlocks = 32;           // blocks a row tile
+constexpr int kJoinThreads = 32 * kJoinWarps;
 constexpr int kJoinAlone = 8;             // pieces a warp takes by itself
+static_assert(kJoinThreads >= kMaxCtas, "a thread a record");
 
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(kJoinThreads)
 latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws_lse,
                    const float *__restrict__ ws_o, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
-                   int NR) {
-    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces are written
-    const Split sp = split[c];
-    const int n = sp.last - c + 1;
-    const bool alone = n <= kJoinAlone;
-    const int r0 = alone ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
-    const int step = alone ? kJoinBlocks * kJoinWarps : kJoinBlocks;
+                   int NR, int G) {
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     __shared__ float4 part[kJoinWarps][kLatent / 4];
-    auto slot = [&](int k) { return k == 0 ? 2 * c + 1 : 2 * (c + k); };
-    for (int r = r0; r < sp.rows; r += step) {
+    __shared__ Split rec[kMaxCtas];
+    __shared__ int upto[kJoinThreads];        // units of the records up to and with this one
+    __shared__ int warp_sum[kJoinWarps];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces are written
+    {
+        Split sp{0, 0, 0, 0};
+        if (t < G) {
+            sp = split[t];
+            rec[t] = sp;
+        }
+        const int n = sp.last - t + 1;
+        int incl = sp.rows == 0 ? 0 : n <= kJoinAlone ? (sp.rows + kJoinWarps - 1) / kJoinWarps : sp.rows;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) incl += warp_sum[w];
+        upto[t] = incl;
+        __syncthreads();
+    }
+    const int units = upto[kJoinThreads - 1];
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        int c = 0, hi = kJoinThreads - 1;         // the first record that reaches past u
+        while (c < hi) {
+            const int mid = (c + hi) >> 1;
+            if (upto[mid] > u) hi = mid;
+            else c = mid + 1;
+        }
+        const Split sp = rec[c];
+        const int n = sp.last - c + 1, in = u - (c > 0 ? upto[c - 1] : 0);
+        const bool alone = n <= kJoinAlone;
+        const int r = alone ? in * kJoinWarps + warp : in;
+        if (alone && r >= sp.rows) continue;
+        auto slot = [&](int k) { return k == 0 ? 2 * c + 1 : 2 * (c + k); };
         // every warp finds the maximum and the sum by itself
         float v[kMaxCtas / 32], mx = -CUDART_INF_F, sum = 0.f;
 #pragma unroll
@@ -695,9 +727,9 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
 #pragma unroll
         for (int e = 0; e < kMaxCtas / 32; ++e) {
             if (32 * e >= n) break;
-            const int hi = min(32, n - 32 * e);
+            const int last = min(32, n - 32 * e);
 #pragma unroll 2
-            for (int k = alone ? 0 : warp; k < hi; k += alone ? 1 : kJoinWarps) {
+            for (int k = alone ? 0 : warp; k < last; k += alone ? 1 : kJoinWarps) {
                 const float w = __shfl_sync(0xffffffffu, v[e], k) * inv;
                 const float4 *src = reinterpret_cast<const float4 *>(ws_o + ((size_t)slot(32 * e + k) * NR + r) * kLatent);
 #pragma unroll
@@ -720,14 +752,14 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
 #pragma unroll
             for (int q = 0; q < 4; ++q) part[warp][32 * q + lane] = acc[q];
             __syncthreads();
-            if (threadIdx.x < kLatent / 4) {
-                float4 x = part[0][threadIdx.x];
+            if (t < kLatent / 4) {
+                float4 x = part[0][t];
 #pragma unroll
                 for (int w = 1; w < kJoinWarps; ++w) {
-                    const float4 y = part[w][threadIdx.x];
+                    const float4 y = part[w][t];
                     x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
                 }
-                dst[threadIdx.x] = make_uint2(pack_bf2(x.x, x.y), pack_bf2(x.z, x.w));
+                dst[t] = make_uint2(pack_bf2(x.x, x.y), pack_bf2(x.z, x.w));
             }
             __syncthreads();
         }
@@ -764,13 +796,13 @@ cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const void *cac
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(G, kJoinBlocks);
-    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.gridDim = dim3(4 * G);                // all of them fit the SMs at once
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, latent_join_kernel, (const Split *)a.split, (const float *)a.ws_lse,
-                              (const float *)a.ws_o, a.o, a.lse, NR);
+                              (const float *)a.ws_o, a.o, a.lse, NR, G);
 }
 
 }  // namespace
