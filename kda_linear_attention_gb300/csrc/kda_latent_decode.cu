@@ -75,12 +75,20 @@ struct Cfg {
     static_assert(BYTES + 1024 <= 232448, "shared memory of an SM");
 };
 
+// A sequence as the kernel sees it (clamped to what its buffers hold).
+struct Seq {
+    int row0, rows;                       // flat rows over [T * H], of this sequence
+    int first;                            // positions its first new token sees (may be <= 0)
+    int len, tiles, row_tiles;
+};
+
 struct Misc {
     uint64_t full_p[5], empty_p[5], full_r[2], empty_r[2];
     uint64_t x_full, x_empty, s_full, p_full, o_full, done;
     uint32_t tmem;
     int fail;
     int b0, j0, t0;                       // first unit
+    Seq seq0;                             // its sequence
     int32_t units;                        // units of this CTA
     int used;                             // CTAs with units
     long long scan[kThreads / 32 + 1];
@@ -104,13 +112,6 @@ struct Args {
     Split *split;
     float *ws_lse;                        // [2 G][NR]
     float *ws_o;                          // [2 G][NR][512]
-};
-
-// A sequence as the kernel sees it (clamped to what its buffers hold).
-struct Seq {
-    int row0, rows;                       // flat rows over [T * H], of this sequence
-    int first;                            // positions its first new token sees (may be <= 0)
-    int len, tiles, row_tiles;
 };
 
 template <int NR>
@@ -160,7 +161,7 @@ struct Walk {
     Seq s;
     __device__ __forceinline__ Walk(const Args &a, const Misc *m)
         : b(m->b0), j(m->j0), t(m->t0), left(m->units), u(m->start) {
-        if (left > 0) s = get_seq<NR>(a, b, false);
+        if (left > 0) s = m->seq0;
     }
     __device__ __forceinline__ bool next(const Args &a, Item &it) {
         if (left <= 0) return false;
@@ -242,8 +243,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         const int per = (a.N + kThreads - 1) / kThreads;
         const int b_lo = min(a.N, t * per), b_hi = min(a.N, b_lo + per);
         long long mine = 0;
+        Seq s;                                         // the only one where there are few
         for (int b = b_lo; b < b_hi; ++b) {
-            const Seq s = get_seq<NR>(a, b, cta == 0);     // CTA 0 flags what is wrong with a sequence
+            s = get_seq<NR>(a, b, cta == 0);           // CTA 0 flags what is wrong with a sequence
             mine += (long long)s.tiles * s.row_tiles;
         }
         long long incl = mine;
@@ -290,10 +292,11 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         }
         if (u1 > u0 && u0 >= before && u0 < before + mine) {
             for (int b = b_lo; b < b_hi; ++b) {
-                const Seq s = get_seq<NR>(a, b, false);
+                if (per > 1) s = get_seq<NR>(a, b, false);
                 const long long n = (long long)s.tiles * s.row_tiles;
                 if (u0 < before + n) {
                     M->b0 = b;
+                    M->seq0 = s;
                     M->j0 = (int)((u0 - before) / s.tiles);
                     M->t0 = (int)((u0 - before) % s.tiles);
                     break;
@@ -318,17 +321,38 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         const int page = 1 << a.pages.page_log2;
         const int brows = min(page, kTile), boxes = kTile / brows;   // TMA boxes down a tile
         bool ok = true;
+        // the flat cache row of box `lane` of an item's tile `i` (P * page: past the end, reads zeros)
+        auto box_row = [&](const Item &of, int i, bool flag) -> int {
+            const int pos = (of.tile + i) * kTile + lane * brows;
+            if (lane >= boxes || pos >= of.len) return -1;
+            const int64_t r = a.pages.row(of.b, pos);
+            if (r < 0 && flag) atomicOr(&g_kda_latent_decode_error, kErrSlot);
+            return r < 0 ? (int)(a.pages.P << a.pages.page_log2) : (int)r;
+        };
+        // A second walk, a tile in front, that only brings the rows into L2 (a page's rows are
+        // contiguous): shared memory holds little more than one tile, which is busy while it is
+        // computed with.  128 sequences of 8,000-8,192 tokens at 64 heads: 247 us a call without
+        // it, 211 us one tile in front, asked for behind the present tile's own copies, 238 us
+        // two and 319 us three tiles in front (more than L2 keeps for all the SMs).
+        Walk<NR> ahead(a, M);
+        Item ia;
+        int i_ahead = 0, n_ahead = 0;
+        bool more = true;
+        auto prefetch = [&](bool issue) {
+            while (more && i_ahead == n_ahead) {
+                more = ahead.next(a, ia);
+                i_ahead = 0;
+                n_ahead = more ? ia.n : 0;
+            }
+            if (!more) return;
+            const int rows = box_row(ia, i_ahead++, false);
+            if (issue && rows >= 0 && rows < (a.pages.P << a.pages.page_log2))
+                for (int e = 0; e < brows; e += 16)
+                    bulk_prefetch_l2(cache + ((size_t)rows + e) * 1152u, 16 * 1152u);
+        };
         while (ok && walk.next(a, it)) {
             if (it.n == 0) continue;
-            // the flat cache row of box `lane` of tile `i` (P * page: past the end, reads zeros)
-            auto box_row = [&](int i, bool flag) -> int {
-                const int pos = (it.tile + i) * kTile + lane * brows;
-                if (lane >= boxes || pos >= it.len) return -1;
-                const int64_t r = a.pages.row(it.b, pos);
-                if (r < 0 && flag) atomicOr(&g_kda_latent_decode_error, kErrSlot);
-                return r < 0 ? (int)(a.pages.P << a.pages.page_log2) : (int)r;
-            };
-            int rows = box_row(0, true);
+            int rows = box_row(it, 0, true);
             if (n_item > 0) ok = warp_wait(&M->x_empty, (n_item - 1) & 1, fail);
             if (!ok) break;
             ++n_x;
@@ -339,11 +363,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             }
             for (int i = 0; ok && i < it.n; ++i, ++n_tile) {
                 const int live = __popc(__ballot_sync(0xffffffffu, rows >= 0));
-                const int next_rows = i + 1 < it.n ? box_row(i + 1, true) : -1;
-                // the next tile's rows toward L2 (a page's rows are contiguous)
-                if (next_rows >= 0 && next_rows < (a.pages.P << a.pages.page_log2))
-                    for (int e = 0; e < brows; e += 16)
-                        bulk_prefetch_l2(cache + ((size_t)next_rows + e) * 1152u, 16 * 1152u);
+                const int next_rows = i + 1 < it.n ? box_row(it, i + 1, true) : -1;
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t u = 4 * n_tile + j, slot = u % F::NP, use = u / F::NP;
                     if (use > 0) ok = warp_wait(&M->empty_p[slot], (use - 1) & 1, fail);
@@ -369,6 +389,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                     tma_load_2d(sm + F::ROPE + slot * kRope + lane * brows * 128u, &map_c, &M->full_r[slot], kLatent, rows);
                 __syncwarp();
                 rows = next_rows;
+                if (n_tile == 0) prefetch(false);          // the first tile itself
+                prefetch(true);
             }
             ++n_item;
         }
@@ -768,10 +790,14 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
     }
 }
 
-// Rows of a tile: the average sequence's rows in as few tiles of at most 64
-// as hold them, in steps of 16 (the products' column step).
-int rows_of_tile(int N, int64_t T, int H) {
-    const int64_t rows = (T + N - 1) / N * H;
+// Rows of a tile, in steps of 16 (the products' column step) up to 64.  One
+// token a sequence: its H rows in as few tiles as hold them.  Ragged new
+// tokens: a third more than the average sequence's rows, because a tile costs
+// little more with more columns (a product step is bound by its 128-lane
+// operand: 72 cycles at 32 columns, 80 at 64) and a second tile for the longer
+// sequences' last rows costs as much as the first.
+int rows_of_tile(int N, int64_t T, int H, bool ragged) {
+    const int64_t rows = ragged ? (T * H + N - 1) / N * 4 / 3 : H;
     const int64_t tiles = (rows + 63) / 64;
     return (int)std::min<int64_t>(64, ((rows + tiles - 1) / tiles + 15) / 16 * 16);
 }
@@ -809,14 +835,15 @@ cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const void *cac
 
 // Workspace: the split records, the pieces' log2-sum-exp, the pieces.
 size_t latent_decode_workspace_bytes(int N, int64_t T, int H) {
-    return kSplitBytes + kLseBytes + (size_t)2 * kMaxCtas * rows_of_tile(N, T, H) * kLatent * sizeof(float);
+    const int most = std::max(rows_of_tile(N, T, H, true), T == N ? rows_of_tile(N, T, H, false) : 0);
+    return kSplitBytes + kLseBytes + (size_t)2 * kMaxCtas * most * kLatent * sizeof(float);
 }
 
 cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t *table,
                                  const int32_t *seq_lens, const int32_t *cu, float scale, void *o,
                                  float *lse, int N, int64_t T, int H, int64_t P, int page,
                                  int max_pages, void *ws, cudaStream_t stream) {
-    const int NR = rows_of_tile(N, T, H);
+    const int NR = rows_of_tile(N, T, H, cu != nullptr);
     CUtensorMap mx, mc;
     if (!make_map_rows(&mx, q, kLatentRow, T * H, kLatentRow, (uint32_t)NR) ||
         !make_map_rows(&mc, cache, kLatentRow, P * page, kLatentRow, (uint32_t)std::min(page, kTile)))
