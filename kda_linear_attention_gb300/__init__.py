@@ -516,42 +516,44 @@ LATENT_SCALE = (DK + LATENT_PE) ** -0.5   # 1/sqrt(expanded key width)
 # The calls below run once a layer and step with kernels of a few
 # microseconds, so their own checks cost less than the others': one chain of
 # cheap comparisons a tensor, and _check for the error's words.
+_Tensor, _BF16, _F32, _I32, _U8 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
 def _need(name, t, dtype, shape, dev):
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == dev and t.is_contiguous()):
-        _check(name, t, dtype, shape, dev)
+    """The address of a tensor that _check accepts (dev: a device index)."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        _check(name, t, dtype, shape, torch.device("cuda", dev))
     return t.data_ptr()
 
 
 def _need_cache(cache, block_table, N, dev):
-    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
+    if not isinstance(cache, _Tensor) or cache.dim() != 3:
         raise ValueError("cache must be a [P, page, %d] tensor" % LATENT_ROW)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+    if not isinstance(block_table, _Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a [N, max_pages] tensor")
     P, page, _ = cache.shape
     pages = block_table.shape[1]
-    return (_need("cache", cache, torch.bfloat16, (P, page, LATENT_ROW), dev),
-            _need("block_table", block_table, torch.int32, (N, pages), dev), P, page, pages)
+    return (_need("cache", cache, _BF16, (P, page, LATENT_ROW), dev),
+            _need("block_table", block_table, _I32, (N, pages), dev), P, page, pages)
 
 
-def _elsewhere(t) -> bool:
-    """Whether the tensor's device is not the current one (a launch goes to
-    the current device)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _device(t) -> int:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
-    return t.get_device() != torch.cuda.current_device()
+    return t.get_device()
 
 
 def _raw_stream(dev, stream):
-    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _empty(shape, dtype, dev, stream):
-    """Memory of the stream that uses it."""
+def _empty(shape, dtype, like, stream):
+    """Memory on the tensor's device, of the stream that uses it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def latent_append(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
@@ -565,17 +567,17 @@ def latent_append(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     [N + 1] int32 (None: one new token a sequence).  With norm_w [512] fp32
     the latent part is RMS-normalised.  Returns cache.
     """
-    if _elsewhere(x):
-        with torch.cuda.device(x.device):
+    dev = _device(x)
+    if dev != torch.cuda.current_device():      # a launch goes to the current device
+        with torch.cuda.device(dev):
             return latent_append(x, cache, block_table, seq_lens, cu_seqlens, norm_w, eps, stream)
-    dev = x.device
     T, N = x.shape[0], seq_lens.numel()
     c, table, P, page, pages = _need_cache(cache, block_table, N, dev)
     rc = lib().kda_latent_append(
-        _need("x", x, torch.bfloat16, (T, LATENT_ROW), dev), c, table,
-        _need("seq_lens", seq_lens, torch.int32, (N,), dev),
-        None if cu_seqlens is None else _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev),
-        None if norm_w is None else _need("norm_w", norm_w, torch.float32, (LATENT,), dev),
+        _need("x", x, _BF16, (T, LATENT_ROW), dev), c, table,
+        _need("seq_lens", seq_lens, _I32, (N,), dev),
+        None if cu_seqlens is None else _need("cu_seqlens", cu_seqlens, _I32, (N + 1,), dev),
+        None if norm_w is None else _need("norm_w", norm_w, _F32, (LATENT,), dev),
         eps, N, T, P, page, pages, LATENT, LATENT_PE, _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_append")
@@ -588,20 +590,20 @@ def latent_gather(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: to
     """Read every sequence's first rows back, packed by cu_seqlens
     (``kda_latent_gather``).  total: the packed length cu_seqlens[N] (where
     ``out`` [total, 576] bf16 is not given).  Returns out."""
-    if _elsewhere(cache):
-        with torch.cuda.device(cache.device):
+    dev = _device(cache)
+    if dev != torch.cuda.current_device():      # a launch goes to the current device
+        with torch.cuda.device(dev):
             return latent_gather(cache, block_table, cu_seqlens, total, out, stream)
-    dev = cache.device
     N = cu_seqlens.numel() - 1
     c, table, P, page, pages = _need_cache(cache, block_table, N, dev)
     if out is None:
         if total is None:
             raise ValueError("give the packed length (total) or the output (out)")
-        out = _empty((total, LATENT_ROW), torch.bfloat16, dev, stream)
+        out = _empty((total, LATENT_ROW), _BF16, cache, stream)
     T = out.shape[0]
     rc = lib().kda_latent_gather(
-        c, table, _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev),
-        _need("out", out, torch.bfloat16, (T, LATENT_ROW), dev), N, T, P, page, pages, LATENT, LATENT_PE,
+        c, table, _need("cu_seqlens", cu_seqlens, _I32, (N + 1,), dev),
+        _need("out", out, _BF16, (T, LATENT_ROW), dev), N, T, P, page, pages, LATENT, LATENT_PE,
         _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_gather")
@@ -629,28 +631,28 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     (``latent_decode_workspace_bytes``) comes from torch's allocator unless
     one is given.
     """
-    if _elsewhere(q):
-        with torch.cuda.device(q.device):
+    dev = _device(q)
+    if dev != torch.cuda.current_device():      # a launch goes to the current device
+        with torch.cuda.device(dev):
             return latent_decode(q, cache, block_table, seq_lens, cu_seqlens, scale, o, lse, workspace, stream)
-    dev = q.device
     T, H, N = q.shape[0], q.shape[1], seq_lens.numel()
     c, table, P, page, pages = _need_cache(cache, block_table, N, dev)
     if o is None:
-        o = _empty((T, H, LATENT), torch.bfloat16, dev, stream)
+        o = _empty((T, H, LATENT), _BF16, q, stream)
     if lse is None:
-        lse = _empty((T, H), torch.float32, dev, stream)
+        lse = _empty((T, H), _F32, q, stream)
     if workspace is None:
         nbytes = latent_decode_workspace_bytes(N, T, H)
-        workspace = _empty((nbytes,), torch.uint8, dev, stream) if nbytes else None
+        workspace = _empty((nbytes,), _U8, q, stream) if nbytes else None
     else:
-        if workspace.device != dev or not workspace.is_contiguous():
+        if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the inputs' device")
         nbytes = workspace.numel() * workspace.element_size()
     rc = lib().kda_latent_decode(
-        _need("q", q, torch.bfloat16, (T, H, LATENT_ROW), dev), c, table,
-        _need("seq_lens", seq_lens, torch.int32, (N,), dev),
-        None if cu_seqlens is None else _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev),
-        scale, _need("o", o, torch.bfloat16, (T, H, LATENT), dev), _need("lse", lse, torch.float32, (T, H), dev),
+        _need("q", q, _BF16, (T, H, LATENT_ROW), dev), c, table,
+        _need("seq_lens", seq_lens, _I32, (N,), dev),
+        None if cu_seqlens is None else _need("cu_seqlens", cu_seqlens, _I32, (N + 1,), dev),
+        scale, _need("o", o, _BF16, (T, H, LATENT), dev), _need("lse", lse, _F32, (T, H), dev),
         N, T, H, P, page, pages, LATENT, LATENT_PE,
         None if workspace is None else workspace.data_ptr(), nbytes, _raw_stream(dev, stream))
     if rc != 0:
@@ -673,28 +675,29 @@ def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seq
     sequence are its last tokens.  Returns (o [Tq, H, 128] bf16, lse [Tq, H]
     fp32).
     """
-    if _elsewhere(q):
-        with torch.cuda.device(q.device):
+    dev = _device(q)
+    if dev != torch.cuda.current_device():      # a launch goes to the current device
+        with torch.cuda.device(dev):
             return latent_prefill(q, kv, k_pe, cu_seqlens, cu_seqlens_k, scale, causal, o, lse, stream)
-    dev = q.device
     Tq, H, N, Tk = q.shape[0], q.shape[1], cu_seqlens.numel() - 1, kv.shape[0]
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens
-    if not (isinstance(k_pe, torch.Tensor) and k_pe.device == dev and k_pe.dtype is torch.bfloat16
+    if not (isinstance(k_pe, _Tensor) and k_pe.get_device() == dev and k_pe.dtype is _BF16
             and k_pe.shape == (Tk, LATENT_PE) and (Tk == 0 or k_pe.stride(1) == 1)):
-        raise ValueError("k_pe must be [%d, %d] bfloat16 on %s with dense rows" % (Tk, LATENT_PE, dev))
+        raise ValueError("k_pe must be [%d, %d] bfloat16 on %s with dense rows"
+                         % (Tk, LATENT_PE, q.device))
     # the stride of a dimension of one row means nothing
     pe_stride = k_pe.stride(0) if Tk > 1 else LATENT_PE
     if o is None:
-        o = _empty((Tq, H, DV), torch.bfloat16, dev, stream)
+        o = _empty((Tq, H, DV), _BF16, q, stream)
     if lse is None:
-        lse = _empty((Tq, H), torch.float32, dev, stream)
+        lse = _empty((Tq, H), _F32, q, stream)
     rc = lib().kda_latent_prefill(
-        _need("q", q, torch.bfloat16, (Tq, H, DK + LATENT_PE), dev),
-        _need("kv", kv, torch.bfloat16, (Tk, H, DK + DV), dev), k_pe.data_ptr(), pe_stride,
-        _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev),
-        _need("cu_seqlens_k", cu_seqlens_k, torch.int32, (N + 1,), dev), scale, 1 if causal else 0,
-        _need("o", o, torch.bfloat16, (Tq, H, DV), dev), _need("lse", lse, torch.float32, (Tq, H), dev),
+        _need("q", q, _BF16, (Tq, H, DK + LATENT_PE), dev),
+        _need("kv", kv, _BF16, (Tk, H, DK + DV), dev), k_pe.data_ptr(), pe_stride,
+        _need("cu_seqlens", cu_seqlens, _I32, (N + 1,), dev),
+        _need("cu_seqlens_k", cu_seqlens_k, _I32, (N + 1,), dev), scale, 1 if causal else 0,
+        _need("o", o, _BF16, (Tq, H, DV), dev), _need("lse", lse, _F32, (Tq, H), dev),
         N, Tq, Tk, H, DK, LATENT_PE, DV, _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_prefill")

@@ -18,6 +18,15 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
+// Block 0 raises bit 0 for offsets that decrease or leave [0, T] (the rest of
+// the kernel stays inside its buffers whatever they are).
+__device__ __forceinline__ void check_offsets(const int32_t *cu, int N, int T) {
+    if (!cu || blockIdx.x != 0) return;
+    bool bad = false;
+    for (int b = threadIdx.x; b < N; b += blockDim.x) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > T;
+    if (bad) atomicOr(&g_kda_latent_error, kErrWait);
+}
+
 // ---------------------------------------------------------------- append
 // A warp a token: the row's 72 16-byte pieces are read once (lane l holds
 // latent pieces l and 32 + l, lanes 0..7 one of the shared part), the sum of
@@ -49,9 +58,11 @@ __global__ void __launch_bounds__(kAppendThreads)
 latent_append_kernel(const uint4 *__restrict__ x, uint4 *__restrict__ cache, PagedRows pages,
                      const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ cu,
                      const float *__restrict__ norm_w, float eps, int N, int T) {
-    const int t = (int)((blockIdx.x * (unsigned)kAppendThreads + threadIdx.x) >> 5);
+    const int64_t t_of_warp = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (t >= T) return;
+    check_offsets(cu, N, T);
+    if (t_of_warp >= T) return;
+    const int t = (int)t_of_warp;
     // the row does not wait for the walk to its place
     const uint4 *src = x + (size_t)t * kRowChunks;
     uint4 a = __ldcs(src + lane), b = __ldcs(src + 32 + lane), c = make_uint4(0, 0, 0, 0);
@@ -90,8 +101,9 @@ constexpr int kGatherThreads = 256;
 __global__ void __launch_bounds__(kGatherThreads)
 latent_gather_kernel(const uint4 *__restrict__ cache, PagedRows pages, const int32_t *__restrict__ cu,
                      uint4 *__restrict__ out, int N, int T) {
-    const int64_t t0 = 4 * (int64_t)((blockIdx.x * (unsigned)kGatherThreads + threadIdx.x) >> 5);
+    const int64_t t0 = 4 * ((int64_t)blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5));
     const int lane = threadIdx.x & 31;
+    check_offsets(cu, N, T);
     if (t0 >= T) return;
     // source row of output row t0 + lane; -2: no such row, -1: its page is bad
     long long src = -2;

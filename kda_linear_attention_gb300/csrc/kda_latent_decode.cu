@@ -89,10 +89,9 @@ struct Misc {
     int fail;
     int b0, j0, t0;                       // first unit
     Seq seq0;                             // its sequence
-    int32_t units;                        // units of this CTA
     int used;                             // CTAs with units
     long long scan[kThreads / 32 + 1];
-    long long start, total;
+    long long start, units, total;        // this CTA's first unit and units; all units
     // per column (row of the tile), by softmax group
     float red[2][4][32];                  // cross-warp reductions
     alignas(16) float neg_m[2][32];       // minus the running maximum, log2 units
@@ -156,8 +155,8 @@ struct Item {
 // Walks a CTA's units row tile by row tile; every role takes the same walk.
 template <int NR>
 struct Walk {
-    int b, j, t, left;
-    long long u;
+    int b, j, t;
+    long long left, u;
     Seq s;
     __device__ __forceinline__ Walk(const Args &a, const Misc *m)
         : b(m->b0), j(m->j0), t(m->t0), left(m->units), u(m->start) {
@@ -170,7 +169,7 @@ struct Walk {
             s = get_seq<NR>(a, b, false);
             j = t = 0;
         }
-        const int units = min(s.tiles - t, left);
+        const int units = (int)min((long long)(s.tiles - t), left);
         it.b = b;
         it.row_in_seq = j * NR;
         it.row = s.row0 + j * NR;
@@ -286,7 +285,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         const long long u1 = cta < used ? total * (cta + 1) / used : total;
         if (t == 0) {
             M->used = used;
-            M->units = (int)(u1 - u0);
+            M->units = u1 - u0;
             M->start = u0;
             M->total = total;
         }

@@ -183,6 +183,28 @@ def test_gather_ragged(page):
     assert torch.equal(again, out[:cu[-1]])
 
 
+@pytest.mark.parametrize("bad", [[0, 30, 20, 40], [-3, 10, 20, 40], [0, 10, 20, 41]])
+def test_broken_offsets_are_flagged_and_touch_nothing_outside(bad):
+    """Offsets that decrease or leave [0, T]: bit 0 from every call on them,
+    and guard rows around the buffers keep their values."""
+    import torch
+    kda = _kda()
+    c = Paged(16, [40, 40, 40], 16, nan=False)
+    cu = _i32(bad)
+    guard = torch.full((60, ol.ROW), 7.0, dtype=torch.bfloat16, device="cuda")
+    kda.latent_gather(c.dev, c.table_dev, cu, out=guard[10:50])
+    _clear(1)
+    assert (guard[:10] == 7.0).all() and (guard[50:] == 7.0).all()
+    kda.latent_append(guard[10:50], c.dev, c.table_dev, c.lens_dev, cu)
+    _clear(1)
+    q, _ = c.q(40, 4)
+    o = torch.full((60, 4, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((60, 4), 7.0, device="cuda")
+    kda.latent_decode(q, c.dev, c.table_dev, c.lens_dev, cu, o=o[10:50], lse=lse[12:52])
+    _clear(1)
+    assert (o[:10] == 7.0).all() and (o[50:] == 7.0).all() and (lse[:12] == 7.0).all() and (lse[52:] == 7.0).all()
+
+
 def test_gather_reads_zeros_for_a_bad_page():
     import torch
     kda = _kda()
@@ -240,7 +262,8 @@ def test_decode_more_new_tokens_than_positions():
     assert (o[:3] == 0).all() and np.isneginf(_np(lse)[:3]).all()
 
 
-@pytest.mark.parametrize("lens,H,page", [([5000, 1, 2049], 16, 128), ([9001], 64, 16), ([300] * 200, 8, 64)])
+@pytest.mark.parametrize("lens,H,page", [([5000, 1, 2049], 16, 128), ([9001], 64, 16), ([300] * 200, 8, 64),
+                                         ([(37 * i) % 150 for i in range(1000)], 1, 16)])
 def test_decode_split_over_positions(lens, H, page):
     """Few long sequences (each split over the SMs) and many short ones."""
     c = Paged(24, lens, page)
@@ -412,6 +435,69 @@ def test_prefill_takes_strided_shared_keys():
         kda.latent_prefill(q, kv, torch.zeros((170, 68), dtype=torch.bfloat16, device="cuda")[:, :64], _i32(cu))
 
 
+def test_prefill_many_sequences():
+    """More sequences than a block has threads, lengths 0 to 12 and a few long
+    ones among them."""
+    kda = _kda()
+    lens = [(7 * i) % 13 for i in range(1000)]
+    lens[17], lens[640], lens[999] = 300, 513, 129
+    cu, _, (q, kv, pe), (qr, kvr, per) = _prefill_inputs(37, lens, lens, 1)
+    o, lse = kda.latent_prefill(q, kv, pe, _i32(cu))
+    _clear()
+    check(o, lse, ol.prefill(qr, kvr, per, cu, cu, SCALE), "many sequences")
+
+
+def test_prefill_more_work_tiles_than_sms():
+    """Work tiles taken over by running blocks: every head of a batch whose
+    tiles are several times the SMs', against the same heads one at a time."""
+    import torch
+    kda = _kda()
+    lens, H = [1, 700, 260, 1300], 64
+    cu, _, (q, kv, pe), _ = _prefill_inputs(38, lens, lens, H)
+    cu = _i32(cu)
+    o, lse = kda.latent_prefill(q, kv, pe, cu)
+    for h in (0, 31, 63):
+        oh, lh = kda.latent_prefill(q[:, h:h + 1].contiguous(), kv[:, h:h + 1].contiguous(), pe, cu)
+        assert torch.equal(oh[:, 0], o[:, h]) and torch.equal(lh[:, 0], lse[:, h])
+    for _ in range(3):
+        o2, lse2 = kda.latent_prefill(q, kv, pe, cu)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    _clear()
+
+
+def test_prefill_output_without_wide_alignment():
+    """An output that starts on a 16-byte boundary but not on a 32-byte one."""
+    import torch
+    kda = _kda()
+    cu, _, (q, kv, pe), _ = _prefill_inputs(39, [150], [150], 2)
+    want, _ = kda.latent_prefill(q, kv, pe, _i32(cu))
+    flat = torch.empty(150 * 2 * 128 + 8, dtype=torch.bfloat16, device="cuda")
+    o = flat[8:].view(150, 2, 128)
+    assert o.data_ptr() % 32 == 16
+    kda.latent_prefill(q, kv, pe, _i32(cu), o=o)
+    _clear()
+    assert torch.equal(o, want)
+
+
+def test_prefill_captured_and_replayed():
+    import torch
+    kda = _kda()
+    cu, _, (q, kv, pe), _ = _prefill_inputs(40, [300, 77], [300, 77], 4)
+    cu = _i32(cu)
+    o, lse = kda.latent_prefill(q, kv, pe, cu)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kda.latent_prefill(q, kv, pe, cu, o=o, lse=lse)
+    for seed in (1, 2):
+        nq, nkv = _prefill_inputs(50 + seed, [300, 77], [300, 77], 4)[2][:2]
+        q.copy_(nq)
+        kv.copy_(nkv)
+        g.replay()
+        want = kda.latent_prefill(nq, nkv, pe, cu)
+        _clear()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 def test_prefill_flags_bad_offsets():
     kda = _kda()
     cu, _, (q, kv, pe), _ = _prefill_inputs(36, [40], [40], 1)
@@ -517,6 +603,54 @@ def test_calls_on_another_stream():
     _clear()
     for o, lse in got:
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_two_streams_at_once():
+    """Decode and prefill calls of two streams in flight together, each with
+    its own workspace, give what they give alone."""
+    import torch
+    kda = _kda()
+    c = Paged(45, [3000, 300, 64], 64)
+    q, _ = c.q(3, 48)
+    want = _decode(c, q, None)
+    cu, _, (pq, kv, pe), _ = _prefill_inputs(46, [900, 40], [900, 40], 16)
+    cu = _i32(cu)
+    pwant = kda.latent_prefill(pq, kv, pe, cu)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got, pgot = [], []
+    for _ in range(5):
+        for s in streams:
+            got.append(_decode(c, q, None, stream=s))
+            pgot.append(kda.latent_prefill(pq, kv, pe, cu, stream=s))
+    _clear()
+    for o, lse in got:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    for o, lse in pgot:
+        assert torch.equal(o, pwant[0]) and torch.equal(lse, pwant[1])
+
+
+def test_c_entries_take_no_lse():
+    import torch
+    kda = _kda()
+    c = Paged(47, [300, 5], 64)
+    q, _ = c.q(2, 4)
+    want, _ = _decode(c, q, None)
+    o = torch.empty_like(want)
+    n = kda.latent_decode_workspace_bytes(2, 2, 4)
+    ws = torch.empty((n,), dtype=torch.uint8, device="cuda")
+    st = torch.cuda.current_stream().cuda_stream
+    assert kda.lib().kda_latent_decode(q.data_ptr(), c.dev.data_ptr(), c.table_dev.data_ptr(), c.lens_dev.data_ptr(),
+                                       None, SCALE, o.data_ptr(), None, 2, 2, 4, c.P, 64, c.table.shape[1], 512, 64,
+                                       ws.data_ptr(), n, st) == 0
+    cu, _, (pq, kv, pe), _ = _prefill_inputs(48, [140], [140], 2)
+    cu = _i32(cu)
+    pwant, _ = kda.latent_prefill(pq, kv, pe, cu)
+    po = torch.empty_like(pwant)
+    assert kda.lib().kda_latent_prefill(pq.data_ptr(), kv.data_ptr(), pe.data_ptr(), 64, cu.data_ptr(), cu.data_ptr(),
+                                        SCALE, 1, po.data_ptr(), None, 1, 140, 140, 2, 128, 64, 128, st) == 0
+    _clear()
+    assert torch.equal(o, want) and torch.equal(po, pwant)
 
 
 def test_binding_refuses_wrong_tensors():
