@@ -18,8 +18,9 @@
 //
 // Work is cut in units of (sequence, row tile, 128 positions); CTA c of G
 // (one an SM) takes units c W / G .. (c + 1) W / G, so every SM has the same
-// number of units whatever the lengths are.  A CTA's first and last row tile
-// may be pieces of longer ones: pieces are written normalised in fp32 with
+// number of units whatever the lengths are.  (The row tiles of one token of
+// many heads are taken side by side, by groups of CTAs that share the units'
+// numbering.)  A CTA's first and last row tile may be pieces of longer ones: pieces are written normalised in fp32 with
 // their log2-sum-exp into the workspace, and a second kernel joins them in the
 // order of the positions (no atomics: the same bits every time).
 //
@@ -45,6 +46,7 @@ namespace {
 
 constexpr int kTile = 128;                // positions a unit
 constexpr int kMaxCtas = 160;             // grid bound (one CTA an SM; 152 SMs)
+constexpr int kMaxSide = 8;               // row tiles of a token that CTAs take side by side
 constexpr int kSoftWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + 2);
 constexpr int kSoftThreads = 32 * kSoftWarps;
@@ -59,7 +61,7 @@ constexpr uint32_t TM_S = 0, TM_O = 64;   // S^T: 64 columns; O^T: 4 blocks of 6
 struct Split {
     int32_t row;                          // first row (flat over [T * H])
     int32_t rows;                         // rows of the tile; 0: nothing
-    int32_t last;                         // the CTA that holds the last piece
+    int32_t pieces;                       // of it: here and in the CTAs `side` further on each
     int32_t pad;
 };
 
@@ -89,7 +91,7 @@ struct Misc {
     int fail;
     int b0, j0, t0;                       // first unit
     Seq seq0;                             // its sequence
-    int used;                             // CTAs with units
+    int used;                             // groups with units
     long long scan[kThreads / 32 + 1];
     long long start, units, total;        // this CTA's first unit and units; all units
     // per column (row of the tile), by softmax group
@@ -105,6 +107,7 @@ struct Args {
     PagedRows pages;
     const int32_t *seq_lens, *cu;
     int N, T, H;
+    int side;                             // CTAs side by side: row tiles of a token (one token a sequence)
     float scale_log2;                     // scale * log2 e
     __nv_bfloat16 *o;
     float *lse;
@@ -115,6 +118,7 @@ struct Args {
 
 template <int NR>
 __device__ __forceinline__ Seq get_seq(const Args &a, int b, bool flag) {
+    const int j = blockIdx.x % a.side;    // with side > 1 every CTA knows its row tile only
     Seq s;
     int t0 = b, n = 1;
     bool bad = false;
@@ -132,8 +136,8 @@ __device__ __forceinline__ Seq get_seq(const Args &a, int b, bool flag) {
         L = max(0, min(L, most));
     }
     if (bad && flag) atomicOr(&g_kda_latent_decode_error, kErrWait);
-    s.row0 = t0 * a.H;
-    s.rows = n * a.H;
+    s.row0 = t0 * a.H + j * NR;
+    s.rows = a.side > 1 ? min(NR, a.H - j * NR) : n * a.H;
     s.first = L - n + 1;
     s.len = L;
     s.tiles = max(1, (L + kTile - 1) / kTile);
@@ -235,7 +239,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Misc *M = reinterpret_cast<Misc *>(sm + F::MISC);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int G = gridDim.x, cta = blockIdx.x;
+    const int cta = blockIdx.x, side = a.side;
+    const int G = gridDim.x / side, group = cta / side;   // groups of CTAs side by side
 
     // ---- this CTA's units: a block-wide scan of the sequences' units
     {
@@ -279,10 +284,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             if (w < warp) before += M->scan[w];
             total += M->scan[w];
         }
-        // no CTA between a row tile's pieces is without one: with fewer units than CTAs, one each
+        // no group between a row tile's pieces is without one: with fewer units than groups, one each
         const int used = (int)min((long long)G, total);
-        const long long u0 = cta < used ? total * cta / used : total;
-        const long long u1 = cta < used ? total * (cta + 1) / used : total;
+        const long long u0 = group < used ? total * group / used : total;
+        const long long u1 = group < used ? total * (group + 1) / used : total;
         if (t == 0) {
             M->used = used;
             M->units = u1 - u0;
@@ -653,10 +658,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             tc_fence_before();
             // the tile that starts here and goes on: who holds its last piece
             if (t == 0 && it.head && !it.tail) {
-                // CTA c holds unit u when c W / G <= u < (c + 1) W / G (rounded down), so the
+                // group c holds unit u when c W / G <= u < (c + 1) W / G (rounded down), so the
                 // last c with c W / G < u + 1
                 const long long last = it.unit + it.tiles - 1;
-                a.split[cta] = Split{it.row, it.rows, (int)(((last + 1) * M->used - 1) / M->total), 0};
+                a.split[cta] = Split{it.row, it.rows, (int)(((last + 1) * M->used - 1) / M->total) - group + 1, 0};
             }
         }
         if (!ok && t == 0) atomicOr(&g_kda_latent_decode_error, kErrWait);
@@ -684,7 +689,7 @@ static_assert(kJoinThreads >= kMaxCtas, "a thread a record");
 __global__ void __launch_bounds__(kJoinThreads)
 latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws_lse,
                    const float *__restrict__ ws_o, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
-                   int NR, int G) {
+                   int NR, int ctas, int side) {
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     __shared__ float4 part[kJoinWarps][kLatent / 4];
     __shared__ Split rec[kMaxCtas];
@@ -693,12 +698,11 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces are written
     {
         Split sp{0, 0, 0, 0};
-        if (t < G) {
+        if (t < ctas) {
             sp = split[t];
             rec[t] = sp;
         }
-        const int n = sp.last - t + 1;
-        int incl = sp.rows == 0 ? 0 : n <= kJoinAlone ? (sp.rows + kJoinWarps - 1) / kJoinWarps : sp.rows;
+        int incl = sp.rows == 0 ? 0 : sp.pieces <= kJoinAlone ? (sp.rows + kJoinWarps - 1) / kJoinWarps : sp.rows;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, off);
@@ -719,11 +723,11 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
             else c = mid + 1;
         }
         const Split sp = rec[c];
-        const int n = sp.last - c + 1, in = u - (c > 0 ? upto[c - 1] : 0);
+        const int n = sp.pieces, in = u - (c > 0 ? upto[c - 1] : 0);
         const bool alone = n <= kJoinAlone;
         const int r = alone ? in * kJoinWarps + warp : in;
         if (alone && r >= sp.rows) continue;
-        auto slot = [&](int k) { return k == 0 ? 2 * c + 1 : 2 * (c + k); };
+        auto slot = [&](int k) { return k == 0 ? 2 * c + 1 : 2 * (c + k * side); };
         // every warp finds the maximum and the sum by itself
         float v[kMaxCtas / 32], mx = -CUDART_INF_F, sum = 0.f;
 #pragma unroll
@@ -827,7 +831,7 @@ cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const void *cac
     cfg.attrs = &early;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, latent_join_kernel, (const Split *)a.split, (const float *)a.ws_lse,
-                              (const float *)a.ws_o, a.o, a.lse, NR, G);
+                              (const float *)a.ws_o, a.o, a.lse, NR, G, a.side);
 }
 
 }  // namespace
@@ -855,6 +859,10 @@ cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t
     a.N = N;
     a.T = (int)T;
     a.H = H;
+    // One token a sequence and more heads than a tile's rows: the row tiles of a sequence are taken
+    // by neighbouring CTAs at the same time, so that its cached rows come from HBM once.
+    const int row_tiles = cu ? 1 : (H + NR - 1) / NR;
+    a.side = row_tiles <= kMaxSide ? row_tiles : 1;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.o = static_cast<__nv_bfloat16 *>(o);
     a.lse = lse;

@@ -235,6 +235,18 @@ def test_decode_one_token(H, page):
     check(o, lse, r, "decode H=%d" % H)
 
 
+@pytest.mark.parametrize("H", [130, 200, 530])
+def test_decode_many_heads(H):
+    """Three and four row tiles a token, taken side by side, and nine, which
+    one CTA takes in turn."""
+    lens = [1000, 3, 0, 129, 640]
+    c = Paged(30, lens, 64)
+    q, qr = c.q(len(lens), H)
+    o, lse = _decode(c, q, None)
+    _clear()
+    check(o, lse, ol.decode(qr, c.ref, c.table, lens, np.arange(len(lens) + 1), SCALE), "decode H=%d" % H)
+
+
 @pytest.mark.parametrize("H", [1, 5, 16, 96])
 def test_decode_ragged_new_tokens(H):
     lens = [5, 130, 0, 64, 257, 3, 128, 140]
