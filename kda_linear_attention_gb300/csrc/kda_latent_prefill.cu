@@ -25,6 +25,7 @@
 // feeds a ring of eight 16 KB slots (three a key tile, two a value tile: 1.6
 // tiles in flight).  TMEM: S_0, S_1, O_0, O_1, 128 columns each.
 #include <algorithm>
+#include <type_traits>
 
 #include "latent_tc.cuh"
 
@@ -51,11 +52,21 @@ constexpr float kMoveAt = 8.f;            // log2 of the factor a score may pass
 constexpr uint32_t TM_S = 0, TM_O = 256;
 constexpr int64_t kL2Bytes = 48 << 20;    // keys and values of the heads listed together
 
+struct Work {
+    int valid;                            // 0: there is none
+    int h, q0, k0, nk;                    // head; first token of the sequence's queries; of its keys, and keys
+    int i0;                               // first query of the tile
+    int rows[2];                          // queries of each half
+    int n[2];                             // key tiles each half sees any of
+    int first;                            // keys that the sequence's query 0 sees (may be <= 0)
+};
+
 struct Misc {
     uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2];   // by key tile, even and odd
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], done;
-    uint64_t work_full[2], work_empty[2];
-    alignas(16) uint4 work[2];            // answers to the requests for a further work tile
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], done;
+    uint64_t answer_full, work_full[2], work_empty[2];
+    alignas(16) uint4 answer;             // to the request for a further work tile
+    Work work[2];                         // the copy warp's, for the other roles
     uint32_t tmem;
     int fail;
     int tiles;                            // work tiles of all sequences (of one head)
@@ -86,24 +97,17 @@ __device__ __forceinline__ int queries_of(const Args &a, int b, bool flag) {
     return bad ? 0 : t1 - t0;
 }
 
-struct Work {
-    int h, q0, nq, k0, nk;                // head; first token and tokens of the sequence's queries and keys
-    int i0;                               // first query of the tile
-    int rows[2];                          // queries of each half
-    int n[2];                             // key tiles each half sees any of
-    int first;                            // keys that the sequence's query 0 sees (may be <= 0)
-};
-
 // Work tile `id` of the grid.  Heads are listed in groups whose keys and
 // values fit in L2 together; in a group, from the tiles of the last queries
 // (which see the most keys) to those of the first, so that what is handed out
 // last is short.
-__device__ __forceinline__ bool get_work(const Args &a, const Misc *M, unsigned id, Work &w) {
+__device__ __forceinline__ void get_work(const Args &a, const Misc *M, int id, Work &w) {
     const int tiles = M->tiles;
-    if (id >= (unsigned)tiles * (unsigned)a.H) return false;
-    const unsigned group = id / ((unsigned)tiles * a.heads_together);
+    w.valid = id >= 0 && (unsigned)id < (unsigned)tiles * (unsigned)a.H;
+    if (!w.valid) return;
+    const unsigned group = (unsigned)id / ((unsigned)tiles * a.heads_together);
     const int h0 = group * a.heads_together, heads = min(a.heads_together, a.H - h0);
-    const int in = (int)(id - group * tiles * a.heads_together);
+    const int in = (int)((unsigned)id - group * tiles * a.heads_together);
     w.h = h0 + in % heads;
     int k = tiles - 1 - in / heads;
     // the thread whose sequences hold tile k, then the sequence
@@ -120,7 +124,6 @@ __device__ __forceinline__ bool get_work(const Args &a, const Misc *M, unsigned 
         k -= (nq + kTileQ - 1) / kTileQ;
         nq = queries_of(a, ++b, false);
     }
-    w.nq = nq;
     w.q0 = a.cu_q[b];
     w.k0 = a.cu_k[b];
     w.nk = a.cu_k[b + 1] - w.k0;
@@ -133,7 +136,6 @@ __device__ __forceinline__ bool get_work(const Args &a, const Misc *M, unsigned 
         const int sees = a.causal ? max(0, w.first + w.i0 + g * kHalf + w.rows[g] - 1) : w.nk;
         w.n[g] = w.rows[g] > 0 ? (sees + kTileK - 1) / kTileK : 0;
     }
-    return true;
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -174,19 +176,19 @@ __device__ __forceinline__ int taken_work(const uint4 *answer) {
         : "memory");
     return ok ? (int)x : -1;
 }
-// One role's walk over the CTA's work tiles, by whole warps: its own block
-// index first, then what the copy warp's requests bring.
+// The other roles' walk over the CTA's work tiles, by whole warps: the copy
+// warp finds out what they are (a search and a few dependent loads, 2,500
+// cycles) while the tile before is computed.
 struct Tiles {
     uint32_t r = 0;
-    int id;
-    __device__ __forceinline__ Tiles() : id((int)blockIdx.x) {}
-    __device__ __forceinline__ void step(Misc *M, bool &ok, volatile int *fail) {
+    __device__ __forceinline__ bool next(Misc *M, Work &w, bool &ok, volatile int *fail) {
         const uint32_t at = r & 1;
         ok = ok && warp_wait(&M->work_full[at], (r >> 1) & 1, fail);
-        id = ok ? taken_work(&M->work[at]) : -1;
-        fence_proxy_async_smem();         // read before a later request writes there
+        if (!ok) return false;
+        w = M->work[at];
         warp_arrive(&M->work_empty[at]);
         ++r;
+        return w.valid;
     }
 };
 
@@ -235,17 +237,18 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 mbar_init(&M->k_empty[i], 1);
                 mbar_init(&M->v_empty[i], 1);
             }
-            mbar_init(&M->q_full, 1);
-            mbar_init(&M->q_empty, 1);
             for (int g = 0; g < 2; ++g) {
+                mbar_init(&M->q_full[g], 1);
+                mbar_init(&M->q_empty[g], 1);
                 mbar_init(&M->s_full[g], 1);
                 mbar_init(&M->p_full[g], 4);      // warps of a group
                 mbar_init(&M->o_full[g], 1);
             }
             mbar_init(&M->done, 1);
+            mbar_init(&M->answer_full, 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&M->work_full[i], 1);
-                mbar_init(&M->work_empty[i], kThreads / 32);
+                mbar_init(&M->work_empty[i], kThreads / 32 - 1);
             }
             fence_mbar_init();
         }
@@ -271,7 +274,6 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     const uint32_t tmem = M->tmem;
     volatile int *fail = &M->fail;
     Work w;
-    Tiles tiles;
 
     if (warp == 9) {
         // ================================================= copies
@@ -279,28 +281,60 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         // The key slots were last the third of key tile u - 2 and both of its value tile, the value
         // slots the first two of key tile u - 1; the MMA warp releases in the order of u.
         uint32_t u = 0;                           // key tiles asked for
-        uint32_t n_v = 0, n_work = 0, asked = 0;  // value tiles, Q tiles, further work tiles
+        uint32_t n_v = 0, asked = 0, told = 0;    // value tiles, further work tiles, work tiles
+        uint32_t n_q[2] = {0, 0};                 // query halves
         bool ok = true;
-        for (; ok && tiles.id >= 0 && get_work(a, M, tiles.id, w); tiles.step(M, ok, fail)) {
-            // the next work tile's request; its answer is there long before this one is done
-            if (tiles.r >= 2) ok = warp_wait(&M->work_empty[tiles.r & 1], ((tiles.r >> 1) - 1) & 1, fail);
-            if (!ok) break;
-            if (lane == 0) ask_work(&M->work[tiles.r & 1], &M->work_full[tiles.r & 1]);
+        auto tell = [&](const Work &x) {          // the other roles, of a work tile (or that none is left)
+            const uint32_t at = told & 1;
+            if (told >= 2) ok = ok && warp_wait(&M->work_empty[at], ((told >> 1) - 1) & 1, fail);
+            if (!ok) return;
+            ++told;
+            if (lane == 0) {
+                M->work[at] = x;
+                mbar_arrive(&M->work_full[at]);
+            }
+            __syncwarp();
+            // its queries toward L2 while the tile before still holds their place
+            if (x.valid && lane < 6 && (lane < 3 ? x.n[0] : x.n[1]) > 0)
+                tma_prefetch_l2_3d(&map_q, 64 * (lane % 3), x.h, x.q0 + x.i0 + (lane / 3) * kHalf);
+            __syncwarp();
+        };
+        get_work(a, M, (int)blockIdx.x, w);
+        tell(w);
+        while (ok && w.valid) {
+            // the next work tile: asked for here, known a few key tiles on
+            if (lane == 0) ask_work(&M->answer, &M->answer_full);
             ++asked;
             __syncwarp();
+            Work next;
+            bool known = false;
+            auto learn = [&]() {
+                if (known) return;
+                known = true;
+                ok = ok && warp_wait(&M->answer_full, (asked - 1) & 1, fail);
+                if (!ok) return;
+                get_work(a, M, taken_work(&M->answer), next);
+                fence_proxy_async_smem();         // read before the next answer is written there
+                __syncwarp();
+                tell(next);
+            };
             const int n = max(w.n[0], w.n[1]);
-            if (n == 0) continue;
-            if (n_work > 0) ok = warp_wait(&M->q_empty, (n_work - 1) & 1, fail);
-            if (!ok) break;
-            ++n_work;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&M->q_full, (w.n[0] > 0 ? 3 * kSlot : 0) + (w.n[1] > 0 ? 3 * kSlot : 0));
-                for (int g = 0; g < 2; ++g)
-                    for (int c = 0; w.n[g] > 0 && c < 3; ++c)
-                        tma_load_3d(sm + SM_Q + (3 * g + c) * kSlot, &map_q, &M->q_full, 64 * c, w.h,
+            // half g's queries, once the tile before is done with theirs
+            auto queries = [&](int g) {
+                if (w.n[g] == 0) return;
+                if (n_q[g] > 0) ok = ok && warp_wait(&M->q_empty[g], (n_q[g] - 1) & 1, fail);
+                if (!ok) return;
+                ++n_q[g];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&M->q_full[g], 3 * kSlot);
+                    for (int c = 0; c < 3; ++c)
+                        tma_load_3d(sm + SM_Q + (3 * g + c) * kSlot, &map_q, &M->q_full[g], 64 * c, w.h,
                                     w.q0 + w.i0 + g * kHalf);
-            }
-            for (int i = 0; i < n; ++i) {
+                }
+                __syncwarp();
+            };
+            if (n > 0) queries(0);
+            for (int i = 0; ok && i < n; ++i) {
                 const int tok = w.k0 + i * kTileK;
                 auto slot = [&](int c) { return sm + SM_RING + ((5 * n_v + c) % kSlots) * kSlot; };
                 if (u >= 2) ok = warp_wait(&M->v_empty[u & 1], ((u >> 1) - 1) & 1, fail);
@@ -314,6 +348,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 }
                 __syncwarp();
                 ++u;
+                if (i == 0) queries(1);
+                if (!ok) break;
                 if (n_v >= 1) ok = warp_wait(&M->k_empty[(n_v - 1) & 1], ((n_v - 1) >> 1) & 1, fail);
                 if (!ok) break;
                 if (lane == 0) {
@@ -327,7 +363,10 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 }
                 __syncwarp();
                 ++n_v;
+                if (i == 1) learn();
             }
+            learn();
+            w = next;
         }
         if (!__all_sync(0xffffffffu, ok) || *fail) {
             // given up: what was asked for still has to land before the block may end
@@ -335,10 +374,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 for (uint32_t i = uses > bars ? uses - bars : 0; i < uses; ++i)
                     mbar_wait(bar + i % bars, (i / bars) & 1, kWaitLimit);
             };
-            land(&M->q_full, n_work, 1);
+            land(&M->q_full[0], n_q[0], 1);
+            land(&M->q_full[1], n_q[1], 1);
             land(M->k_full, u, 2);
             land(M->v_full, n_v, 2);
-            land(M->work_full, asked, 2);
+            land(&M->answer_full, asked, 1);
         }
     } else if (warp == 8) {
         // ================================================= matrix products
@@ -350,8 +390,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         const uint32_t k_full = smem_u32(M->k_full), v_full = smem_u32(M->v_full);
         const uint32_t k_empty = smem_u32(M->k_empty), v_empty = smem_u32(M->v_empty);
         const uint32_t s_full = smem_u32(M->s_full), p_full = smem_u32(M->p_full), o_full = smem_u32(M->o_full);
-        const uint32_t q_empty = smem_u32(&M->q_empty);
-        uint32_t u = 0, n_work = 0, cnt0 = 0, cnt1 = 0;   // key tiles, work tiles, tiles of each half
+        const uint32_t q_full = smem_u32(M->q_full), q_empty = smem_u32(M->q_empty);
+        uint32_t u = 0, cnt0 = 0, cnt1 = 0;               // key tiles, tiles of each half
+        uint32_t nq0 = 0, nq1 = 0;                        // query halves
         bool ok = true;
         auto scores = [&](int g, uint32_t tile) {         // one lane
 #pragma unroll
@@ -375,18 +416,34 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                            acc || c > 0 || e > 0);
             }
         };
-        for (; ok && tiles.id >= 0 && get_work(a, M, tiles.id, w); tiles.step(M, ok, fail)) {
+        // half 0's first scores of a work tile, whose first key tile is `tile`
+        auto first_scores = [&](int n0, uint32_t tile) {
+            ok &= wait_or_fail(q_full, nq0++ & 1, fail);
+            ok &= wait_or_fail(k_full + 8 * (tile & 1), (tile >> 1) & 1, fail);
+            tc_fence_after();
+            if (elect_one()) {
+                scores(0, tile);
+                if (n0 == 1) commit(q_empty);
+            }
+            __syncwarp();
+        };
+        Tiles tiles;
+        bool more = tiles.next(M, w, ok, fail), begun = false;
+        while (more && __all_sync(0xffffffffu, ok)) {
             const int n0 = w.n[0], n1 = w.n[1], n = max(n0, n1);
-            if (n == 0) continue;
-            ok &= wait_or_fail(&M->q_full, n_work & 1, fail);
-            ++n_work;
+            if (n == 0) {
+                more = tiles.next(M, w, ok, fail);
+                continue;
+            }
+            if (n0 > 0 && !begun) first_scores(n0, u);
+            begun = false;
+            if (n1 > 0) ok &= wait_or_fail(q_full + 8, nq1++ & 1, fail);
             ok &= wait_or_fail(k_full + 8 * (u & 1), (u >> 1) & 1, fail);
             tc_fence_after();
             if (elect_one()) {
-                if (n0 > 0) scores(0, u);
                 if (n1 > 0) scores(1, u);
+                if (n1 == 1) commit(q_empty + 8);
                 commit(k_empty + 8 * (u & 1));
-                if (n == 1) commit(q_empty);
             }
             __syncwarp();
             for (int i = 0; i < n; ++i, ++u) {
@@ -402,10 +459,22 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     if (i + 1 == n0) commit(o_full);
                 }
                 __syncwarp();
-                if (i + 1 < n) ok &= wait_or_fail(k_full + 8 * (x & 1), (x >> 1) & 1, fail);
-                tc_fence_after();
-                if (i + 1 < n0 && elect_one()) scores(0, x);
-                __syncwarp();
+                if (i + 1 < n) {
+                    ok &= wait_or_fail(k_full + 8 * (x & 1), (x >> 1) & 1, fail);
+                    tc_fence_after();
+                    if (i + 1 < n0 && elect_one()) {
+                        scores(0, x);
+                        if (i + 2 == n0) commit(q_empty);
+                    }
+                    __syncwarp();
+                } else {
+                    // the last key tile: half 0 begins the next work tile while half 1 ends this one
+                    more = tiles.next(M, w, ok, fail);
+                    if (more && w.n[0] > 0) {
+                        first_scores(w.n[0], x);
+                        begun = true;
+                    }
+                }
                 if (i < n1) ok &= wait_or_fail(p_full + 8, cnt1++ & 1, fail);
                 tc_fence_after();
                 if (elect_one()) {
@@ -415,8 +484,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     }
                     commit(v_empty + 8 * (u & 1));
                     if (i + 1 < n1) scores(1, x);
+                    if (i + 2 == n1) commit(q_empty + 8);
                     if (i + 1 < n) commit(k_empty + 8 * (x & 1));
-                    if (i + 2 == n) commit(q_empty);
                 }
                 __syncwarp();
             }
@@ -433,8 +502,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
         uint32_t cnt = 0, n_out = 0, u = 0;
         bool ok = true;
-        for (; ok && tiles.id >= 0 && get_work(a, M, tiles.id, w); tiles.step(M, ok, fail)) {
-            const int rows = w.rows[g], n = w.n[g];
+        Tiles tiles;
+        while (ok && tiles.next(M, w, ok, fail)) {
+            const int rows = g ? w.rows[1] : w.rows[0], n = g ? w.n[1] : w.n[0];
             const int n_all = max(w.n[0], w.n[1]);
             if (rows == 0) { u += n_all; continue; }
             const int i_row = w.i0 + g * kHalf + row;     // query of the sequence
@@ -450,7 +520,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 uint32_t p[64];
                 float top, sum;
                 // p and their sum from the row's present maximum; the largest exponent
-                auto weights = [&]() {
+                auto weights = [&](auto with_mask) {
+                    constexpr bool kMask = decltype(with_mask)::value;
                     const float2 nm2 = make_float2(neg_m, neg_m);
                     float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
                     float tp = -CUDART_INF_F;
@@ -462,7 +533,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
                             float2 d = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, nm2);
-                            if (masked) {
+                            if (kMask) {
                                 if (32 * ch + c >= lim) d.x = -CUDART_INF_F;
                                 if (32 * ch + c + 1 >= lim) d.y = -CUDART_INF_F;
                             }
@@ -476,8 +547,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     top = tp;
                     sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
                 };
-                // a new maximum: the first tile sets it, later ones raise it (and rescale O and
-                // the sum).  A row that sees nothing in the first tile sees nothing at all
+                // a new maximum: in the first tile the tile's own, later only a larger one (and O
+                // and the sum are rescaled).  A row that sees nothing in the first tile sees
+                // nothing at all
                 auto move = [&]() {
                     float mx = -CUDART_INF_F;
 #pragma unroll 1
@@ -510,11 +582,26 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                         tmem_wait_st();
                     }
                 };
-                if (i == 0) move();
-                weights();
-                if (i > 0 && __any_sync(0xffffffffu, top > kMoveAt)) {
+                auto weigh = [&]() {
+                    if (masked) weights(std::true_type{});
+                    else weights(std::false_type{});
+                };
+                if (i == 0) {
+                    // a first maximum from 32 of the columns: the others seldom pass it by kMoveAt.
+                    // A row that sees none of them sees nothing
+                    uint32_t s[32];
+                    tmem_ld32(ts, s);
+                    tmem_wait_ld();
+                    float mx = -CUDART_INF_F;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        mx = fmaxf(mx, c >= lim ? -CUDART_INF_F : __uint_as_float(s[c]) * a.scale_log2);
+                    neg_m = mx == -CUDART_INF_F ? 0.f : -mx;
+                }
+                weigh();
+                if (__any_sync(0xffffffffu, top > kMoveAt)) {
                     move();
-                    weights();
+                    weigh();
                 }
                 l += sum;
 #pragma unroll
