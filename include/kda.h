@@ -481,13 +481,22 @@ size_t kda_latent_decode_workspace_bytes(int N, int64_t T, int H, int d_latent, 
  *   o          [Tq, H, 128] bf16, written
  *   lse        [Tq, H] fp32, written, or NULL
  *   d_nope, d_pe, dv   must be 128, 64, 128
+ *   workspace  kda_latent_prefill_workspace_bytes(...) bytes of device memory,
+ *              256-byte aligned, alive and unshared until the call's kernels
+ *              finish; nothing in it has to be initialised.  Few queries over
+ *              many keys need some (their keys are cut into pieces that are
+ *              joined); NULL is accepted where the size is 0
  * The keys and values of every sequence are finite.  Returns KDA_OK or a
  * kda_status_t; Tq = 0 is a no-op.
  */
 int kda_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t k_pe_stride,
                        const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, float scale,
                        int causal, void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
-                       int d_nope, int d_pe, int dv, void *stream);
+                       int d_nope, int d_pe, int dv, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace of kda_latent_prefill (0 where it needs none and for
+ * invalid sizes). */
+size_t kda_latent_prefill_workspace_bytes(int N, int64_t Tq, int64_t Tk, int H, int d_nope, int d_pe, int dv);
 
 /*
  * Gives back the memory that the library's workspace pool on the current

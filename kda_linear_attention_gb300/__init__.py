@@ -44,7 +44,8 @@ __all__ = ["prefill_chunked", "prefill_chunked_noalloc", "prefill_chunked_events
            "prefill_workspace_bytes", "decode_step",
            "decode_step_pool", "conv_prologue", "prefill_chunked_gated", "prefill_layer",
            "decode_layer_step", "latent_append", "latent_gather", "latent_decode",
-           "latent_decode_workspace_bytes", "latent_prefill", "device_error", "lib",
+           "latent_decode_workspace_bytes", "latent_prefill", "latent_prefill_workspace_bytes",
+           "device_error", "lib",
            "KDAError", "KDA_BF16", "KDA_F32", "library_path"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -129,8 +130,10 @@ def lib() -> ctypes.CDLL:
         L.kda_latent_decode_workspace_bytes.argtypes = [i32, i64, i32, i32, i32]
         L.kda_latent_decode_workspace_bytes.restype = ctypes.c_size_t
         L.kda_latent_prefill.argtypes = [vp, vp, vp, i64, vp, vp, f32, i32, vp, vp, i32, i64, i64,
-                                         i32, i32, i32, i32, vp]
+                                         i32, i32, i32, i32, vp, ctypes.c_size_t, vp]
         L.kda_latent_prefill.restype = i32
+        L.kda_latent_prefill_workspace_bytes.argtypes = [i32, i64, i64, i32, i32, i32, i32]
+        L.kda_latent_prefill_workspace_bytes.restype = ctypes.c_size_t
         L.kda_workspace_release.argtypes = []
         L.kda_workspace_release.restype = i32
         L.kda_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
@@ -556,6 +559,15 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _workspace(given, need, like, stream):
+    """(tensor or None, its bytes): the caller's, or one of `need` bytes."""
+    if given is None:
+        return (_empty((need,), _U8, like, stream), need) if need else (None, 0)
+    if given.get_device() != like.get_device() or not given.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return given, given.numel() * given.element_size()
+
+
 def latent_append(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
                   seq_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
                   norm_w: Optional[torch.Tensor] = None, eps: float = NORM_EPS,
@@ -641,29 +653,29 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         o = _empty((T, H, LATENT), _BF16, q, stream)
     if lse is None:
         lse = _empty((T, H), _F32, q, stream)
-    if workspace is None:
-        nbytes = latent_decode_workspace_bytes(N, T, H)
-        workspace = _empty((nbytes,), _U8, q, stream) if nbytes else None
-    else:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-        nbytes = workspace.numel() * workspace.element_size()
+    ws, nbytes = _workspace(workspace, latent_decode_workspace_bytes(N, T, H), q, stream)
     rc = lib().kda_latent_decode(
         _need("q", q, _BF16, (T, H, LATENT_ROW), dev), c, table,
         _need("seq_lens", seq_lens, _I32, (N,), dev),
         None if cu_seqlens is None else _need("cu_seqlens", cu_seqlens, _I32, (N + 1,), dev),
         scale, _need("o", o, _BF16, (T, H, LATENT), dev), _need("lse", lse, _F32, (T, H), dev),
         N, T, H, P, page, pages, LATENT, LATENT_PE,
-        None if workspace is None else workspace.data_ptr(), nbytes, _raw_stream(dev, stream))
+        None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_decode")
     return o, lse
 
 
+@functools.lru_cache(maxsize=1024)
+def latent_prefill_workspace_bytes(N: int, Tq: int, Tk: int, H: int) -> int:
+    """Bytes of workspace of ``latent_prefill`` (``kda_latent_prefill_workspace_bytes``)."""
+    return int(lib().kda_latent_prefill_workspace_bytes(int(N), int(Tq), int(Tk), int(H), DK, LATENT_PE, DV))
+
+
 def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seqlens: torch.Tensor,
                    cu_seqlens_k: Optional[torch.Tensor] = None, scale: float = LATENT_SCALE,
                    causal: bool = True, o: Optional[torch.Tensor] = None,
-                   lse: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Expanded attention of new tokens over their sequence's keys and values
     (``kda_latent_prefill``).
@@ -673,12 +685,13 @@ def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seq
     ``rows[:, 512:]`` of gathered cache rows is taken as it is); cu_seqlens
     and cu_seqlens_k [N + 1] int32 (None: the same).  The queries of a
     sequence are its last tokens.  Returns (o [Tq, H, 128] bf16, lse [Tq, H]
-    fp32).
+    fp32).  The workspace (``latent_prefill_workspace_bytes``, often none)
+    comes from torch's allocator unless one is given.
     """
     dev = _device(q)
     if dev != torch.cuda.current_device():      # a launch goes to the current device
         with torch.cuda.device(dev):
-            return latent_prefill(q, kv, k_pe, cu_seqlens, cu_seqlens_k, scale, causal, o, lse, stream)
+            return latent_prefill(q, kv, k_pe, cu_seqlens, cu_seqlens_k, scale, causal, o, lse, workspace, stream)
     Tq, H, N, Tk = q.shape[0], q.shape[1], cu_seqlens.numel() - 1, kv.shape[0]
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens
@@ -692,13 +705,15 @@ def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seq
         o = _empty((Tq, H, DV), _BF16, q, stream)
     if lse is None:
         lse = _empty((Tq, H), _F32, q, stream)
+    ws, nbytes = _workspace(workspace, latent_prefill_workspace_bytes(N, Tq, Tk, H), q, stream)
     rc = lib().kda_latent_prefill(
         _need("q", q, _BF16, (Tq, H, DK + LATENT_PE), dev),
         _need("kv", kv, _BF16, (Tk, H, DK + DV), dev), k_pe.data_ptr(), pe_stride,
         _need("cu_seqlens", cu_seqlens, _I32, (N + 1,), dev),
         _need("cu_seqlens_k", cu_seqlens_k, _I32, (N + 1,), dev), scale, 1 if causal else 0,
         _need("o", o, _BF16, (Tq, H, DV), dev), _need("lse", lse, _F32, (Tq, H), dev),
-        N, Tq, Tk, H, DK, LATENT_PE, DV, _raw_stream(dev, stream))
+        N, Tq, Tk, H, DK, LATENT_PE, DV, None if ws is None else ws.data_ptr(), nbytes,
+        _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_prefill")
     return o, lse

@@ -349,10 +349,17 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
                                                  static_cast<cudaStream_t>(stream)));
 }
 
+size_t kda_latent_prefill_workspace_bytes(int N, int64_t Tq, int64_t Tk, int H, int d_nope, int d_pe, int dv) {
+    if (d_nope != kda::kDK || d_pe != kda::kLatentPeDim || dv != kda::kDV || N < 1 || H < 1 || Tq < 1 || Tk < 0 ||
+        Tq * H >= (int64_t(1) << 31) || Tk * H >= (int64_t(1) << 31))
+        return 0;
+    return kda::latent_prefill_workspace_bytes(N, Tq, Tk, H);
+}
+
 int kda_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t k_pe_stride,
                        const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, float scale,
                        int causal, void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
-                       int d_nope, int d_pe, int dv, void *stream) {
+                       int d_nope, int d_pe, int dv, void *workspace, size_t ws_bytes, void *stream) {
     if (d_nope != kda::kDK || d_pe != kda::kLatentPeDim || dv != kda::kDV) return KDA_ERR_DIM;
     if (N < 1 || H < 1 || Tq < 0 || Tk < 0 || Tq * H >= (int64_t(1) << 31) ||
         Tk * H >= (int64_t(1) << 31))
@@ -365,8 +372,11 @@ int kda_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t 
     const void *ptrs[] = {q, kv, k_pe, cu_seqlens_q, cu_seqlens_k, o, lse};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_ALIGN;
+    const size_t need = kda::latent_prefill_workspace_bytes(N, Tq, Tk, H);
+    if (need > 0 && (!workspace || ws_bytes < need)) return KDA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_ALIGN;
     return cuda_status(kda::launch_latent_prefill(q, kv, k_pe, k_pe_stride, cu_seqlens_q, cu_seqlens_k,
-                                                  scale, causal != 0, o, lse, N, Tq, Tk, H,
+                                                  scale, causal != 0, o, lse, N, Tq, Tk, H, workspace,
                                                   static_cast<cudaStream_t>(stream)));
 }
 

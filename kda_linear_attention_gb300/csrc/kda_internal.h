@@ -164,8 +164,9 @@ cudaError_t read_latent_decode_error(unsigned int *code, bool reset);
 // Attention with expanded keys and values (kda_latent_prefill.cu).
 cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t pe_stride,
                                   const int32_t *cu_q, const int32_t *cu_k, float scale, bool causal,
-                                  void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
+                                  void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H, void *ws,
                                   cudaStream_t stream);
+size_t latent_prefill_workspace_bytes(int N, int64_t Tq, int64_t Tk, int H);
 cudaError_t read_latent_prefill_error(unsigned int *code, bool reset);
 
 // The conv prologue's arithmetic, shared by the prologue kernel and the

@@ -21,6 +21,11 @@
 // probabilities hold without loss) does the row take a new maximum, is O_g
 // rescaled in TMEM and the tile's p computed again.
 //
+// Few work tiles over many keys (a short chunk behind a long context) would
+// leave SMs idle: then the keys of each are cut into pieces, each a work tile
+// of its own that leaves its normalised output in fp32 with its log2-sum-exp
+// in the workspace, and a second kernel joins them.
+//
 // Roles: two groups of four softmax warps, an MMA warp, a copy warp that
 // feeds a ring of eight 16 KB slots (three a key tile, two a value tile: 1.6
 // tiles in flight).  TMEM: S_0, S_1, O_0, O_1, 128 columns each.
@@ -43,6 +48,8 @@ constexpr int kThreads = 320;             // 8 softmax warps, the MMA warp, the 
 constexpr int kHalf = 128;                // queries a half
 constexpr int kTileQ = 2 * kHalf;
 constexpr int kTileK = 128;
+constexpr int kSms = 152;                 // the device's, for the host's choice of pieces
+constexpr int kMaxPieces = 32;            // a lane each in the joining kernel
 constexpr int kSlots = 8;
 constexpr uint32_t kSlot = 16384;
 constexpr uint32_t SM_Q = 0;              // [2 halves][3 blocks of 64 channels][128 rows x 128 B]
@@ -57,7 +64,9 @@ struct Work {
     int h, q0, k0, nk;                    // head; first token of the sequence's queries; of its keys, and keys
     int i0;                               // first query of the tile
     int rows[2];                          // queries of each half
-    int n[2];                             // key tiles each half sees any of
+    int lo;                               // first key tile of this piece
+    int n[2];                             // key tiles of it that each half sees any of
+    int piece;
     int first;                            // keys that the sequence's query 0 sees (may be <= 0)
 };
 
@@ -81,6 +90,8 @@ struct Args {
     int N, Tq, Tk, H;
     bool causal;
     int heads_together;                   // heads whose work tiles are listed together
+    int pieces;                           // of a work tile's keys; 1: not cut
+    float *ws_lse, *ws_o;                 // pieces' log2-sum-exp [pieces][Tq * H], outputs [pieces][Tq * H][128]
     bool o_aligned32;
     float scale_log2;                     // scale * log2 e
     __nv_bfloat16 *o;
@@ -103,8 +114,10 @@ __device__ __forceinline__ int queries_of(const Args &a, int b, bool flag) {
 // last is short.
 __device__ __forceinline__ void get_work(const Args &a, const Misc *M, int id, Work &w) {
     const int tiles = M->tiles;
-    w.valid = id >= 0 && (unsigned)id < (unsigned)tiles * (unsigned)a.H;
+    w.valid = id >= 0 && (unsigned)id / a.pieces < (unsigned)tiles * (unsigned)a.H;
     if (!w.valid) return;
+    w.piece = id % a.pieces;
+    id /= a.pieces;
     const unsigned group = (unsigned)id / ((unsigned)tiles * a.heads_together);
     const int h0 = group * a.heads_together, heads = min(a.heads_together, a.H - h0);
     const int in = (int)((unsigned)id - group * tiles * a.heads_together);
@@ -136,6 +149,12 @@ __device__ __forceinline__ void get_work(const Args &a, const Misc *M, int id, W
         const int sees = a.causal ? max(0, w.first + w.i0 + g * kHalf + w.rows[g] - 1) : w.nk;
         w.n[g] = w.rows[g] > 0 ? (sees + kTileK - 1) / kTileK : 0;
     }
+    // this piece's share of the key tiles
+    const int n = max(w.n[0], w.n[1]);
+    w.lo = (int)((int64_t)n * w.piece / a.pieces);
+    const int end = (int)((int64_t)n * (w.piece + 1) / a.pieces);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) w.n[g] = max(0, min(w.n[g], end) - w.lo);
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -192,7 +211,7 @@ struct Tiles {
     }
 };
 
-__device__ __forceinline__ void st_global32(void *p, const uint32_t (&v)[8]) {
+__device__ __forceinline__ void st_global32(void *p, const uint32_t *v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
@@ -268,6 +287,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         M->ahead[t] = before;
         if (t == 0) M->tiles = total;
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -335,7 +355,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             };
             if (n > 0) queries(0);
             for (int i = 0; ok && i < n; ++i) {
-                const int tok = w.k0 + i * kTileK;
+                const int tok = w.k0 + (w.lo + i) * kTileK;
                 auto slot = [&](int c) { return sm + SM_RING + ((5 * n_v + c) % kSlots) * kSlot; };
                 if (u >= 2) ok = warp_wait(&M->v_empty[u & 1], ((u >> 1) - 1) & 1, fail);
                 if (!ok) break;
@@ -508,8 +528,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             const int n_all = max(w.n[0], w.n[1]);
             if (rows == 0) { u += n_all; continue; }
             const int i_row = w.i0 + g * kHalf + row;     // query of the sequence
-            const int sees = a.causal ? min(w.nk, w.first + i_row) : w.nk;
-            const int all_see = a.causal ? min(w.nk, w.first + w.i0 + g * kHalf + quarter * 32) : w.nk;
+            // keys that the row sees, and those that all rows of the warp see, from the piece's first on
+            const int from_key = w.lo * kTileK;
+            const int sees = (a.causal ? min(w.nk, w.first + i_row) : w.nk) - from_key;
+            const int all_see = (a.causal ? min(w.nk, w.first + w.i0 + g * kHalf + quarter * 32) : w.nk) - from_key;
+            const int nk = w.nk - from_key;
             float neg_m = 0.f, l = 0.f;
             for (int i = 0; i < n; ++i, ++cnt) {
                 const int lim = sees - i * kTileK;        // columns from here on are masked
@@ -606,12 +629,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 l += sum;
 #pragma unroll
                 for (int c = 0; c < 64; c += 16) tmem_st16u(ts + c, p + c);
-                if ((i + 1) * kTileK > w.nk) {
+                if ((i + 1) * kTileK > nk) {
                     // value rows behind the sequence's end are its neighbour's: they must not meet
                     // a zero weight
                     const uint32_t first = 5 * (u + i) + 3;
                     ok = warp_wait(&M->v_full[(u + i) & 1], ((u + i) >> 1) & 1, fail);
-                    const int from = w.nk - i * kTileK;
+                    const int from = nk - i * kTileK;
                     for (int e = row; ok && e < (kTileK - from) * 16; e += kHalf) {
                         const int rr = from + (e >> 4), ch = e & 15;
                         *reinterpret_cast<uint4 *>(sm + SM_RING + ((first + (rr >> 6)) % kSlots) * kSlot +
@@ -635,7 +658,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 tc_fence_after();
             }
             const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float lg = l > 0.f ? log2f(l) - neg_m : -CUDART_INF_F;
             const size_t out = ((size_t)w.q0 + i_row) * a.H + w.h;
+            const size_t at = (size_t)w.piece * a.Tq * a.H + out;   // in the workspace
 #pragma unroll
             for (int c0 = 0; c0 < 128; c0 += 32) {
                 uint32_t ov[32] = {};
@@ -643,28 +668,36 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     tmem_ld32(to + c0, ov);
                     tmem_wait_ld();
                 }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) ov[c] = l > 0.f ? __float_as_uint(__uint_as_float(ov[c]) * inv) : 0u;
                 if (row < rows) {
                     // a lane stores its own row: whole 32-byte sectors halve the store unit's work
-                    __nv_bfloat16 *dst = a.o + out * 128 + c0;
+                    if (a.pieces > 1) {
 #pragma unroll
-                    for (int c = 0; c < 32; c += 16) {
-                        uint32_t x[8];
+                        for (int c = 0; c < 32; c += 8)
+                            st_global32(a.ws_o + at * 128 + c0 + c, ov + c);
+                    } else {
+                        __nv_bfloat16 *dst = a.o + out * 128 + c0;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            x[e] = l > 0.f ? pack_bf2(__uint_as_float(ov[c + 2 * e]) * inv,
-                                                      __uint_as_float(ov[c + 2 * e + 1]) * inv)
-                                           : 0u;
-                        if (a.o_aligned32) {
-                            st_global32(dst + c, x);
-                        } else {
-                            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(x[0], x[1], x[2], x[3]);
-                            *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+                        for (int c = 0; c < 32; c += 16) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                x[e] = pack_bf2(__uint_as_float(ov[c + 2 * e]), __uint_as_float(ov[c + 2 * e + 1]));
+                            if (a.o_aligned32) {
+                                st_global32(dst + c, x);
+                            } else {
+                                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(x[0], x[1], x[2], x[3]);
+                                *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+                            }
                         }
                     }
                 }
             }
-            if (a.lse && row < rows)
-                a.lse[out] = l > 0.f ? (log2f(l) - neg_m) * 0.6931471805599453f : -CUDART_INF_F;
+            if (row < rows) {
+                if (a.pieces > 1) a.ws_lse[at] = lg;
+                else if (a.lse) a.lse[out] = lg * 0.6931471805599453f;
+            }
             tc_fence_before();
         }
         if (!ok && lane == 0) atomicOr(&g_kda_latent_prefill_error, kErrWait);
@@ -676,15 +709,69 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
+// Joins the pieces of every row, o = sum_k 2^(lse_k - lse) o_k in the order of
+// the keys: a warp a row, four channels a lane.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads)
+latent_prefill_join_kernel(const Args a) {
+    const int64_t rows = (int64_t)a.Tq * a.H;
+    const int64_t r = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const bool held = r < rows && seq_of_token(a.cu_q, a.N, (int)(r / a.H)) >= 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces are written
+    if (!held) return;                        // behind the last sequence
+    float v = lane < a.pieces ? a.ws_lse[lane * rows + r] : -CUDART_INF_F, mx = v;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    v = mx == -CUDART_INF_F ? 0.f : ex2_approx(v - mx);
+    float sum = v;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < a.pieces; ++k) {
+        const float f = __shfl_sync(0xffffffffu, v, k) * inv;
+        const float4 x = reinterpret_cast<const float4 *>(a.ws_o + (k * rows + r) * 128)[lane];
+        acc.x = fmaf(f, x.x, acc.x);
+        acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z);
+        acc.w = fmaf(f, x.w, acc.w);
+    }
+    reinterpret_cast<uint2 *>(a.o + r * 128)[lane] = make_uint2(pack_bf2(acc.x, acc.y), pack_bf2(acc.z, acc.w));
+    if (a.lse && lane == 0) a.lse[r] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -CUDART_INF_F;
+}
+
+// Work tiles there can be at most: a sequence's last tile may be part of one.
+int64_t most_tiles(int N, int64_t Tq, int H) { return std::min<int64_t>(Tq, Tq / kTileQ + N) * H; }
+
+// Pieces that a work tile's keys are cut into.  With work tiles for half of
+// the SMs or more, one (a piece's output in fp32 and back costs more than the
+// uneven end).  With fewer, as many as there are SMs for, of two key tiles at
+// least by the average sequence.
+int pieces_of(int N, int64_t Tq, int64_t Tk, int H) {
+    const int64_t tiles = most_tiles(N, Tq, H), keys = (Tk / N + kTileK - 1) / kTileK;
+    if (tiles == 0 || tiles * 2 > kSms) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kSms / tiles, kMaxPieces), keys / 2));
+}
+
 }  // namespace
+
+// Workspace of a call that cuts its keys: the pieces' outputs, then their
+// log2-sum-exp.
+size_t latent_prefill_workspace_bytes(int N, int64_t Tq, int64_t Tk, int H) {
+    const int pieces = pieces_of(N, Tq, Tk, H);
+    return pieces > 1 ? (size_t)pieces * Tq * H * 129 * sizeof(float) : 0;
+}
 
 cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t pe_stride,
                                   const int32_t *cu_q, const int32_t *cu_k, float scale, bool causal,
-                                  void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
+                                  void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H, void *ws,
                                   cudaStream_t stream) {
     static KernelSetup setup;
     int sms = 0;                          // not needed: the grid is the work's
-    const cudaError_t e = setup.get(reinterpret_cast<const void *>(latent_prefill_kernel), SM_BYTES + 1024, &sms);
+    cudaError_t e = setup.get(reinterpret_cast<const void *>(latent_prefill_kernel), SM_BYTES + 1024, &sms);
     if (e != cudaSuccess) return e;
     CUtensorMap mq, mk, mv, mp;
     if (!make_map_heads(&mq, q, 192, H, Tq, kHalf)) return cudaErrorInvalidValue;
@@ -693,13 +780,38 @@ cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_p
                    !make_map_rows(&mp, k_pe, 64, Tk, pe_stride, kTileK)))
         return cudaErrorInvalidValue;
     const int together = (int)std::min<int64_t>(H, std::max<int64_t>(1, kL2Bytes / (std::max<int64_t>(Tk, 1) * 512)));
-    const Args a{cu_q, cu_k, N, (int)Tq, (int)Tk, H, causal, together,
-                 (reinterpret_cast<uintptr_t>(o) & 31u) == 0, scale * 1.4426950408889634f,
-                 static_cast<__nv_bfloat16 *>(o), lse};
-    // a CTA for each work tile there can be: a sequence's last tile may be part of one
-    const int64_t most = std::min<int64_t>(Tq, Tq / kTileQ + N) * H;
-    latent_prefill_kernel<<<(unsigned)most, kThreads, SM_BYTES + 1024, stream>>>(mq, mk, mv, mp, a);
-    return cudaGetLastError();
+    Args a;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.N = N;
+    a.Tq = (int)Tq;
+    a.Tk = (int)Tk;
+    a.H = H;
+    a.causal = causal;
+    a.heads_together = together;
+    a.pieces = pieces_of(N, Tq, Tk, H);
+    a.ws_o = static_cast<float *>(ws);
+    a.ws_lse = a.pieces > 1 ? a.ws_o + (size_t)a.pieces * Tq * H * 128 : nullptr;
+    a.o_aligned32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.o = static_cast<__nv_bfloat16 *>(o);
+    a.lse = lse;
+    // a CTA for each piece of each work tile there can be
+    latent_prefill_kernel<<<(unsigned)(most_tiles(N, Tq, H) * a.pieces), kThreads, SM_BYTES + 1024, stream>>>(
+        mq, mk, mv, mp, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.pieces == 1) return e;
+    // launched while the first kernel runs: its blocks wait for that one's end on the device
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((Tq * H + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_prefill_join_kernel, a);
 }
 
 cudaError_t read_latent_prefill_error(unsigned int *code, bool reset) {

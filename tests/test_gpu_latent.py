@@ -460,21 +460,46 @@ def test_prefill_many_sequences():
 
 
 def test_prefill_more_work_tiles_than_sms():
-    """Work tiles taken over by running blocks: every head of a batch whose
-    tiles are several times the SMs', against the same heads one at a time."""
+    """Work tiles taken over by running blocks: a batch whose tiles are several
+    times the SMs', against the same heads in smaller calls."""
     import torch
     kda = _kda()
     lens, H = [1, 700, 260, 1300], 64
     cu, _, (q, kv, pe), _ = _prefill_inputs(38, lens, lens, H)
     cu = _i32(cu)
     o, lse = kda.latent_prefill(q, kv, pe, cu)
-    for h in (0, 31, 63):
-        oh, lh = kda.latent_prefill(q[:, h:h + 1].contiguous(), kv[:, h:h + 1].contiguous(), pe, cu)
-        assert torch.equal(oh[:, 0], o[:, h]) and torch.equal(lh[:, 0], lse[:, h])
+    for h in (0, 24, 48):
+        oh, lh = kda.latent_prefill(q[:, h:h + 16].contiguous(), kv[:, h:h + 16].contiguous(), pe, cu)
+        assert torch.equal(oh, o[:, h:h + 16]) and torch.equal(lh, lse[:, h:h + 16])
     for _ in range(3):
         o2, lse2 = kda.latent_prefill(q, kv, pe, cu)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
     _clear()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk,H", [([5], [9000], 1), ([1, 40, 0, 300], [700, 2500, 100, 300], 2),
+                                     ([300], [1000], 3), ([128], [128 * 33 + 1], 4)])
+def test_prefill_few_queries_over_many_keys(nq, nk, H, causal):
+    """Keys cut into pieces and joined: rows that see none of a piece, pieces
+    of sequences shorter than the pieces' number, rows behind the last
+    sequence."""
+    import torch
+    kda = _kda()
+    cu, cuk, (q, kv, pe), (qr, kvr, per) = _prefill_inputs(43, nq, nk, H, extra=2)
+    n = int(cu[-1])
+    assert kda.latent_prefill_workspace_bytes(len(nq), n + 2, int(cuk[-1]) + 2, H) > 0
+    o = torch.full((n + 2, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n + 2, H), 7.0, device="cuda")
+    kda.latent_prefill(q, kv, pe, _i32(cu), _i32(cuk), causal=causal, o=o, lse=lse)
+    _clear()
+    assert (o[n:] == 7.0).all() and (lse[n:] == 7.0).all()
+    check(o[:n], lse[:n], ol.prefill(qr[:n], kvr, per, cu, cuk, SCALE, causal), "pieces")
+    need = kda.latent_prefill_workspace_bytes(len(nq), n + 2, int(cuk[-1]) + 2, H)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    o2, lse2 = kda.latent_prefill(q, kv, pe, _i32(cu), _i32(cuk), causal=causal, workspace=ws)
+    _clear()
+    assert torch.equal(o2[:n], o[:n]) and torch.equal(lse2[:n], lse[:n])
 
 
 def test_prefill_output_without_wide_alignment():
@@ -660,7 +685,7 @@ def test_c_entries_take_no_lse():
     pwant, _ = kda.latent_prefill(pq, kv, pe, cu)
     po = torch.empty_like(pwant)
     assert kda.lib().kda_latent_prefill(pq.data_ptr(), kv.data_ptr(), pe.data_ptr(), 64, cu.data_ptr(), cu.data_ptr(),
-                                        SCALE, 1, po.data_ptr(), None, 1, 140, 140, 2, 128, 64, 128, st) == 0
+                                        SCALE, 1, po.data_ptr(), None, 1, 140, 140, 2, 128, 64, 128, None, 0, st) == 0
     _clear()
     assert torch.equal(o, want) and torch.equal(po, pwant)
 

@@ -48,11 +48,11 @@ def _decode(L, **kw):
 
 def _prefill(L, **kw):
     a = dict(q=GOOD, kv=GOOD, pe=GOOD, stride=64, cu=GOOD, cuk=GOOD, scale=0.1, causal=1, o=GOOD, lse=GOOD, N=1,
-             Tq=3, Tk=5, H=2, dn=128, dp=64, dv=128)
+             Tq=3, Tk=5, H=2, dn=128, dp=64, dv=128, ws=GOOD, nbytes=1 << 40)
     a.update(kw)
     return L.kda_latent_prefill(a["q"], a["kv"], a["pe"], a["stride"], a["cu"], a["cuk"], a["scale"],
                                 a["causal"], a["o"], a["lse"], a["N"], a["Tq"], a["Tk"], a["H"], a["dn"],
-                                a["dp"], a["dv"], None)
+                                a["dp"], a["dv"], a["ws"], a["nbytes"], None)
 
 
 @pytest.mark.parametrize("kw,status", BAD_CACHE + [
@@ -92,10 +92,24 @@ def test_decode_workspace(L):
     (dict(dn=64), 2), (dict(dp=32), 2), (dict(dv=64), 2), (dict(N=0), 2), (dict(H=0), 2), (dict(Tq=-1), 2),
     (dict(Tk=-1), 2), (dict(Tq=1 << 30, H=2), 2), (dict(Tk=1 << 30, H=2), 2), (dict(stride=63), 2),
     (dict(stride=68), 2), (dict(stride=0), 2), (dict(scale=0.0), 8), (dict(scale=float("nan")), 8),
-    (dict(causal=2), 8), (dict(q=None), 1), (dict(kv=None), 1), (dict(pe=None), 1), (dict(cu=None), 1),
+    (dict(causal=2), 8), (dict(ws=ctypes.c_void_p(0x10010)), 4), (dict(q=None), 1), (dict(kv=None), 1), (dict(pe=None), 1), (dict(cu=None), 1),
     (dict(cuk=None), 1), (dict(o=None), 1), (dict(q=OFF4), 4), (dict(pe=OFF4), 4), (dict(lse=OFF4), 4)])
 def test_prefill_rejects_bad_arguments(L, kw, status):
     assert _prefill(L, **kw) == status
+
+
+def test_prefill_workspace(L):
+    """None with many work tiles (256 queries of a head each) or few keys; one
+    for few queries over many keys."""
+    for none in ((1, 4096, 4096, 96, 128, 64, 128), (1, 16, 16, 1, 128, 64, 128), (0, 16, 9000, 1, 128, 64, 128),
+                 (1, 0, 9000, 1, 128, 64, 128), (1, 16, 9000, 1, 128, 64, 64), (1, 16, 0, 1, 128, 64, 128)):
+        assert L.kda_latent_prefill_workspace_bytes(*none) == 0
+    need = L.kda_latent_prefill_workspace_bytes(1, 16, 9000, 2, 128, 64, 128)
+    pieces = need // (16 * 2 * 129 * 4)
+    assert need == pieces * 16 * 2 * 129 * 4 and 2 <= pieces <= 32
+    big = dict(Tq=16, Tk=9000)
+    assert _prefill(L, ws=None, nbytes=need, **big) == 6
+    assert _prefill(L, nbytes=need - 1, **big) == 6
 
 
 def test_calls_without_tokens_are_noops(L):
