@@ -50,7 +50,7 @@ constexpr int kMaxSide = 8;               // row tiles of a token that CTAs take
 constexpr int kSoftWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + 2);
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr uint32_t kPair = 32768;         // 128 positions x 128 channels
+constexpr uint32_t kPair = 32768;         // 128 positions x 128 channels: [16 groups][2 blocks][8 rows][128 B]
 constexpr uint32_t kRope = 16384;         // 128 positions x 64 channels; later P [128][64]
 constexpr float kMoveAt = 8.f;            // log2 of the factor a score may pass the maximum by
 constexpr uint32_t kTmemCols = 512;
@@ -232,7 +232,7 @@ __device__ __forceinline__ float lanes_reduce(float (&v)[NC], int lane) {
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_c,
-                     const uint8_t *__restrict__ cache, const Args a) {
+                     const __grid_constant__ CUtensorMap map_r, const uint8_t *__restrict__ cache, const Args a) {
     using F = Cfg<NR>;
     constexpr int NC = NR / 2;                // columns of a softmax group
     extern __shared__ uint8_t smem_raw[];
@@ -277,6 +277,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         if (warp == kSoftWarps + 1 && lane == 0) {
             prefetch_tmap(&map_x);
             prefetch_tmap(&map_c);
+            prefetch_tmap(&map_r);
         }
         __syncthreads();
         long long before = incl - mine, total = 0;
@@ -376,10 +377,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                     if (lane == 0) mbar_arrive_expect_tx(&M->full_p[slot], (uint32_t)live * brows * 256u);
                     __syncwarp();
                     uint8_t *dst = sm + F::PAIR + slot * kPair;
-                    if (rows >= 0) {
-                        tma_load_2d(dst + lane * brows * 128u, &map_c, &M->full_p[slot], 128 * j, rows);
-                        tma_load_2d(dst + 16384u + lane * brows * 128u, &map_c, &M->full_p[slot], 128 * j + 64, rows);
-                    }
+                    if (rows >= 0) tma_load_4d(dst + lane * brows * 256u, &map_c, &M->full_p[slot], 0, 0, 2 * j, rows >> 3);
                     __syncwarp();
                 }
                 if (!ok) break;
@@ -390,7 +388,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 if (lane == 0) mbar_arrive_expect_tx(&M->full_r[slot], (uint32_t)live * brows * 128u);
                 __syncwarp();
                 if (rows >= 0)
-                    tma_load_2d(sm + F::ROPE + slot * kRope + lane * brows * 128u, &map_c, &M->full_r[slot], kLatent, rows);
+                    tma_load_4d(sm + F::ROPE + slot * kRope + lane * brows * 128u, &map_r, &M->full_r[slot], 0, 0, kLatent / 64,
+                                rows >> 3);
                 __syncwarp();
                 rows = next_rows;
                 if (n_tile == 0) prefetch(false);          // the first tile itself
@@ -417,8 +416,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         bool ok = true;
         constexpr uint32_t id_s = instr_desc(kFmtBF16, 128, NR, 0, 0);
         constexpr uint32_t id_o = instr_desc(kFmtBF16, 128, NR, 1, 1);
-        const Operand x_op = operand(sm + F::X, 16, 1024), k_op = operand(sm + F::PAIR, 16, 1024);
-        const Operand v_op = operand(sm + F::PAIR, 16384, 1024), r_op = operand(sm + F::ROPE, 16, 1024);
+        const Operand x_op = operand(sm + F::X, 16, 1024), k_op = operand(sm + F::PAIR, 16, 2048);
+        const Operand v_op = operand(sm + F::PAIR, 1024, 2048), r_op = operand(sm + F::ROPE, 16, 1024);
         const uint32_t full_p = smem_u32(M->full_p), empty_p = smem_u32(M->empty_p);
         const uint32_t full_r = smem_u32(M->full_r), empty_r = smem_u32(M->empty_r);
         const uint32_t s_full = smem_u32(&M->s_full), p_full = smem_u32(&M->p_full);
@@ -440,7 +439,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                     if (elect_one()) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const Operand ke = k + ((e >> 2) * 16384u + (e & 3) * 32u);
+                            const Operand ke = k + ((e >> 2) * 1024u + (e & 3) * 32u);
                             const Operand xe = x_op + ((2 * j + (e >> 2)) * NR * 128u + (e & 3) * 32u);
                             if (j == 0 && e == 0) mma_ss<false>(tmem + TM_S, ke, xe, id_s, false);
                             else mma_ss<true>(tmem + TM_S, ke, xe, id_s);
@@ -471,7 +470,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             if (e == 0) mma_ss<false>(tmem + TM_O + 64 * j, v, rope, id_o, i > 0);
-                            else mma_ss<true>(tmem + TM_O + 64 * j, v + e * 2048u, rope + e * 2048u, id_o);
+                            else mma_ss<true>(tmem + TM_O + 64 * j, v + e * 4096u, rope + e * 2048u, id_o);
                         }
                         commit(empty_p + 8 * at[j]);
                     }
@@ -522,8 +521,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                     for (int e = t; e < (kTile - from) * 64; e += kSoftThreads) {
                         const int r = from + (e >> 6), blk = (e >> 3) & 7, ch = e & 7;
                         const uint32_t slot = (4 * n_tile + (blk >> 1)) % F::NP;
-                        *reinterpret_cast<uint4 *>(sm + F::PAIR + slot * kPair + (blk & 1) * 16384u + r * 128u + ch * 16u) =
-                            make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(sm + F::PAIR + slot * kPair + (r >> 3) * 2048u + (blk & 1) * 1024u +
+                                                   (r & 7) * 128u + ch * 16u) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 // s <- s scale log2 e - m
@@ -809,7 +808,7 @@ constexpr size_t kSplitBytes = 4096, kLseBytes = 2 * kMaxCtas * 64 * sizeof(floa
 static_assert(kSplitBytes >= kMaxCtas * sizeof(Split), "records of the split row tiles");
 
 template <int NR>
-cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const void *cache, const Args &a,
+cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const CUtensorMap &mr, const void *cache, const Args &a,
                    cudaStream_t stream) {
     static KernelSetup setup;
     int sms = 0;
@@ -817,7 +816,7 @@ cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const void *cac
     if (e != cudaSuccess) return e;
     const int G = std::min(sms, kMaxCtas);
     latent_decode_kernel<NR><<<G, kThreads, Cfg<NR>::BYTES + 1024, stream>>>(
-        mx, mc, static_cast<const uint8_t *>(cache), a);
+        mx, mc, mr, static_cast<const uint8_t *>(cache), a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     // launched while the first kernel runs: its blocks wait for that one's end on the device
@@ -847,9 +846,11 @@ cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t
                                  float *lse, int N, int64_t T, int H, int64_t P, int page,
                                  int max_pages, void *ws, cudaStream_t stream) {
     const int NR = rows_of_tile(N, T, H, cu != nullptr);
-    CUtensorMap mx, mc;
+    CUtensorMap mx, mc, mr;
+    const uint32_t groups = (uint32_t)std::min(page, kTile) / 8;
     if (!make_map_rows(&mx, q, kLatentRow, T * H, kLatentRow, (uint32_t)NR) ||
-        !make_map_rows(&mc, cache, kLatentRow, P * page, kLatentRow, (uint32_t)std::min(page, kTile)))
+        !make_map_groups(&mc, cache, kLatentRow, P * page, 2, groups) ||
+        !make_map_groups(&mr, cache, kLatentRow, P * page, 1, groups))
         return cudaErrorInvalidValue;
     uint8_t *w = static_cast<uint8_t *>(ws);
     Args a;
@@ -870,10 +871,10 @@ cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t
     a.ws_lse = reinterpret_cast<float *>(w + kSplitBytes);
     a.ws_o = reinterpret_cast<float *>(w + kSplitBytes + kLseBytes);
     switch (NR) {
-        case 16: return launch<16>(mx, mc, cache, a, stream);
-        case 32: return launch<32>(mx, mc, cache, a, stream);
-        case 48: return launch<48>(mx, mc, cache, a, stream);
-        default: return launch<64>(mx, mc, cache, a, stream);
+        case 16: return launch<16>(mx, mc, mr, cache, a, stream);
+        case 32: return launch<32>(mx, mc, mr, cache, a, stream);
+        case 48: return launch<48>(mx, mc, mr, cache, a, stream);
+        default: return launch<64>(mx, mc, mr, cache, a, stream);
     }
 }
 

@@ -156,6 +156,33 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// 128B-swizzled map of dense bf16 rows (their number a multiple of 8) as
+// [8-row group][64-column block][row][column]: boxes of box_blocks column
+// blocks x box_groups groups, which lie in shared memory as [group][block][8
+// rows][128 B].  One copy brings several column blocks of a page; groups are
+// box_blocks KB apart, blocks 1 KB, in both operand readings.
+inline bool make_map_groups(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, uint32_t box_blocks,
+                            uint32_t box_groups) {
+    auto enc = tmap_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {64, 8, (cuuint64_t)(cols / 64), (cuuint64_t)(rows / 8)};
+    cuuint64_t strides[3] = {(cuuint64_t)cols * 2, 128, (cuuint64_t)cols * 16};
+    cuuint32_t box[4] = {64, 8, box_blocks, box_groups};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 128B-swizzled maps of bf16 rows: boxes of 64 columns x box_rows rows.
 inline bool make_map_rows(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t stride,
                           uint32_t box_rows) {
