@@ -1,8 +1,7 @@
 // The paged latent cache: writing new tokens' rows (append) and reading a
 // sequence's rows back in order (gather).  A cached row is [c | r], 512
 // latent and 64 shared key channels in bf16.
-#include "kda_internal.h"
-#include "latent_common.cuh"
+#include "latent_tc.cuh"
 
 namespace kda {
 
@@ -60,6 +59,7 @@ latent_append_kernel(const uint4 *__restrict__ x, uint4 *__restrict__ cache, Pag
                      const float *__restrict__ norm_w, float eps, int N, int T) {
     const int64_t t_of_warp = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
+    tc::let_next_begin();
     check_offsets(cu, N, T);
     if (t_of_warp >= T) return;
     const int t = (int)t_of_warp;

@@ -242,6 +242,27 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
     const int cta = blockIdx.x, side = a.side;
     const int G = gridDim.x / side, group = cta / side;   // groups of CTAs side by side
 
+    // ---- barriers and tensor memory, under the end of the kernel before this one
+    if (t == 0) {
+        M->fail = 0;
+        M->b0 = M->j0 = M->t0 = 0;
+        for (int i = 0; i < F::NP; ++i) { mbar_init(&M->full_p[i], 1); mbar_init(&M->empty_p[i], 1); }
+        for (int i = 0; i < F::NQ; ++i) { mbar_init(&M->full_r[i], 1); mbar_init(&M->empty_r[i], 1); }
+        mbar_init(&M->x_full, 1);
+        mbar_init(&M->x_empty, 1);
+        mbar_init(&M->s_full, 1);
+        mbar_init(&M->p_full, kSoftWarps);
+        mbar_init(&M->o_full, 1);
+        mbar_init(&M->done, 1);
+        fence_mbar_init();
+    }
+    if (warp == kSoftWarps) tmem_alloc(&M->tmem, kTmemCols);
+    if (warp == kSoftWarps + 1 && lane == 0) {
+        prefetch_tmap(&map_x);
+        prefetch_tmap(&map_c);
+        prefetch_tmap(&map_r);
+    }
+    wait_for_previous();
     // ---- this CTA's units: a block-wide scan of the sequences' units
     {
         const int per = (a.N + kThreads - 1) / kThreads;
@@ -259,26 +280,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             if (lane >= off) incl += v;
         }
         if (lane == 31) M->scan[warp] = incl;
-        if (t == 0) {
-            M->fail = 0;
-            M->b0 = M->j0 = M->t0 = 0;
-            a.split[cta] = Split{0, 0, 0, 0};
-            for (int i = 0; i < F::NP; ++i) { mbar_init(&M->full_p[i], 1); mbar_init(&M->empty_p[i], 1); }
-            for (int i = 0; i < F::NQ; ++i) { mbar_init(&M->full_r[i], 1); mbar_init(&M->empty_r[i], 1); }
-            mbar_init(&M->x_full, 1);
-            mbar_init(&M->x_empty, 1);
-            mbar_init(&M->s_full, 1);
-            mbar_init(&M->p_full, kSoftWarps);
-            mbar_init(&M->o_full, 1);
-            mbar_init(&M->done, 1);
-            fence_mbar_init();
-        }
-        if (warp == kSoftWarps) tmem_alloc(&M->tmem, kTmemCols);
-        if (warp == kSoftWarps + 1 && lane == 0) {
-            prefetch_tmap(&map_x);
-            prefetch_tmap(&map_c);
-            prefetch_tmap(&map_r);
-        }
+        if (t == 0) a.split[cta] = Split{0, 0, 0, 0};
         __syncthreads();
         long long before = incl - mine, total = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
@@ -310,7 +312,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             }
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    let_next_begin();                         // the joining kernel
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -694,7 +696,8 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
     __shared__ Split rec[kMaxCtas];
     __shared__ int upto[kJoinThreads];        // units of the records up to and with this one
     __shared__ int warp_sum[kJoinWarps];
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces are written
+    let_next_begin();
+    wait_for_previous();                      // the pieces are written
     {
         Split sp{0, 0, 0, 0};
         if (t < ctas) {
@@ -815,22 +818,12 @@ cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const CUtensorM
     cudaError_t e = setup.get(reinterpret_cast<const void *>(latent_decode_kernel<NR>), Cfg<NR>::BYTES + 1024, &sms);
     if (e != cudaSuccess) return e;
     const int G = std::min(sms, kMaxCtas);
-    latent_decode_kernel<NR><<<G, kThreads, Cfg<NR>::BYTES + 1024, stream>>>(
-        mx, mc, mr, static_cast<const uint8_t *>(cache), a);
-    e = cudaGetLastError();
+    e = launch_early(latent_decode_kernel<NR>, G, kThreads, Cfg<NR>::BYTES + 1024, stream, mx, mc, mr,
+                     static_cast<const uint8_t *>(cache), a);
     if (e != cudaSuccess) return e;
-    // launched while the first kernel runs: its blocks wait for that one's end on the device
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(4 * G);                // all of them fit the SMs at once
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_join_kernel, (const Split *)a.split, (const float *)a.ws_lse,
-                              (const float *)a.ws_o, a.o, a.lse, NR, G, a.side);
+    // 4 G blocks: all of them fit the SMs at once
+    return launch_early(latent_join_kernel, 4 * G, kJoinThreads, 0, stream, a.split, a.ws_lse, a.ws_o, a.o, a.lse, NR, G,
+                        a.side);
 }
 
 }  // namespace

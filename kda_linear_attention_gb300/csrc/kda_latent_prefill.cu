@@ -234,6 +234,38 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     Misc *M = reinterpret_cast<Misc *>(sm + SM_MISC);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
+    // ---- barriers and tensor memory, under the end of the kernel before this one
+    if (t == 0) {
+        M->fail = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&M->k_full[i], 1);
+            mbar_init(&M->v_full[i], 1);
+            mbar_init(&M->k_empty[i], 1);
+            mbar_init(&M->v_empty[i], 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(&M->q_full[g], 1);
+            mbar_init(&M->q_empty[g], 1);
+            mbar_init(&M->s_full[g], 1);
+            mbar_init(&M->p_full[g], 4);      // warps of a group
+            mbar_init(&M->o_full[g], 1);
+        }
+        mbar_init(&M->done, 1);
+        mbar_init(&M->answer_full, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&M->work_full[i], 1);
+            mbar_init(&M->work_empty[i], kThreads / 32 - 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc(&M->tmem, 512);
+    if (warp == 9 && lane == 0) {
+        prefetch_tmap(&map_q);
+        prefetch_tmap(&map_k);
+        prefetch_tmap(&map_v);
+        prefetch_tmap(&map_pe);
+    }
+    wait_for_previous();
     // ---- work tiles ahead of each thread's sequences
     {
         const int per = (a.N + kThreads - 1) / kThreads;
@@ -248,36 +280,6 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             if (lane >= off) incl += v;
         }
         if (lane == 31) M->warp_sum[warp] = incl;
-        if (t == 0) {
-            M->fail = 0;
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&M->k_full[i], 1);
-                mbar_init(&M->v_full[i], 1);
-                mbar_init(&M->k_empty[i], 1);
-                mbar_init(&M->v_empty[i], 1);
-            }
-            for (int g = 0; g < 2; ++g) {
-                mbar_init(&M->q_full[g], 1);
-                mbar_init(&M->q_empty[g], 1);
-                mbar_init(&M->s_full[g], 1);
-                mbar_init(&M->p_full[g], 4);      // warps of a group
-                mbar_init(&M->o_full[g], 1);
-            }
-            mbar_init(&M->done, 1);
-            mbar_init(&M->answer_full, 1);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&M->work_full[i], 1);
-                mbar_init(&M->work_empty[i], kThreads / 32 - 1);
-            }
-            fence_mbar_init();
-        }
-        if (warp == 8) tmem_alloc(&M->tmem, 512);
-        if (warp == 9 && lane == 0) {
-            prefetch_tmap(&map_q);
-            prefetch_tmap(&map_k);
-            prefetch_tmap(&map_v);
-            prefetch_tmap(&map_pe);
-        }
         __syncthreads();
         int before = incl - mine, total = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
@@ -287,7 +289,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         M->ahead[t] = before;
         if (t == 0) M->tiles = total;
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (a.pieces > 1) let_next_begin();   // the joining kernel (another prefill's blocks would take SMs from this one's)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -322,15 +324,16 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
         get_work(a, M, (int)blockIdx.x, w);
         tell(w);
         while (ok && w.valid) {
-            // the next work tile: asked for here, known a few key tiles on
-            if (lane == 0) ask_work(&M->answer, &M->answer_full);
-            ++asked;
-            __syncwarp();
+            // The next work tile is asked for four key tiles before the end and known two before it:
+            // early enough for its first copies, late enough that a block with a long tile does not
+            // hold one back that another could begin.
             Work next;
-            bool known = false;
+            auto ask = [&]() {
+                if (lane == 0) ask_work(&M->answer, &M->answer_full);
+                ++asked;
+                __syncwarp();
+            };
             auto learn = [&]() {
-                if (known) return;
-                known = true;
                 ok = ok && warp_wait(&M->answer_full, (asked - 1) & 1, fail);
                 if (!ok) return;
                 get_work(a, M, taken_work(&M->answer), next);
@@ -339,6 +342,10 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 tell(next);
             };
             const int n = max(w.n[0], w.n[1]);
+            if (n == 0) {
+                ask();
+                learn();
+            }
             // half g's queries, once the tile before is done with theirs
             auto queries = [&](int g) {
                 if (w.n[g] == 0) return;
@@ -383,9 +390,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 }
                 __syncwarp();
                 ++n_v;
-                if (i == 1) learn();
+                if (i == max(0, n - 4)) ask();
+                if (i == max(0, n - 2)) learn();
             }
-            learn();
             w = next;
         }
         if (!__all_sync(0xffffffffu, ok) || *fail) {
@@ -718,9 +725,9 @@ latent_prefill_join_kernel(const Args a) {
     const int64_t rows = (int64_t)a.Tq * a.H;
     const int64_t r = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    const bool held = r < rows && seq_of_token(a.cu_q, a.N, (int)(r / a.H)) >= 0;
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces are written
-    if (!held) return;                        // behind the last sequence
+    let_next_begin();
+    wait_for_previous();                      // the pieces are written
+    if (r >= rows || seq_of_token(a.cu_q, a.N, (int)(r / a.H)) < 0) return;   // behind the last sequence
     float v = lane < a.pieces ? a.ws_lse[lane * rows + r] : -CUDART_INF_F, mx = v;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -797,21 +804,11 @@ cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_p
     a.o = static_cast<__nv_bfloat16 *>(o);
     a.lse = lse;
     // a CTA for each piece of each work tile there can be
-    latent_prefill_kernel<<<(unsigned)(most_tiles(N, Tq, H) * a.pieces), kThreads, SM_BYTES + 1024, stream>>>(
-        mq, mk, mv, mp, a);
-    e = cudaGetLastError();
+    e = launch_early(latent_prefill_kernel, (unsigned)(most_tiles(N, Tq, H) * a.pieces), kThreads, SM_BYTES + 1024,
+                     stream, mq, mk, mv, mp, a);
     if (e != cudaSuccess || a.pieces == 1) return e;
-    // launched while the first kernel runs: its blocks wait for that one's end on the device
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((Tq * H + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_prefill_join_kernel, a);
+    return launch_early(latent_prefill_join_kernel,
+                        (unsigned)((Tq * H + kJoinThreads / 32 - 1) / (kJoinThreads / 32)), kJoinThreads, 0, stream, a);
 }
 
 cudaError_t read_latent_prefill_error(unsigned int *code, bool reset) {

@@ -210,6 +210,31 @@ inline bool make_map_heads(CUtensorMap *m, const void *base, int64_t cols, int64
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// ---- launches that follow one another closely
+// A kernel launched with launch_early may begin once every block of the one
+// before it in the stream has called let_next_begin() or ended; it must call
+// wait_for_previous(), which returns when that one is complete and its writes
+// are visible, before it touches any global memory.  What it does before that
+// (barriers, tensor memory) runs under the other's end.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                         A &&...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ---- host: a kernel's shared-memory limit and the device's SM count
 // Both cost a driver call of a microsecond or so; they hold for a device's
 // context, so they are asked for and set once in each (`id` of cuCtxGetId
