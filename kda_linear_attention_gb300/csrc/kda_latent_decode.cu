@@ -25,10 +25,23 @@
 // order of the positions (no atomics: the same bits every time).
 //
 // Roles: a copy warp (TMA boxes of one page each, and L2 prefetch of the next
-// tile's pages, whose rows are contiguous), an MMA thread, two groups of four
+// tile's pages, whose rows are contiguous), an MMA warp, two groups of four
 // softmax warps that each take half of the rows (columns).  Shared memory: X
 // (NR x 1152 B), a ring of 32 KB slots (128 positions x 128 channels) and the
 // 16 KB slots of the shared key part, which hold P once the scores are done.
+//
+// What bounds it: a tile's 147 KB fill shared memory, so its chain is serial:
+// P's product frees a slot, the next tile's rows arrive in it 1,100 to 2,400
+// cycles later, scores, softmax (700 cycles).  A product step costs about 64
+// cycles for its 128-lane A operand from shared memory and a quarter of the
+// columns more (70 to 80; 68 steps a unit), so a unit takes 5,200 to 5,600
+// cycles.  An SM's share of HBM brings a unit in 6,400: HBM bounds up to 64
+// rows.  Two CTAs side by side share the rows, which then come in 3,200: the
+// chain bounds 65 to 128 rows.  Measured, a call with everything: 128
+// sequences of 8,000-8,192 tokens at 64 heads 209 us (5.8 TB/s, 85 % of the
+// measured copy); tokens 131,072 and 100,001 at 32 heads 62 us (63 %); 64
+// sequences of 2,000-4,096 at 96 heads 74 us (46 %); one of 1,000 at 16 heads
+// 16 us (launches and one unit's chain).
 #include <algorithm>
 
 #include "latent_tc.cuh"
