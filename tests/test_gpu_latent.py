@@ -642,6 +642,64 @@ def test_calls_on_another_stream():
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
+def test_steps_follow_one_another_closely():
+    """Kernels that begin under the end of the one before them see what it
+    wrote: 100 decode steps (new rows and queries copied in, append,
+    attention, expanded attention of the gathered rows) without a wait between
+    them, against the same steps one at a time."""
+    import torch
+    kda = _kda()
+    lens = [200, 64, 1000]
+    c = Paged(49, lens, 64, nan=False)
+    start = c.dev.clone()
+    xs, qs = _bf(c.rng.normal(size=(100, 3, ol.ROW)))[0], _bf(c.rng.normal(size=(100, 3, 16, ol.ROW)))[0]
+    pq = _bf(c.rng.normal(size=(3, 2, 192)))[0]
+    cu, cuk = _i32([0, 1, 2, 3]), _i32(np.cumsum([0] + lens))
+    x, q = torch.empty_like(xs[0]), torch.empty_like(qs[0])
+
+    def steps(wait):
+        c.dev.copy_(start)
+        out = []
+        for i in range(100):
+            x.copy_(xs[i])
+            q.copy_(qs[i])
+            kda.latent_append(x, c.dev, c.table_dev, c.lens_dev)
+            out += kda.latent_decode(q, c.dev, c.table_dev, c.lens_dev)
+            rows = kda.latent_gather(c.dev, c.table_dev, cuk, total=sum(lens))
+            kv = rows[:, :512].reshape(-1, 2, 256).contiguous()
+            out += kda.latent_prefill(pq, kv, rows[:, 512:], cu, cuk)
+            if wait:
+                torch.cuda.synchronize()
+        return out
+
+    want = steps(True)
+    for _ in range(3):
+        for a, b in zip(steps(False), want):
+            assert torch.equal(a, b)
+    _clear()
+
+
+def test_decode_captured_with_memory_of_its_own():
+    """Two graphs that each take their workspace from the capture's memory."""
+    import torch
+    kda = _kda()
+    c = Paged(50, [700, 90], 64)
+    q, _ = c.q(2, 16)
+    want = _decode(c, q, None)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = _decode(c, q, None)
+        graphs.append((g, out))
+    for _ in range(3):
+        for g, _ in graphs:
+            g.replay()
+    _clear()
+    for _, (o, lse) in graphs:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 def test_two_streams_at_once():
     """Decode and prefill calls of two streams in flight together, each with
     its own workspace, give what they give alone."""

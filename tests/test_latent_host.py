@@ -102,7 +102,8 @@ def test_prefill_workspace(L):
     """None with many work tiles (256 queries of a head each) or few keys; one
     for few queries over many keys."""
     for none in ((1, 4096, 4096, 96, 128, 64, 128), (1, 16, 16, 1, 128, 64, 128), (0, 16, 9000, 1, 128, 64, 128),
-                 (1, 0, 9000, 1, 128, 64, 128), (1, 16, 9000, 1, 128, 64, 64), (1, 16, 0, 1, 128, 64, 128)):
+                 (1, 0, 9000, 1, 128, 64, 128), (1, 16, 9000, 1, 128, 64, 64), (1, 16, 0, 1, 128, 64, 128),
+                 (1, 300, 600, 16, 128, 64, 128), (2, 2024, 18408, 32, 128, 64, 128)):
         assert L.kda_latent_prefill_workspace_bytes(*none) == 0
     need = L.kda_latent_prefill_workspace_bytes(1, 16, 9000, 2, 128, 64, 128)
     pieces = need // (16 * 2 * 129 * 4)
