@@ -517,34 +517,34 @@ LATENT_SCALE = (DK + LATENT_PE) ** -0.5   # 1/sqrt(expanded key width)
 
 
 # The calls below run once a layer and step with kernels of a few
-# microseconds, so their own checks cost less than the others': one chain of
-# cheap comparisons a tensor, and _check for the error's words.
+# microseconds, so a call that is right passes one chain of cheap comparisons
+# (a shape is asked for once and compared as numbers); one that is not goes
+# through _check for the error's words.
 _Tensor, _BF16, _F32, _I32, _U8 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.uint8
-
-
-def _need(name, t, dtype, shape, dev):
-    """The address of a tensor that _check accepts (dev: a device index)."""
-    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
-            and t.get_device() == dev and t.is_contiguous()):
-        _check(name, t, dtype, shape, torch.device("cuda", dev))
-    return t.data_ptr()
-
-
-def _need_cache(cache, block_table, N, dev):
-    if not isinstance(cache, _Tensor) or cache.dim() != 3:
-        raise ValueError("cache must be a [P, page, %d] tensor" % LATENT_ROW)
-    if not isinstance(block_table, _Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be a [N, max_pages] tensor")
-    P, page, _ = cache.shape
-    pages = block_table.shape[1]
-    return (_need("cache", cache, _BF16, (P, page, LATENT_ROW), dev),
-            _need("block_table", block_table, _I32, (N, pages), dev), P, page, pages)
 
 
 def _device(t) -> int:
     if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
     return t.get_device()
+
+
+def _plain(t, dtype, dev) -> bool:
+    """Dense, of the type, on the device (an index)."""
+    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+
+
+def _refuse(dev, *tensors):
+    """The first of (name, tensor, dtype, shape) that _check refuses; -1 in a
+    shape stands for any size."""
+    device = torch.device("cuda", dev)
+    for name, t, dtype, shape in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, _Tensor) or t.dim() != len(shape):
+            raise ValueError("%s must be a tensor of %d dimensions" % (name, len(shape)))
+        _check(name, t, dtype, [n if m < 0 else m for n, m in zip(t.shape, shape)], device)
+    raise ValueError("unsupported arguments")
 
 
 def _raw_stream(dev, stream):
@@ -580,17 +580,23 @@ def latent_append(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     the latent part is RMS-normalised.  Returns cache.
     """
     dev = _device(x)
-    if dev != torch.cuda.current_device():      # a launch goes to the current device
+    if dev != torch._C._cuda_getDevice():       # a launch goes to the current device
         with torch.cuda.device(dev):
             return latent_append(x, cache, block_table, seq_lens, cu_seqlens, norm_w, eps, stream)
-    T, N = x.shape[0], seq_lens.numel()
-    c, table, P, page, pages = _need_cache(cache, block_table, N, dev)
+    N, xs, cs, ts = seq_lens.numel(), x.shape, cache.shape, block_table.shape
+    if not (len(xs) == 2 and xs[1] == LATENT_ROW and _plain(x, _BF16, dev)
+            and len(cs) == 3 and cs[2] == LATENT_ROW and _plain(cache, _BF16, dev)
+            and len(ts) == 2 and ts[0] == N and _plain(block_table, _I32, dev)
+            and seq_lens.dim() == 1 and _plain(seq_lens, _I32, dev)
+            and (cu_seqlens is None or cu_seqlens.shape == (N + 1,) and _plain(cu_seqlens, _I32, dev))
+            and (norm_w is None or norm_w.shape == (LATENT,) and _plain(norm_w, _F32, dev))):
+        _refuse(dev, ("x", x, _BF16, (-1, LATENT_ROW)), ("cache", cache, _BF16, (-1, -1, LATENT_ROW)),
+                ("block_table", block_table, _I32, (N, -1)), ("seq_lens", seq_lens, _I32, (N,)),
+                ("cu_seqlens", cu_seqlens, _I32, (N + 1,)), ("norm_w", norm_w, _F32, (LATENT,)))
     rc = lib().kda_latent_append(
-        _need("x", x, _BF16, (T, LATENT_ROW), dev), c, table,
-        _need("seq_lens", seq_lens, _I32, (N,), dev),
-        None if cu_seqlens is None else _need("cu_seqlens", cu_seqlens, _I32, (N + 1,), dev),
-        None if norm_w is None else _need("norm_w", norm_w, _F32, (LATENT,), dev),
-        eps, N, T, P, page, pages, LATENT, LATENT_PE, _raw_stream(dev, stream))
+        x.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), None if norm_w is None else norm_w.data_ptr(),
+        eps, N, xs[0], cs[0], cs[1], ts[1], LATENT, LATENT_PE, _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_append")
     return cache
@@ -603,20 +609,22 @@ def latent_gather(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: to
     (``kda_latent_gather``).  total: the packed length cu_seqlens[N] (where
     ``out`` [total, 576] bf16 is not given).  Returns out."""
     dev = _device(cache)
-    if dev != torch.cuda.current_device():      # a launch goes to the current device
+    if dev != torch._C._cuda_getDevice():       # a launch goes to the current device
         with torch.cuda.device(dev):
             return latent_gather(cache, block_table, cu_seqlens, total, out, stream)
-    N = cu_seqlens.numel() - 1
-    c, table, P, page, pages = _need_cache(cache, block_table, N, dev)
     if out is None:
         if total is None:
             raise ValueError("give the packed length (total) or the output (out)")
         out = _empty((total, LATENT_ROW), _BF16, cache, stream)
-    T = out.shape[0]
-    rc = lib().kda_latent_gather(
-        c, table, _need("cu_seqlens", cu_seqlens, _I32, (N + 1,), dev),
-        _need("out", out, _BF16, (T, LATENT_ROW), dev), N, T, P, page, pages, LATENT, LATENT_PE,
-        _raw_stream(dev, stream))
+    N, os, cs, ts = cu_seqlens.numel() - 1, out.shape, cache.shape, block_table.shape
+    if not (len(os) == 2 and os[1] == LATENT_ROW and _plain(out, _BF16, dev)
+            and len(cs) == 3 and cs[2] == LATENT_ROW and _plain(cache, _BF16, dev)
+            and len(ts) == 2 and ts[0] == N and _plain(block_table, _I32, dev)
+            and cu_seqlens.dim() == 1 and _plain(cu_seqlens, _I32, dev)):
+        _refuse(dev, ("cache", cache, _BF16, (-1, -1, LATENT_ROW)), ("block_table", block_table, _I32, (N, -1)),
+                ("cu_seqlens", cu_seqlens, _I32, (N + 1,)), ("out", out, _BF16, (-1, LATENT_ROW)))
+    rc = lib().kda_latent_gather(cache.data_ptr(), block_table.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(),
+                                 N, os[0], cs[0], cs[1], ts[1], LATENT, LATENT_PE, _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_gather")
     return out
@@ -644,23 +652,33 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     one is given.
     """
     dev = _device(q)
-    if dev != torch.cuda.current_device():      # a launch goes to the current device
+    if dev != torch._C._cuda_getDevice():       # a launch goes to the current device
         with torch.cuda.device(dev):
             return latent_decode(q, cache, block_table, seq_lens, cu_seqlens, scale, o, lse, workspace, stream)
-    T, H, N = q.shape[0], q.shape[1], seq_lens.numel()
-    c, table, P, page, pages = _need_cache(cache, block_table, N, dev)
+    N, qs, cs, ts = seq_lens.numel(), q.shape, cache.shape, block_table.shape
+    if not (len(qs) == 3 and qs[2] == LATENT_ROW and _plain(q, _BF16, dev)
+            and len(cs) == 3 and cs[2] == LATENT_ROW and _plain(cache, _BF16, dev)
+            and len(ts) == 2 and ts[0] == N and _plain(block_table, _I32, dev)
+            and seq_lens.dim() == 1 and _plain(seq_lens, _I32, dev)
+            and (cu_seqlens is None or cu_seqlens.shape == (N + 1,) and _plain(cu_seqlens, _I32, dev))):
+        _refuse(dev, ("q", q, _BF16, (-1, -1, LATENT_ROW)), ("cache", cache, _BF16, (-1, -1, LATENT_ROW)),
+                ("block_table", block_table, _I32, (N, -1)), ("seq_lens", seq_lens, _I32, (N,)),
+                ("cu_seqlens", cu_seqlens, _I32, (N + 1,)))
+    T, H, _ = qs
     if o is None:
         o = _empty((T, H, LATENT), _BF16, q, stream)
+    elif not (o.shape == (T, H, LATENT) and _plain(o, _BF16, dev)):
+        _refuse(dev, ("o", o, _BF16, (T, H, LATENT)))
     if lse is None:
         lse = _empty((T, H), _F32, q, stream)
+    elif not (lse.shape == (T, H) and _plain(lse, _F32, dev)):
+        _refuse(dev, ("lse", lse, _F32, (T, H)))
     ws, nbytes = _workspace(workspace, latent_decode_workspace_bytes(N, T, H), q, stream)
     rc = lib().kda_latent_decode(
-        _need("q", q, _BF16, (T, H, LATENT_ROW), dev), c, table,
-        _need("seq_lens", seq_lens, _I32, (N,), dev),
-        None if cu_seqlens is None else _need("cu_seqlens", cu_seqlens, _I32, (N + 1,), dev),
-        scale, _need("o", o, _BF16, (T, H, LATENT), dev), _need("lse", lse, _F32, (T, H), dev),
-        N, T, H, P, page, pages, LATENT, LATENT_PE,
-        None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev, stream))
+        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), scale, o.data_ptr(), lse.data_ptr(),
+        N, T, H, cs[0], cs[1], ts[1], LATENT, LATENT_PE, None if ws is None else ws.data_ptr(), nbytes,
+        _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_decode")
     return o, lse
@@ -689,31 +707,40 @@ def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seq
     comes from torch's allocator unless one is given.
     """
     dev = _device(q)
-    if dev != torch.cuda.current_device():      # a launch goes to the current device
+    if dev != torch._C._cuda_getDevice():       # a launch goes to the current device
         with torch.cuda.device(dev):
             return latent_prefill(q, kv, k_pe, cu_seqlens, cu_seqlens_k, scale, causal, o, lse, workspace, stream)
-    Tq, H, N, Tk = q.shape[0], q.shape[1], cu_seqlens.numel() - 1, kv.shape[0]
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens
-    if not (isinstance(k_pe, _Tensor) and k_pe.get_device() == dev and k_pe.dtype is _BF16
-            and k_pe.shape == (Tk, LATENT_PE) and (Tk == 0 or k_pe.stride(1) == 1)):
+    N, qs, ks, ps = cu_seqlens.numel() - 1, q.shape, kv.shape, k_pe.shape
+    if not (len(qs) == 3 and qs[2] == DK + LATENT_PE and _plain(q, _BF16, dev)
+            and len(ks) == 3 and ks[1] == qs[1] and ks[2] == DK + DV and _plain(kv, _BF16, dev)
+            and cu_seqlens.dim() == 1 and _plain(cu_seqlens, _I32, dev)
+            and cu_seqlens_k.shape == (N + 1,) and _plain(cu_seqlens_k, _I32, dev)):
+        H = qs[1] if len(qs) > 1 else -1
+        _refuse(dev, ("q", q, _BF16, (-1, -1, DK + LATENT_PE)), ("kv", kv, _BF16, (-1, H, DK + DV)),
+                ("cu_seqlens", cu_seqlens, _I32, (N + 1,)), ("cu_seqlens_k", cu_seqlens_k, _I32, (N + 1,)))
+    Tq, H, _ = qs
+    Tk = ks[0]
+    if not (k_pe.get_device() == dev and k_pe.dtype is _BF16 and ps == (Tk, LATENT_PE)
+            and (Tk == 0 or k_pe.stride(1) == 1)):
         raise ValueError("k_pe must be [%d, %d] bfloat16 on %s with dense rows"
                          % (Tk, LATENT_PE, q.device))
     # the stride of a dimension of one row means nothing
     pe_stride = k_pe.stride(0) if Tk > 1 else LATENT_PE
     if o is None:
         o = _empty((Tq, H, DV), _BF16, q, stream)
+    elif not (o.shape == (Tq, H, DV) and _plain(o, _BF16, dev)):
+        _refuse(dev, ("o", o, _BF16, (Tq, H, DV)))
     if lse is None:
         lse = _empty((Tq, H), _F32, q, stream)
+    elif not (lse.shape == (Tq, H) and _plain(lse, _F32, dev)):
+        _refuse(dev, ("lse", lse, _F32, (Tq, H)))
     ws, nbytes = _workspace(workspace, latent_prefill_workspace_bytes(N, Tq, Tk, H), q, stream)
     rc = lib().kda_latent_prefill(
-        _need("q", q, _BF16, (Tq, H, DK + LATENT_PE), dev),
-        _need("kv", kv, _BF16, (Tk, H, DK + DV), dev), k_pe.data_ptr(), pe_stride,
-        _need("cu_seqlens", cu_seqlens, _I32, (N + 1,), dev),
-        _need("cu_seqlens_k", cu_seqlens_k, _I32, (N + 1,), dev), scale, 1 if causal else 0,
-        _need("o", o, _BF16, (Tq, H, DV), dev), _need("lse", lse, _F32, (Tq, H), dev),
-        N, Tq, Tk, H, DK, LATENT_PE, DV, None if ws is None else ws.data_ptr(), nbytes,
-        _raw_stream(dev, stream))
+        q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), pe_stride, cu_seqlens.data_ptr(), cu_seqlens_k.data_ptr(),
+        scale, 1 if causal else 0, o.data_ptr(), lse.data_ptr(), N, Tq, Tk, H, DK, LATENT_PE, DV,
+        None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_prefill")
     return o, lse

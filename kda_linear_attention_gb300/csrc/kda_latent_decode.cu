@@ -811,15 +811,15 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
 }
 
 // Rows of a tile, in steps of 16 (the products' column step) up to 64.  One
-// token a sequence: its H rows in as few tiles as hold them.  Ragged new
-// tokens: a third more than the average sequence's rows, because a tile costs
-// little more with more columns (a product step is bound by its 128-lane
-// operand: 72 cycles at 32 columns, 80 at 64) and a second tile for the longer
-// sequences' last rows costs as much as the first.
-int rows_of_tile(int N, int64_t T, int H, bool ragged) {
-    const int64_t rows = ragged ? (T * H + N - 1) / N * 4 / 3 : H;
+// token a sequence: its H rows in as few tiles as hold them.  More tokens, and
+// then ragged ones: a third more than the average sequence's rows, because a
+// tile costs little more with more columns (a product step is bound by its
+// 128-lane operand: 72 cycles at 32 columns, 80 at 64) and a second tile for
+// the longer sequences' last rows costs as much as the first.
+int rows_of_tile(int N, int64_t T, int H) {
+    const int64_t rows = T == N ? H : (T * H + N - 1) / N * 4 / 3;
     const int64_t tiles = (rows + 63) / 64;
-    return (int)std::min<int64_t>(64, ((rows + tiles - 1) / tiles + 15) / 16 * 16);
+    return (int)std::min<int64_t>(64, std::max<int64_t>(1, ((rows + tiles - 1) / tiles + 15) / 16) * 16);
 }
 
 constexpr size_t kSplitBytes = 4096, kLseBytes = 2 * kMaxCtas * 64 * sizeof(float);
@@ -845,15 +845,14 @@ cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const CUtensorM
 
 // Workspace: the split records, the pieces' log2-sum-exp, the pieces.
 size_t latent_decode_workspace_bytes(int N, int64_t T, int H) {
-    const int most = std::max(rows_of_tile(N, T, H, true), T == N ? rows_of_tile(N, T, H, false) : 0);
-    return kSplitBytes + kLseBytes + (size_t)2 * kMaxCtas * most * kLatent * sizeof(float);
+    return kSplitBytes + kLseBytes + (size_t)2 * kMaxCtas * rows_of_tile(N, T, H) * kLatent * sizeof(float);
 }
 
 cudaError_t launch_latent_decode(const void *q, const void *cache, const int32_t *table,
                                  const int32_t *seq_lens, const int32_t *cu, float scale, void *o,
                                  float *lse, int N, int64_t T, int H, int64_t P, int page,
                                  int max_pages, void *ws, cudaStream_t stream) {
-    const int NR = rows_of_tile(N, T, H, cu != nullptr);
+    const int NR = rows_of_tile(N, T, H);
     CUtensorMap mx, mc, mr;
     const uint32_t groups = (uint32_t)std::min(page, kTile) / 8;
     if (!make_map_rows(&mx, q, kLatentRow, T * H, kLatentRow, (uint32_t)NR) ||
