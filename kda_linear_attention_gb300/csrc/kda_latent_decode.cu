@@ -16,9 +16,9 @@
 // sums and bf16 probabilities hold without loss); then O^T and the sums are
 // rescaled in TMEM and registers.
 //
-// Work is cut in units of (sequence, row tile, 128 positions); CTA c of G
-// (one an SM) takes units c W / G .. (c + 1) W / G, so every SM has the same
-// number of units whatever the lengths are.  (The row tiles of one token of
+// Work is cut in units of (sequence, row tile, 128 positions); with W units on
+// G CTAs (one an SM) each takes the next ceil(W / G), whatever the lengths are.
+// (The row tiles of one token of
 // many heads are taken side by side, by groups of CTAs that share the units'
 // numbering.)  A CTA's first and last row tile may be pieces of longer ones: pieces are written normalised in fp32 with
 // their log2-sum-exp into the workspace, and a second kernel joins them in the
@@ -104,9 +104,8 @@ struct Misc {
     int fail;
     int b0, j0, t0;                       // first unit
     Seq seq0;                             // its sequence
-    int used;                             // groups with units
     long long scan[kThreads / 32 + 1];
-    long long start, units, total;        // this CTA's first unit and units; all units
+    long long start, units, each;         // this CTA's first unit and units; a group's units
     // per column (row of the tile), by softmax group
     float red[2][4][32];                  // cross-warp reductions
     alignas(16) float neg_m[2][32];       // minus the running maximum, log2 units
@@ -300,15 +299,14 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             if (w < warp) before += M->scan[w];
             total += M->scan[w];
         }
-        // no group between a row tile's pieces is without one: with fewer units than groups, one each
-        const int used = (int)min((long long)G, total);
-        const long long u0 = group < used ? total * group / used : total;
-        const long long u1 = group < used ? total * (group + 1) / used : total;
+        // as many units for each group as the one with the most must have: fewer groups, and fewer
+        // pieces, where that leaves some without
+        const long long each = max(1LL, (total + G - 1) / G);
+        const long long u0 = min(total, group * each), u1 = group < G ? min(total, u0 + each) : u0;
         if (t == 0) {
-            M->used = used;
             M->units = u1 - u0;
             M->start = u0;
-            M->total = total;
+            M->each = each;
         }
         if (u1 > u0 && u0 >= before && u0 < before + mine) {
             for (int b = b_lo; b < b_hi; ++b) {
@@ -672,10 +670,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             tc_fence_before();
             // the tile that starts here and goes on: who holds its last piece
             if (t == 0 && it.head && !it.tail) {
-                // group c holds unit u when c W / G <= u < (c + 1) W / G (rounded down), so the
-                // last c with c W / G < u + 1
                 const long long last = it.unit + it.tiles - 1;
-                a.split[cta] = Split{it.row, it.rows, (int)(((last + 1) * M->used - 1) / M->total) - group + 1, 0};
+                a.split[cta] = Split{it.row, it.rows, (int)(last / M->each) - group + 1, 0};
             }
         }
         if (!ok && t == 0) atomicOr(&g_kda_latent_decode_error, kErrWait);
