@@ -16,8 +16,8 @@
 // sums and bf16 probabilities hold without loss); then O^T and the sums are
 // rescaled in TMEM and registers.
 //
-// Work is cut in units of (sequence, row tile, 128 positions); with W units on
-// G CTAs (one an SM) each takes the next ceil(W / G), whatever the lengths are.
+// Work is cut in units of (sequence, row tile, 128 positions), and one more a
+// row tile for what it costs beside them; with W units on G CTAs (one an SM) each takes the next ceil(W / G), whatever the lengths are.
 // (The row tiles of one token of
 // many heads are taken side by side, by groups of CTAs that share the units'
 // numbering.)  A CTA's first and last row tile may be pieces of longer ones: pieces are written normalised in fp32 with
@@ -58,6 +58,11 @@ __device__ unsigned int g_kda_latent_decode_error = 0;
 namespace {
 
 constexpr int kTile = 128;                // positions a unit
+// Units that a row tile counts beside its tiles of positions, in front of them
+// (queries, first scores, output).  24 sequences of 100-2,100 tokens with
+// drafts: 26.0 us without, 24.3 with one, 24.5 with two; 64 of 2,000-4,096 at
+// 96 heads: 75, 73, 74; 128 of 8,000-8,192 at 64 heads: 207, 208, 208.
+constexpr int kExtra = 1;
 constexpr int kMaxCtas = 160;             // grid bound (one CTA an SM; 152 SMs)
 constexpr int kMaxSide = 8;               // row tiles of a token that CTAs take side by side
 constexpr int kSoftWarps = 8;
@@ -94,7 +99,7 @@ struct Cfg {
 struct Seq {
     int row0, rows;                       // flat rows over [T * H], of this sequence
     int first;                            // positions its first new token sees (may be <= 0)
-    int len, tiles, row_tiles;
+    int len, units, row_tiles;            // units: of each of its row tiles
 };
 
 struct Misc {
@@ -152,7 +157,7 @@ __device__ __forceinline__ Seq get_seq(const Args &a, int b, bool flag) {
     s.rows = a.side > 1 ? min(NR, a.H - j * NR) : n * a.H;
     s.first = L - n + 1;
     s.len = L;
-    s.tiles = max(1, (L + kTile - 1) / kTile);
+    s.units = max(1, (L + kTile - 1) / kTile) + kExtra;
     s.row_tiles = (s.rows + NR - 1) / NR;
     return s;
 }
@@ -163,9 +168,9 @@ struct Item {
     int tile, n;                          // first tile of positions, tiles with anything to see
     int len;                              // the sequence's length
     int first_tok, row_in_seq;            // positions its first new token sees; row - row0
-    bool head, tail;                      // holds the row tile's first / last unit
-    long long unit;                       // the first unit here
-    int tiles;                            // units of the whole row tile
+    bool head, tail;                      // holds the row tile's first / last tile of positions
+    long long unit;                       // the unit of its first tile
+    int tiles;                            // tiles of the whole row tile
 };
 
 // Walks a CTA's units row tile by row tile; every role takes the same walk.
@@ -179,31 +184,36 @@ struct Walk {
         if (left > 0) s = m->seq0;
     }
     __device__ __forceinline__ bool next(const Args &a, Item &it) {
-        if (left <= 0) return false;
-        while (j >= s.row_tiles) {        // units are left, so a sequence with rows follows
-            if (++b >= a.N) { left = 0; return false; }
-            s = get_seq<NR>(a, b, false);
-            j = t = 0;
-        }
-        const int units = (int)min((long long)(s.tiles - t), left);
+        int from, to;                     // tiles of positions
+        do {
+            if (left <= 0) return false;
+            while (j >= s.row_tiles) {    // units are left, so a sequence with rows follows
+                if (++b >= a.N) { left = 0; return false; }
+                s = get_seq<NR>(a, b, false);
+                j = t = 0;
+            }
+            const int units = (int)min((long long)(s.units - t), left);
+            from = max(0, t - kExtra);
+            to = max(0, t + units - kExtra);
+            it.unit = u - t + kExtra;
+            it.row_in_seq = j * NR;
+            left -= units;
+            u += units;
+            t = 0;
+            ++j;
+        } while (to <= from);             // none of its tiles is here
         it.b = b;
-        it.row_in_seq = j * NR;
-        it.row = s.row0 + j * NR;
-        it.rows = min(NR, s.rows - j * NR);
+        it.row = s.row0 + it.row_in_seq;
+        it.rows = min(NR, s.rows - it.row_in_seq);
         it.len = s.len;
         it.first_tok = s.first;
-        it.head = t == 0;
-        it.tail = t + units == s.tiles;
-        it.tile = t;
-        it.unit = u;
-        it.tiles = s.tiles;
+        it.head = from == 0;
+        it.tail = to == s.units - kExtra;
+        it.tile = from;
+        it.tiles = s.units - kExtra;
         // the last row sees the most positions
         const int most = min(s.len, s.first + (it.row_in_seq + it.rows - 1) / a.H);
-        it.n = max(0, min(t + units, (max(0, most) + kTile - 1) / kTile) - t);
-        left -= units;
-        u += units;
-        t = 0;
-        ++j;
+        it.n = max(0, min(to, (max(0, most) + kTile - 1) / kTile) - from);
         return true;
     }
 };
@@ -283,7 +293,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         Seq s;                                         // the only one where there are few
         for (int b = b_lo; b < b_hi; ++b) {
             s = get_seq<NR>(a, b, cta == 0);           // CTA 0 flags what is wrong with a sequence
-            mine += (long long)s.tiles * s.row_tiles;
+            mine += (long long)s.units * s.row_tiles;
         }
         long long incl = mine;
 #pragma unroll
@@ -311,12 +321,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         if (u1 > u0 && u0 >= before && u0 < before + mine) {
             for (int b = b_lo; b < b_hi; ++b) {
                 if (per > 1) s = get_seq<NR>(a, b, false);
-                const long long n = (long long)s.tiles * s.row_tiles;
+                const long long n = (long long)s.units * s.row_tiles;
                 if (u0 < before + n) {
                     M->b0 = b;
                     M->seq0 = s;
-                    M->j0 = (int)((u0 - before) / s.tiles);
-                    M->t0 = (int)((u0 - before) % s.tiles);
+                    M->j0 = (int)((u0 - before) / s.units);
+                    M->t0 = (int)((u0 - before) % s.units);
                     break;
                 }
                 before += n;
