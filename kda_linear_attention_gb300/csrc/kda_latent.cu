@@ -62,6 +62,7 @@ latent_append_kernel(const uint4 *__restrict__ x, uint4 *__restrict__ cache, Pag
     const int64_t t_of_warp = (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     tc::let_next_begin();
+    tc::wait_for_previous();
     check_offsets(cu, N, T);
     if (t_of_warp >= T) return;
     const int t = (int)t_of_warp;
@@ -105,6 +106,8 @@ latent_gather_kernel(const uint4 *__restrict__ cache, PagedRows pages, const int
                      uint4 *__restrict__ out, int N, int T) {
     const int64_t t0 = 4 * ((int64_t)blockIdx.x * (kGatherThreads / 32) + (threadIdx.x >> 5));
     const int lane = threadIdx.x & 31;
+    tc::let_next_begin();
+    tc::wait_for_previous();
     check_offsets(cu, N, T);
     if (t0 >= T) return;
     // source row of output row t0 + lane; -2: no such row, -1: its page is bad
@@ -141,20 +144,18 @@ cudaError_t launch_latent_append(const void *x, void *cache, const int32_t *tabl
                                  float eps, int N, int64_t T, int64_t P, int page, int max_pages,
                                  cudaStream_t stream) {
     const unsigned blocks = (unsigned)((T * 32 + kAppendThreads - 1) / kAppendThreads);
-    latent_append_kernel<<<blocks, kAppendThreads, 0, stream>>>(
-        static_cast<const uint4 *>(x), static_cast<uint4 *>(cache), paged_rows(table, P, page, max_pages),
-        seq_lens, cu, norm_w, eps, N, (int)T);
-    return cudaGetLastError();
+    return tc::launch_early(latent_append_kernel, blocks, kAppendThreads, 0, stream, static_cast<const uint4 *>(x),
+                            static_cast<uint4 *>(cache), paged_rows(table, P, page, max_pages), seq_lens, cu, norm_w,
+                            eps, N, (int)T);
 }
 
 cudaError_t launch_latent_gather(const void *cache, const int32_t *table, const int32_t *cu, void *out,
                                  int N, int64_t T, int64_t P, int page, int max_pages,
                                  cudaStream_t stream) {
     const unsigned blocks = (unsigned)(((T + 3) / 4 * 32 + kGatherThreads - 1) / kGatherThreads);
-    latent_gather_kernel<<<blocks, kGatherThreads, 0, stream>>>(
-        static_cast<const uint4 *>(cache), paged_rows(table, P, page, max_pages), cu,
-        static_cast<uint4 *>(out), N, (int)T);
-    return cudaGetLastError();
+    return tc::launch_early(latent_gather_kernel, blocks, kGatherThreads, 0, stream,
+                            static_cast<const uint4 *>(cache), paged_rows(table, P, page, max_pages), cu,
+                            static_cast<uint4 *>(out), N, (int)T);
 }
 
 cudaError_t read_latent_error(unsigned int *code, bool reset) {
