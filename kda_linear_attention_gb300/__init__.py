@@ -520,7 +520,7 @@ LATENT_SCALE = (DK + LATENT_PE) ** -0.5   # 1/sqrt(expanded key width)
 # microseconds, so a call that is right passes one chain of cheap comparisons
 # (a shape is asked for once and compared as numbers); one that is not goes
 # through _check for the error's words.
-_Tensor, _BF16, _F32, _I32, _U8 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_Tensor, _BF16, _F32, _I32 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32
 
 
 def _device(t) -> int:
@@ -559,13 +559,20 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _workspace(given, need, like, stream):
-    """(tensor or None, its bytes): the caller's, or one of `need` bytes."""
-    if given is None:
-        return (_empty((need,), _U8, like, stream), need) if need else (None, 0)
-    if given.get_device() != like.get_device() or not given.is_contiguous():
+# A call's own workspace comes from torch's caching allocator without a tensor
+# around it (10 MB as a tensor add 7 us to a call's host time, as plain memory
+# 2 us).  It belongs to the stream (or to the graph being captured on it), so
+# that giving it back right after the launches is safe: what the stream does
+# later may have it next.
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)     # none in a torch without CUDA
+_raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+
+
+def _given_workspace(t, dev):
+    """(address, bytes) of the caller's workspace."""
+    if not isinstance(t, _Tensor) or t.get_device() != dev or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return given, given.numel() * given.element_size()
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def latent_append(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
@@ -673,12 +680,20 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         lse = _empty((T, H), _F32, q, stream)
     elif not (lse.shape == (T, H) and _plain(lse, _F32, dev)):
         _refuse(dev, ("lse", lse, _F32, (T, H)))
-    ws, nbytes = _workspace(workspace, latent_decode_workspace_bytes(N, T, H), q, stream)
-    rc = lib().kda_latent_decode(
-        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-        None if cu_seqlens is None else cu_seqlens.data_ptr(), scale, o.data_ptr(), lse.data_ptr(),
-        N, T, H, cs[0], cs[1], ts[1], LATENT, LATENT_PE, None if ws is None else ws.data_ptr(), nbytes,
-        _raw_stream(dev, stream))
+    s, own = _raw_stream(dev, stream), None
+    if workspace is not None:
+        ws, nbytes = _given_workspace(workspace, dev)
+    else:
+        nbytes = latent_decode_workspace_bytes(N, T, H)
+        ws = own = _raw_alloc(nbytes, s) if nbytes else None
+    try:
+        rc = lib().kda_latent_decode(
+            q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            None if cu_seqlens is None else cu_seqlens.data_ptr(), scale, o.data_ptr(), lse.data_ptr(),
+            N, T, H, cs[0], cs[1], ts[1], LATENT, LATENT_PE, ws, nbytes, s)
+    finally:
+        if own:
+            _raw_free(own)
     if rc != 0:
         raise KDAError(rc, "kda_latent_decode")
     return o, lse
@@ -736,11 +751,20 @@ def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seq
         lse = _empty((Tq, H), _F32, q, stream)
     elif not (lse.shape == (Tq, H) and _plain(lse, _F32, dev)):
         _refuse(dev, ("lse", lse, _F32, (Tq, H)))
-    ws, nbytes = _workspace(workspace, latent_prefill_workspace_bytes(N, Tq, Tk, H), q, stream)
-    rc = lib().kda_latent_prefill(
-        q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), pe_stride, cu_seqlens.data_ptr(), cu_seqlens_k.data_ptr(),
-        scale, 1 if causal else 0, o.data_ptr(), lse.data_ptr(), N, Tq, Tk, H, DK, LATENT_PE, DV,
-        None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dev, stream))
+    s, own = _raw_stream(dev, stream), None
+    if workspace is not None:
+        ws, nbytes = _given_workspace(workspace, dev)
+    else:
+        nbytes = latent_prefill_workspace_bytes(N, Tq, Tk, H)
+        ws = own = _raw_alloc(nbytes, s) if nbytes else None
+    try:
+        rc = lib().kda_latent_prefill(
+            q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), pe_stride, cu_seqlens.data_ptr(),
+            cu_seqlens_k.data_ptr(), scale, 1 if causal else 0, o.data_ptr(), lse.data_ptr(), N, Tq, Tk, H,
+            DK, LATENT_PE, DV, ws, nbytes, s)
+    finally:
+        if own:
+            _raw_free(own)
     if rc != 0:
         raise KDAError(rc, "kda_latent_prefill")
     return o, lse

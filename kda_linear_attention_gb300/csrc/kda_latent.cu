@@ -30,7 +30,7 @@ __device__ __forceinline__ void check_offsets(const int32_t *cu, int N, int T) {
 // A warp a token: the row's 72 16-byte pieces are read once (lane l holds
 // latent pieces l and 32 + l, lanes 0..7 one of the shared part), the sum of
 // squares is a warp reduction in fp32, each value is rounded to bf16 once.
-// Bound by HBM: 1,152 B in and out a token (66,048 tokens: 32 us, 70 % of the
+// Bound by HBM: 1,152 B in and out a token (66,048 tokens: 30 us, 75 % of the
 // measured copy; two or four tokens a warp, and a grid that stays with the
 // weights in registers, measured 31 to 34 us).
 constexpr int kAppendThreads = 256;
@@ -98,7 +98,7 @@ latent_append_kernel(const uint4 *__restrict__ x, uint4 *__restrict__ cache, Pag
 // ---------------------------------------------------------------- gather
 // A warp copies four consecutive rows: 288 16-byte pieces, nine a lane, all
 // in flight at once; lanes 0..3 walk to the four source rows.  Bound by HBM:
-// 1,152 B in and out a row (66,048 rows: 28 us, 79 % of the measured copy).
+// 1,152 B in and out a row (66,048 rows: 26 us, 87 % of the measured copy).
 constexpr int kGatherThreads = 256;
 
 __global__ void __launch_bounds__(kGatherThreads)

@@ -39,9 +39,9 @@
 // rows.  Two CTAs side by side share the rows, which then come in 3,200: the
 // chain bounds 65 to 128 rows.  Measured, a call with everything: 128
 // sequences of 8,000-8,192 tokens at 64 heads 209 us (5.8 TB/s, 85 % of the
-// measured copy); tokens 131,072 and 100,001 at 32 heads 62 us (63 %); 64
+// measured copy); 131,072 and 100,001 tokens at 32 heads 62 us (63 %); 64
 // sequences of 2,000-4,096 at 96 heads 74 us (46 %); one of 1,000 at 16 heads
-// 16 us (launches and one unit's chain).
+// 15 us (launches and one unit's chain).
 #include <algorithm>
 
 #include "latent_tc.cuh"

@@ -34,9 +34,9 @@
 // halves 3,600 cycles against 2,560 of multiply-adds: a step of S reads both
 // operands from shared memory (about 96 cycles instead of 64), one of P V a
 // transposed operand (about 80); the softmax (1,200 cycles a half) hides under
-// the other half.  Measured: 4,096 tokens at 96 heads 392 us (1.31 PFLOP/s of
+// the other half.  Measured: 4,096 tokens at 96 heads 390 us (1.32 PFLOP/s of
 // the causal multiply-adds, 70 % of the measured dense rate); 1,024 and 1,000
-// tokens behind 8,192 at 32 heads 286 us (67 %: 256 equal work tiles on 152
+// tokens behind 8,192 at 32 heads 285 us (67 %: 256 equal work tiles on 152
 // SMs, two rounds).
 #include <algorithm>
 #include <type_traits>
