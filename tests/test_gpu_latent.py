@@ -748,6 +748,26 @@ def test_c_entries_take_no_lse():
     assert torch.equal(o, want) and torch.equal(po, pwant)
 
 
+def test_calls_without_tokens_or_keys():
+    import torch
+    kda = _kda()
+    c = Paged(51, [20, 5], 16, nan=False)
+    before = c.dev.clone()
+    none, bf = _i32([0, 0, 0]), torch.bfloat16
+    kda.latent_append(torch.empty((0, ol.ROW), dtype=bf, device="cuda"), c.dev, c.table_dev, c.lens_dev, none)
+    assert kda.latent_gather(c.dev, c.table_dev, none, total=0).shape == (0, ol.ROW)
+    o, lse = kda.latent_decode(torch.empty((0, 4, ol.ROW), dtype=bf, device="cuda"), c.dev, c.table_dev, c.lens_dev, none)
+    assert o.shape == (0, 4, 512) and lse.shape == (0, 4)
+    _clear()
+    assert torch.equal(c.dev, before)
+    q, kv, pe = _prefill_inputs(52, [3, 4], [0, 0], 2)[2]
+    o, lse = kda.latent_prefill(q, kv, pe, _i32([0, 3, 7]), none)       # queries without any key
+    _clear()
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    o, lse = kda.latent_prefill(q[:0], kv, pe, none, none)
+    assert o.shape == (0, 2, 128)
+
+
 def test_binding_refuses_wrong_tensors():
     import torch
     kda = _kda()
