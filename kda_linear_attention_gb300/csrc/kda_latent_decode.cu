@@ -32,12 +32,13 @@
 //
 // What bounds it: a tile's 147 KB fill shared memory, so its chain is serial:
 // P's product frees a slot, the next tile's rows arrive in it 1,100 to 2,400
-// cycles later, scores, softmax (700 cycles).  A product step costs about 64
-// cycles for its 128-lane A operand from shared memory and a quarter of the
-// columns more (70 to 80; 68 steps a unit), so a unit takes 5,200 to 5,600
-// cycles.  An SM's share of HBM brings a unit in 6,400: HBM bounds up to 64
-// rows.  Two CTAs side by side share the rows, which then come in 3,200: the
-// chain bounds 65 to 128 rows.  Measured, a call with everything: 128
+// cycles later, scores, softmax (700 cycles).  A product step reads its
+// 128-lane A operand and the columns' from shared memory (alone 32 cycles and a
+// quarter of the columns, at 128 B a cycle; 68 steps a unit), and the copies
+// write there meanwhile: 530 KB a unit at 48 columns, 4,200 cycles, and with
+// the softmax between the products 5,200 to 5,600.  An SM's share of HBM brings
+// a unit in 6,400: HBM bounds up to 64 rows.  Two CTAs side by side share the
+// rows, which then come in 3,200: shared memory bounds 65 to 128 rows.  Measured, a call with everything: 128
 // sequences of 8,000-8,192 tokens at 64 heads 209 us (5.8 TB/s, 85 % of the
 // measured copy); 131,072 and 100,001 tokens at 32 heads 62 us (63 %); 64
 // sequences of 2,000-4,096 at 96 heads 74 us (46 %); one of 1,000 at 16 heads
@@ -819,9 +820,9 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
 // Rows of a tile, in steps of 16 (the products' column step) up to 64.  One
 // token a sequence: its H rows in as few tiles as hold them.  More tokens, and
 // then ragged ones: a third more than the average sequence's rows, because a
-// tile costs little more with more columns (a product step is bound by its
-// 128-lane operand: 72 cycles at 32 columns, 80 at 64) and a second tile for
-// the longer sequences' last rows costs as much as the first.
+// tile costs little more with more columns (a product step reads a 128-lane
+// operand beside them: alone 40 cycles at 32 columns, 48 at 64) and a second
+// tile for the longer sequences' last rows costs as much as the first.
 int rows_of_tile(int N, int64_t T, int H) {
     const int64_t rows = T == N ? H : (T * H + N - 1) / N * 4 / 3;
     const int64_t tiles = (rows + 63) / 64;

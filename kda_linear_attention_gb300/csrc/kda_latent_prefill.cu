@@ -30,11 +30,12 @@
 // feeds a ring of eight 16 KB slots (three a key tile, two a value tile: 1.6
 // tiles in flight).  TMEM: S_0, S_1, O_0, O_1, 128 columns each.
 //
-// What bounds it: the tensor pipe's operand reads.  A key tile takes both
-// halves 3,600 cycles against 2,560 of multiply-adds: a step of S reads both
-// operands from shared memory (about 96 cycles instead of 64), one of P V a
-// transposed operand (about 80); the softmax (1,200 cycles a half) hides under
-// the other half.  Measured: 4,096 tokens at 96 heads 390 us (1.32 PFLOP/s of
+// What bounds it: the products with what shares their memories.  A key tile
+// takes both halves 3,600 cycles: 2,560 of multiply-adds (a step of S reads both
+// operands from shared memory at its full rate, so the copies' 80 KB delay it:
+// 2,660), the scores' and weights' way out of and into TMEM beside the
+// accumulators, and the waits between a half's product and its next scores; the
+// softmax (1,200 cycles a half) hides under the other half.  Measured: 4,096 tokens at 96 heads 390 us (1.32 PFLOP/s of
 // the causal multiply-adds, 70 % of the measured dense rate); 1,024 and 1,000
 // tokens behind 8,192 at 32 heads 285 us (67 %: 256 equal work tiles on 152
 // SMs, two rounds).
