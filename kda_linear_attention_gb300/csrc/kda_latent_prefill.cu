@@ -35,10 +35,12 @@
 // operands from shared memory at its full rate, so the copies' 80 KB delay it:
 // 2,660), the scores' and weights' way out of and into TMEM beside the
 // accumulators, and the waits between a half's product and its next scores; the
-// softmax (1,200 cycles a half) hides under the other half.  Measured: 4,096 tokens at 96 heads 390 us (1.32 PFLOP/s of
-// the causal multiply-adds, 70 % of the measured dense rate); 1,024 and 1,000
-// tokens behind 8,192 at 32 heads 285 us (67 %: 256 equal work tiles on 152
-// SMs, two rounds).
+// softmax (1,200 cycles a half) hides under the other half.  (Handing P over in
+// two halves of 64 keys, so that P V begins earlier, changed nothing: 394 us.)
+// Measured: 4,096 tokens at 96 heads 390 us (1.32 PFLOP/s of the causal
+// multiply-adds, 70 % of the measured dense rate); 1,024 and 1,000 tokens
+// behind 8,192 at 32 heads 285 us (67 %: 256 equal work tiles on 152 SMs, two
+// rounds).
 #include <algorithm>
 #include <type_traits>
 
@@ -91,7 +93,7 @@ struct Misc {
     uint32_t tmem;
     int fail;
     int tiles;                            // work tiles of all sequences (of one head)
-    int warp_sum[kThreads / 32];
+    long long warp_sum[kThreads / 32];
     int ahead[kThreads];                  // work tiles before thread t's sequences
 };
 constexpr uint32_t SM_BYTES = SM_MISC + sizeof(Misc);
@@ -102,6 +104,7 @@ struct Args {
     int N, Tq, Tk, H;
     bool causal;
     int heads_together;                   // heads whose work tiles are listed together
+    int most;                             // work tiles of one head that valid offsets can give
     int pieces;                           // of a work tile's keys; 1: not cut
     float *ws_lse, *ws_o;                 // pieces' log2-sum-exp [pieces][Tq * H], outputs [pieces][Tq * H][128]
     bool o_aligned32;
@@ -282,24 +285,24 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     {
         const int per = (a.N + kThreads - 1) / kThreads;
         const int b_lo = min(a.N, t * per), b_hi = min(a.N, b_lo + per);
-        int mine = 0;
+        long long mine = 0;               // overlapping offsets can give more than 32 bits hold
         for (int b = b_lo; b < b_hi; ++b)
             mine += (queries_of(a, b, blockIdx.x == 0) + kTileQ - 1) / kTileQ;   // CTA 0 flags broken offsets
-        int incl = mine;
+        long long incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, off);
+            const long long v = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += v;
         }
         if (lane == 31) M->warp_sum[warp] = incl;
         __syncthreads();
-        int before = incl - mine, total = 0;
+        long long before = incl - mine, total = 0;
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) before += M->warp_sum[w];
             total += M->warp_sum[w];
         }
-        M->ahead[t] = before;
-        if (t == 0) M->tiles = total;
+        M->ahead[t] = (int)before;
+        if (t == 0) M->tiles = total > a.most ? 0 : (int)total;   // broken offsets (flagged): no work
     }
     if (a.pieces > 1) let_next_begin();   // the joining kernel (another prefill's blocks would take SMs from this one's)
     tc_fence_before();
@@ -827,6 +830,7 @@ cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_p
     a.H = H;
     a.causal = causal;
     a.heads_together = together;
+    a.most = (int)most_tiles(N, Tq, 1);
     a.pieces = pieces_of(N, Tq, Tk, H);
     a.ws_o = static_cast<float *>(ws);
     a.ws_lse = a.pieces > 1 ? a.ws_o + (size_t)a.pieces * Tq * H * 128 : nullptr;

@@ -543,6 +543,23 @@ def test_prefill_flags_bad_offsets():
         _clear(1)
 
 
+def test_prefill_broken_query_offsets_do_no_work_outside():
+    """Offsets that go back and forth claim more queries than there are: the
+    call is flagged and rows around the output keep their values."""
+    import torch
+    kda = _kda()
+    T, H, N = 600, 2, 200
+    rng = _rng(47)
+    (q, _), (kv, _), (pe, _) = (_bf(rng.normal(size=n)) for n in ((T, H, 192), (T, H, 256), (T, 64)))
+    cu = _i32([0, T] * (N // 2) + [0])
+    o = torch.full((T + 20, H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T + 40, H), 7.0, device="cuda")
+    kda.latent_prefill(q, kv, pe, cu, o=o[10:10 + T], lse=lse[16:16 + T])
+    _clear(1)
+    assert (o[:10] == 7.0).all() and (o[10 + T:] == 7.0).all()
+    assert (lse[:16] == 7.0).all() and (lse[16 + T:] == 7.0).all()
+
+
 # ------------------------------------------------------------------ together
 def _layer(seed, H):
     rng = _rng(seed)
