@@ -17,12 +17,13 @@
 // rescaled in TMEM and registers.
 //
 // Work is cut in units of (sequence, row tile, 128 positions), and one more a
-// row tile for what it costs beside them; with W units on G CTAs (one an SM) each takes the next ceil(W / G), whatever the lengths are.
-// (The row tiles of one token of
-// many heads are taken side by side, by groups of CTAs that share the units'
-// numbering.)  A CTA's first and last row tile may be pieces of longer ones: pieces are written normalised in fp32 with
-// their log2-sum-exp into the workspace, and a second kernel joins them in the
-// order of the positions (no atomics: the same bits every time).
+// row tile for what it costs beside them; with W units on G CTAs (one an SM)
+// each takes the next ceil(W / G), whatever the lengths are.  (The row tiles
+// of one token of many heads are taken side by side, by groups of CTAs that
+// share the units' numbering.)  A CTA's first and last row tile may be pieces
+// of longer ones: pieces are written normalised in fp32 with their
+// log2-sum-exp into the workspace, and a second kernel joins them in the order
+// of the positions (no atomics: the same bits every time).
 //
 // Roles: a copy warp (TMA boxes of one page each, and L2 prefetch of the next
 // tile's pages, whose rows are contiguous), an MMA warp, two groups of four
@@ -38,11 +39,11 @@
 // write there meanwhile: 530 KB a unit at 48 columns, 4,200 cycles, and with
 // the softmax between the products 5,200 to 5,600.  An SM's share of HBM brings
 // a unit in 6,400: HBM bounds up to 64 rows.  Two CTAs side by side share the
-// rows, which then come in 3,200: shared memory bounds 65 to 128 rows.  Measured, a call with everything: 128
-// sequences of 8,000-8,192 tokens at 64 heads 209 us (5.8 TB/s, 85 % of the
-// measured copy); 131,072 and 100,001 tokens at 32 heads 62 us (63 %); 64
-// sequences of 2,000-4,096 at 96 heads 74 us (46 %); one of 1,000 at 16 heads
-// 15 us (launches and one unit's chain).
+// rows, which then come in 3,200: shared memory bounds 65 to 128 rows.
+// Measured, a call with everything: 128 sequences of 8,000-8,192 tokens at 64
+// heads 209 us (5.8 TB/s, 85 % of the measured copy); 131,072 and 100,001
+// tokens at 32 heads 62 us (63 %); 64 sequences of 2,000-4,096 at 96 heads 74
+// us (46 %); one of 1,000 at 16 heads 15 us (launches and one unit's chain).
 #include <algorithm>
 
 #include "latent_tc.cuh"

@@ -1,5 +1,5 @@
 // Tensor-core pieces shared by the latent-attention kernels: TMEM loads and
-// stores of other widths, waits that give up together, 2D and 3D bf16 TMA
+// stores of other widths, waits that give up together, 2D to 4D bf16 TMA
 // maps.
 #pragma once
 
