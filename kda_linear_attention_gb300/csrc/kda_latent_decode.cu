@@ -42,8 +42,8 @@
 // rows, which then come in 3,200: shared memory bounds 65 to 128 rows.
 // Measured, a call with everything: 128 sequences of 8,000-8,192 tokens at 64
 // heads 209 us (5.8 TB/s, 85 % of the measured copy); 131,072 and 100,001
-// tokens at 32 heads 62 us (63 %); 64 sequences of 2,000-4,096 at 96 heads 74
-// us (46 %); one of 1,000 at 16 heads 15 us (launches and one unit's chain).
+// tokens at 32 heads 60 us (65 %); 64 sequences of 2,000-4,096 at 96 heads 74
+// us (46 %); one of 1,000 at 16 heads 12 us (launches and one unit's chain).
 #include <algorithm>
 
 #include "latent_tc.cuh"
@@ -698,24 +698,111 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
 // Joins the pieces of the row tiles that start in one CTA and go on behind
 // it: o = sum_k 2^(lse_k - lse) o_k, in the order of the positions.  Every
 // block lists all such tiles (at most one a CTA) and takes every gridDim-th
-// unit of them: eight rows of a tile with few pieces, a warp a row, or one row
-// of a tile with many (few long sequences, so few such tiles), whose pieces
-// its warps share and whose warps' sums are added in order.  Bound by the
-// latency of its few loads, from L2, where the first kernel has just left the
-// pieces; a grid of a block a (tile, row) costs more in empty blocks.
+// unit of them: eight slices of rows, a warp each, or one row's slice of a
+// tile with many pieces and few rows, which the block's warps share and whose
+// warps' sums are added in order.
+// Bound by latency and by its own instructions (100 to 400 a slice); the
+// pieces come from L2, where the first kernel has just left them.  So a warp
+// asks for its pieces before it has their weights, and few pieces make a wide
+// slice, whose weights cost less, many a narrow one, of which there are more
+// at the same time.  Measured, in a graph, against whole rows, two pieces at a
+// time behind their weights: one sequence of 1,000 tokens at 16 heads 10.7 us
+// a call (12.8), 24 of 100-2,100 with drafts 22.2 (23.8), 16 of 8,192 at 64
+// heads 47.2 (51.5), 131,072 and 100,001 at 32 heads 58.7 (61.7), 64 of
+// 2,000-4,096 at 96 heads 73.9 (74.4); 24 of 3,000 at 128 heads 44.2 (42.5).
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
-// Pieces a warp takes by itself: 100 sequences of 1,024 tokens at 64 heads 49
-// us a call (59 with 2), 8 of 20,000 at 16 heads 45 us (53 with 32).
-constexpr int kJoinAlone = 8;
+// Pieces a warp takes by itself: in slices of 256 channels, in slices of 128,
+// in slices of 128 where the rows are many beside them.  (Wide slices up to 4
+// pieces: 24 of 3,000 at 128 heads 43.6 us, 64 of 2,000-4,096 at 96 74.2; a
+// block a slice from 9 on whatever the rows: 16 of 8,192 at 64 heads 60.)
+constexpr int kJoinWide = 3, kJoinNarrow = 8, kJoinMost = 32;
 static_assert(kJoinThreads >= kMaxCtas, "a thread a record");
 
-__global__ void __launch_bounds__(kJoinThreads)
-latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws_lse,
-                   const float *__restrict__ ws_o, __nv_bfloat16 *__restrict__ o, float *__restrict__ lse,
-                   int NR, int ctas, int side) {
+struct JoinArgs {
+    const Split *split;
+    const float *ws_lse, *ws_o;
+    __nv_bfloat16 *o;
+    float *lse;
+    int NR, ctas, side;
+};
+
+// Weights of a row's pieces, in each group of L lanes a lane's of piece L e +
+// lane, from their log2-sum-exp; returns the row's.
+template <int L, int E>
+__device__ __forceinline__ float join_weights(float (&v)[E]) {
+    float mx = v[0], sum = 0.f;
+#pragma unroll
+    for (int e = 1; e < E; ++e) mx = fmaxf(mx, v[e]);
+#pragma unroll
+    for (int off = L / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        v[e] = mx == -CUDART_INF_F ? 0.f : ex2_approx(v[e] - mx);
+        sum += v[e];
+    }
+#pragma unroll
+    for (int off = L / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= inv;
+    return sum > 0.f ? mx + log2f(sum) : -CUDART_INF_F;
+}
+__device__ __forceinline__ void add_scaled(float4 &acc, float w, const float4 &x) {
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
+}
+
+__device__ __forceinline__ bool join_alone(int n, int NR) { return n <= kJoinNarrow || (n <= kJoinMost && NR > 2 * n); }
+
+// A warp joins slice `sl` (128 W channels) of row r of CTA c's tile of up to N pieces, K of them in
+// flight together.
+template <int N, int K, int W>
+__device__ __forceinline__ void join_row(const JoinArgs &a, int c, const Split &sp, int r, int sl, int lane) {
+    const int n = sp.pieces;
+    // where piece 0 and piece 1 have the row; the further ones lie a stride apart (the workspace has
+    // less than 2^25 numbers)
+    const int stride = 2 * a.side * a.NR, row0 = (2 * c + 1) * a.NR + r, row1 = 2 * c * a.NR + stride + r;
+    constexpr int L = N <= 4 ? 4 : N <= 8 ? 8 : 32;           // lanes that share the weights out
+    const int mine = lane % L;
+    float v[1] = {mine < n ? a.ws_lse[mine == 0 ? row0 : row1 + (mine - 1) * stride] : -CUDART_INF_F}, lg = 0.f;
+    const float4 *const src = reinterpret_cast<const float4 *>(a.ws_o) + 32 * W * sl + lane;
+    float4 acc[W];
+#pragma unroll
+    for (int q = 0; q < W; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < (N > K ? n : 1); k0 += K) {
+        float4 x[K][W];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int row = k0 + k == 0 ? row0 : row1 + (k0 + k - 1) * stride;
+#pragma unroll
+            for (int q = 0; q < W; ++q)
+                x[k][q] = k0 + k < n ? src[row * (kLatent / 4) + 32 * q] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (k0 == 0) lg = join_weights<L>(v);                 // behind the first loads
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float w = __shfl_sync(0xffffffffu, v[0], k0 + k);   // from the n-th on any: x is 0
+#pragma unroll
+            for (int q = 0; q < W; ++q) add_scaled(acc[q], w, x[k][q]);
+        }
+    }
+    const size_t row = (size_t)sp.row + r;
+    uint2 *dst = reinterpret_cast<uint2 *>(a.o + row * kLatent);
+#pragma unroll
+    for (int q = 0; q < W; ++q)
+        dst[32 * (W * sl + q) + lane] = make_uint2(pack_bf2(acc[q].x, acc[q].y), pack_bf2(acc[q].z, acc[q].w));
+    if (a.lse && sl == 0 && lane == 0) a.lse[row] = lg * 0.6931471805599453f;
+}
+
+__global__ void __launch_bounds__(kJoinThreads, 4)
+latent_join_kernel(const JoinArgs a) {
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    __shared__ float4 part[kJoinWarps][kLatent / 4];
+    __shared__ float4 part[kJoinWarps][32];
+    __shared__ float weight[kMaxCtas];
     __shared__ Split rec[kMaxCtas];
     __shared__ int upto[kJoinThreads];        // units of the records up to and with this one
     __shared__ int warp_sum[kJoinWarps];
@@ -723,11 +810,12 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
     wait_for_previous();                      // the pieces are written
     {
         Split sp{0, 0, 0, 0};
-        if (t < ctas) {
-            sp = split[t];
+        if (t < a.ctas) {
+            sp = a.split[t];
             rec[t] = sp;
         }
-        int incl = sp.rows == 0 ? 0 : sp.pieces <= kJoinAlone ? (sp.rows + kJoinWarps - 1) / kJoinWarps : sp.rows;
+        const int slices = sp.rows * (sp.pieces <= kJoinWide ? 2 : 4);
+        int incl = join_alone(sp.pieces, a.NR) ? (slices + kJoinWarps - 1) / kJoinWarps : slices;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, off);
@@ -749,72 +837,62 @@ latent_join_kernel(const Split *__restrict__ split, const float *__restrict__ ws
         }
         const Split sp = rec[c];
         const int n = sp.pieces, in = u - (c > 0 ? upto[c - 1] : 0);
-        const bool alone = n <= kJoinAlone;
-        const int r = alone ? in * kJoinWarps + warp : in;
-        if (alone && r >= sp.rows) continue;
-        auto slot = [&](int k) { return k == 0 ? 2 * c + 1 : 2 * (c + k * side); };
-        // every warp finds the maximum and the sum by itself
-        float v[kMaxCtas / 32], mx = -CUDART_INF_F, sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < kMaxCtas / 32; ++e) {
-            const int k = 32 * e + lane;
-            v[e] = k < n ? ws_lse[slot(k) * NR + r] : -CUDART_INF_F;
-            mx = fmaxf(mx, v[e]);
+        if (join_alone(n, a.NR)) {
+            const int i = in * kJoinWarps + warp, per = n <= kJoinWide ? 2 : 4;
+            if (i >= sp.rows * per) continue;
+            if (n <= kJoinWide) join_row<kJoinWide, kJoinWide, 2>(a, c, sp, i >> 1, i & 1, lane);
+            else join_row<kJoinMost, 4, 1>(a, c, sp, i >> 2, i & 3, lane);
+            continue;
         }
+        // warp w takes the pieces w, w + 8, .. of 128 channels, eight of them at a time
+        const int r = in >> 2, sl = in & 3;
+        const int stride = 2 * a.side * a.NR, row0 = (2 * c + 1) * a.NR + r, row1 = 2 * c * a.NR + stride + r;
+        const float4 *const src = reinterpret_cast<const float4 *>(a.ws_o) + 32 * sl + lane;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lg = 0.f;
+#pragma unroll 1
+        for (int k0 = warp; k0 < n; k0 += 8 * kJoinWarps) {
+            float4 x[8];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            for (int e = 0; e < 8; ++e) {
+                const int k = k0 + e * kJoinWarps;
+                x[e] = k < n ? src[(k == 0 ? row0 : row1 + (k - 1) * stride) * (kLatent / 4)]
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (k0 == warp) {                 // behind the first loads; every warp has some (n > 8)
+                if (warp == 0) {
+                    float v[kMaxCtas / 32];
 #pragma unroll
-        for (int e = 0; e < kMaxCtas / 32; ++e) {
-            v[e] = mx == -CUDART_INF_F ? 0.f : ex2_approx(v[e] - mx);
-            sum += v[e];
-        }
+                    for (int e = 0; e < kMaxCtas / 32; ++e) {
+                        const int k = 32 * e + lane;
+                        v[e] = k < n ? a.ws_lse[k == 0 ? row0 : row1 + (k - 1) * stride] : -CUDART_INF_F;
+                    }
+                    lg = join_weights<32>(v);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        float4 acc[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int e = 0; e < kMaxCtas / 32; ++e) {
-            if (32 * e >= n) break;
-            const int last = min(32, n - 32 * e);
-#pragma unroll 2
-            for (int k = alone ? 0 : warp; k < last; k += alone ? 1 : kJoinWarps) {
-                const float w = __shfl_sync(0xffffffffu, v[e], k) * inv;
-                const float4 *src = reinterpret_cast<const float4 *>(ws_o + ((size_t)slot(32 * e + k) * NR + r) * kLatent);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 x = src[32 * q + lane];
-                    acc[q].x = fmaf(w, x.x, acc[q].x);
-                    acc[q].y = fmaf(w, x.y, acc[q].y);
-                    acc[q].z = fmaf(w, x.z, acc[q].z);
-                    acc[q].w = fmaf(w, x.w, acc[q].w);
+                    for (int e = 0; e < kMaxCtas / 32; ++e) weight[32 * e + lane] = v[e];
                 }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int k = k0 + e * kJoinWarps;
+                if (k < n) add_scaled(acc, weight[k], x[e]);
             }
         }
-        const size_t row = (size_t)sp.row + r;
-        uint2 *dst = reinterpret_cast<uint2 *>(o + row * kLatent);
-        if (alone) {
+        part[warp][lane] = acc;
+        __syncthreads();
+        if (warp == 0) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                dst[32 * q + lane] = make_uint2(pack_bf2(acc[q].x, acc[q].y), pack_bf2(acc[q].z, acc[q].w));
-        } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) part[warp][32 * q + lane] = acc[q];
-            __syncthreads();
-            if (t < kLatent / 4) {
-                float4 x = part[0][t];
-#pragma unroll
-                for (int w = 1; w < kJoinWarps; ++w) {
-                    const float4 y = part[w][t];
-                    x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
-                }
-                dst[t] = make_uint2(pack_bf2(x.x, x.y), pack_bf2(x.z, x.w));
+            for (int w = 1; w < kJoinWarps; ++w) {
+                const float4 y = part[w][lane];
+                acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
             }
-            __syncthreads();
+            const size_t row = (size_t)sp.row + r;
+            reinterpret_cast<uint2 *>(a.o + row * kLatent)[32 * sl + lane] =
+                make_uint2(pack_bf2(acc.x, acc.y), pack_bf2(acc.z, acc.w));
+            if (a.lse && sl == 0 && lane == 0) a.lse[row] = lg * 0.6931471805599453f;
         }
-        if (lse && lane == 0 && (alone || warp == 0))
-            lse[row] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -CUDART_INF_F;
+        __syncthreads();
     }
 }
 
@@ -845,8 +923,8 @@ cudaError_t launch(const CUtensorMap &mx, const CUtensorMap &mc, const CUtensorM
                      static_cast<const uint8_t *>(cache), a);
     if (e != cudaSuccess) return e;
     // 4 G blocks: all of them fit the SMs at once
-    return launch_early(latent_join_kernel, 4 * G, kJoinThreads, 0, stream, a.split, a.ws_lse, a.ws_o, a.o, a.lse, NR, G,
-                        a.side);
+    return launch_early(latent_join_kernel, 4 * G, kJoinThreads, 0, stream,
+                        JoinArgs{a.split, a.ws_lse, a.ws_o, a.o, a.lse, NR, G, a.side});
 }
 
 }  // namespace

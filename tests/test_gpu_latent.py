@@ -285,6 +285,24 @@ def test_decode_split_over_positions(lens, H, page):
     check(o, lse, ol.decode(qr, c.ref, c.table, lens, np.arange(len(lens) + 1), SCALE), "split")
 
 
+@pytest.mark.parametrize("lens,H", [([1300], 16), ([1300], 33), ([700] * 40, 64), ([5000, 4999, 1, 4000], 64),
+                                    ([5000, 4999, 1, 4000], 16), ([10000, 9000], 16), ([20000], 5), ([20000], 70)])
+def test_decode_joins_pieces(lens, H):
+    """Row tiles in 2, 3, 4 to 8, 9 to 32 and more pieces, with few and many
+    rows, into buffers that held other numbers before."""
+    import torch
+    kda = _kda()
+    c = Paged(31, lens, 64)
+    N = len(lens)
+    q, qr = c.q(N, H)
+    o = torch.full((N, H, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((N, H), 7.0, device="cuda")
+    ws = torch.full((kda.latent_decode_workspace_bytes(N, N, H),), 0xFF, dtype=torch.uint8, device="cuda")
+    _decode(c, q, None, o=o, lse=lse, workspace=ws)
+    _clear()
+    check(o, lse, ol.decode(qr, c.ref, c.table, lens, np.arange(N + 1), SCALE), "pieces H=%d" % H)
+
+
 @pytest.mark.parametrize("kind", ["rising", "falling", "spike", "tiny", "flat"])
 def test_decode_score_ranges(kind):
     """Scores that rise or fall by hundreds over the positions, one position
