@@ -398,4 +398,13 @@ int kda_device_error(unsigned int *code, int reset) {
     return KDA_OK;
 }
 
+#ifdef KDA_DEBUG
+// Not part of the ABI: lets a test make a bounded wait of the decode (prefill)
+// kernel's next calls run out; 0xffffffff ends that.
+int kda_debug_latent_leave_out(unsigned int decode_tile, unsigned int prefill_tile) {
+    const cudaError_t e = kda::latent_decode_leave_out(decode_tile);
+    return cuda_status(e == cudaSuccess ? kda::latent_prefill_leave_out(prefill_tile) : e);
+}
+#endif
+
 }  // extern "C"

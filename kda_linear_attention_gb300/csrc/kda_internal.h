@@ -168,6 +168,11 @@ cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_p
                                   cudaStream_t stream);
 size_t latent_prefill_workspace_bytes(int N, int64_t Tq, int64_t Tk, int H);
 cudaError_t read_latent_prefill_error(unsigned int *code, bool reset);
+#ifdef KDA_DEBUG
+// The key tile whose arrival the kernel leaves out (latent_tc.cuh).
+cudaError_t latent_decode_leave_out(unsigned int tile);
+cudaError_t latent_prefill_leave_out(unsigned int tile);
+#endif
 
 // The conv prologue's arithmetic, shared by the prologue kernel and the
 // layer prefill that fuses it: bf16 pairs (low half = even channel) to and

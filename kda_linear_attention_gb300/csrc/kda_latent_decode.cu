@@ -109,6 +109,7 @@ struct Misc {
     uint64_t x_full, x_empty, s_full, p_full, o_full, done;
     uint32_t tmem;
     int fail;
+    uint32_t n_x, n_pair, n_rope;         // copies asked for, by barrier
     int b0, j0, t0;                       // first unit
     Seq seq0;                             // its sequence
     long long scan[kThreads / 32 + 1];
@@ -383,7 +384,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         while (ok && walk.next(a, it)) {
             if (it.n == 0) continue;
             int rows = box_row(it, 0, true);
-            if (n_item > 0) ok = warp_wait(&M->x_empty, (n_item - 1) & 1, fail);
+            if (n_item > 0) ok = warp_wait_free(&M->x_empty, (n_item - 1) & 1, fail);
             if (!ok) break;
             ++n_x;
             if (lane == 0) {
@@ -396,7 +397,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 const int next_rows = i + 1 < it.n ? box_row(it, i + 1, true) : -1;
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t u = 4 * n_tile + j, slot = u % F::NP, use = u / F::NP;
-                    if (use > 0) ok = warp_wait(&M->empty_p[slot], (use - 1) & 1, fail);
+                    if (use > 0) ok = warp_wait_free(&M->empty_p[slot], (use - 1) & 1, fail);
                     if (!ok) break;
                     ++n_pair;
                     if (lane == 0) mbar_arrive_expect_tx(&M->full_p[slot], (uint32_t)live * brows * 256u);
@@ -407,7 +408,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 }
                 if (!ok) break;
                 const uint32_t slot = n_tile % F::NQ, use = n_tile / F::NQ;
-                if (use > 0) ok = warp_wait(&M->empty_r[slot], (use - 1) & 1, fail);
+                if (use > 0) ok = warp_wait_free(&M->empty_r[slot], (use - 1) & 1, fail);
                 if (!ok) break;
                 ++n_rope;
                 if (lane == 0) mbar_arrive_expect_tx(&M->full_r[slot], (uint32_t)live * brows * 128u);
@@ -422,15 +423,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             }
             ++n_item;
         }
-        if (!ok || *fail) {
-            // given up: what was asked for still has to land before the block may end
-            auto land = [&](uint64_t *bar, uint32_t uses, uint32_t bars) {
-                for (uint32_t i = uses > bars ? uses - bars : 0; i < uses; ++i)
-                    mbar_wait(bar + i % bars, (i / bars) & 1, kWaitLimit);
-            };
-            land(&M->x_full, n_x, 1);
-            land(M->full_p, n_pair, F::NP);
-            land(M->full_r, n_rope, F::NQ);
+        if (lane == 0) {
+            M->n_x = n_x;
+            M->n_pair = n_pair;
+            M->n_rope = n_rope;
         }
     } else if (warp == kSoftWarps) {
         // ================================================= matrix products
@@ -504,11 +500,11 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 }
                 __syncwarp();
             }
+            ok = __all_sync(0xffffffffu, ok);         // one verdict, so that the warp stays together
             ++n_item;
         }
         // nothing of this CTA's products is in flight when its TMEM goes
-        if (elect_one()) mma_commit(&M->done);
-        warp_wait(&M->done, 0, fail);
+        end_products(&M->done, fail);
     } else {
         // ================================================= softmax, output
         const int g = warp >> 2, quarter = warp & 3;
@@ -623,7 +619,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                warp_arrive(&M->p_full);
+                if (!left_out(n_tile)) warp_arrive(&M->p_full);
             }
             if (!ok) break;
             // ---- the row tile's (piece's) output
@@ -686,12 +682,19 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 a.split[cta] = Split{it.row, it.rows, (int)(last / M->each) - group + 1, 0};
             }
         }
-        if (!ok && t == 0) atomicOr(&g_kda_latent_decode_error, kErrWait);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (*fail) {                          // a role gave up: nobody may have waited for the last copies
+        if (t == 0) atomicOr(&g_kda_latent_decode_error, kErrWait);
+        if (warp == kSoftWarps + 1) {
+            land(&M->x_full, M->n_x, 1);
+            land(M->full_p, M->n_pair, F::NP);
+            land(M->full_r, M->n_rope, F::NQ);
+        }
+    }
     if (warp == kSoftWarps) tmem_dealloc(tmem, kTmemCols);
 }
 
@@ -977,5 +980,9 @@ cudaError_t read_latent_decode_error(unsigned int *code, bool reset) {
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(g_kda_latent_decode_error, &zero, sizeof(unsigned int));
 }
+
+#ifdef KDA_DEBUG
+cudaError_t latent_decode_leave_out(unsigned int tile) { return set_leave_out(tile); }
+#endif
 
 }  // namespace kda

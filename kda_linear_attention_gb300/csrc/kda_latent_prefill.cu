@@ -92,6 +92,7 @@ struct Misc {
     Work work[2];                         // the copy warp's, for the other roles
     uint32_t tmem;
     int fail;
+    uint32_t n_q[2], n_k, n_v, asked;     // copies and further work tiles asked for, by barrier
     int tiles;                            // work tiles of all sequences (of one head)
     long long warp_sum[kThreads / 32];
     int ahead[kThreads];                  // work tiles before thread t's sequences
@@ -217,7 +218,7 @@ struct Tiles {
     uint32_t r = 0;
     __device__ __forceinline__ bool next(Misc *M, Work &w, bool &ok, volatile int *fail) {
         const uint32_t at = r & 1;
-        ok = ok && warp_wait(&M->work_full[at], (r >> 1) & 1, fail);
+        ok = __all_sync(0xffffffffu, ok) && warp_wait(&M->work_full[at], (r >> 1) & 1, fail);
         if (!ok) return false;
         w = M->work[at];
         warp_arrive(&M->work_empty[at]);
@@ -364,7 +365,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             // half g's queries, once the tile before is done with theirs
             auto queries = [&](int g) {
                 if (w.n[g] == 0) return;
-                if (n_q[g] > 0) ok = ok && warp_wait(&M->q_empty[g], (n_q[g] - 1) & 1, fail);
+                if (n_q[g] > 0) ok = ok && warp_wait_free(&M->q_empty[g], (n_q[g] - 1) & 1, fail);
                 if (!ok) return;
                 ++n_q[g];
                 if (lane == 0) {
@@ -379,7 +380,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             for (int i = 0; ok && i < n; ++i) {
                 const int tok = w.k0 + (w.lo + i) * kTileK;
                 auto slot = [&](int c) { return sm + SM_RING + ((5 * n_v + c) % kSlots) * kSlot; };
-                if (u >= 2) ok = warp_wait(&M->v_empty[u & 1], ((u >> 1) - 1) & 1, fail);
+                if (u >= 2) ok = warp_wait_free(&M->v_empty[u & 1], ((u >> 1) - 1) & 1, fail);
                 if (!ok) break;
                 if (lane == 0) {
                     uint64_t *bar = &M->k_full[u & 1];
@@ -392,7 +393,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 ++u;
                 if (i == 0) queries(1);
                 if (!ok) break;
-                if (n_v >= 1) ok = warp_wait(&M->k_empty[(n_v - 1) & 1], ((n_v - 1) >> 1) & 1, fail);
+                if (n_v >= 1) ok = warp_wait_free(&M->k_empty[(n_v - 1) & 1], ((n_v - 1) >> 1) & 1, fail);
                 if (!ok) break;
                 if (lane == 0) {
                     uint64_t *bar = &M->v_full[n_v & 1];
@@ -410,17 +411,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             }
             w = next;
         }
-        if (!__all_sync(0xffffffffu, ok) || *fail) {
-            // given up: what was asked for still has to land before the block may end
-            auto land = [&](uint64_t *bar, uint32_t uses, uint32_t bars) {
-                for (uint32_t i = uses > bars ? uses - bars : 0; i < uses; ++i)
-                    mbar_wait(bar + i % bars, (i / bars) & 1, kWaitLimit);
-            };
-            land(&M->q_full[0], n_q[0], 1);
-            land(&M->q_full[1], n_q[1], 1);
-            land(M->k_full, u, 2);
-            land(M->v_full, n_v, 2);
-            land(&M->answer_full, asked, 1);
+        if (lane == 0) {
+            M->n_q[0] = n_q[0];
+            M->n_q[1] = n_q[1];
+            M->n_k = u;
+            M->n_v = n_v;
+            M->asked = asked;
         }
     } else if (warp == 8) {
         // ================================================= matrix products
@@ -533,8 +529,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             }
         }
         // nothing of this CTA's products is in flight when its TMEM goes
-        if (elect_one()) mma_commit(&M->done);
-        warp_wait(&M->done, 0, fail);
+        end_products(&M->done, fail);
     } else {
         // ================================================= softmax, output
         const int g = warp >> 2, quarter = warp & 3;
@@ -667,7 +662,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(&M->p_full[g]);
+                if (!left_out(cnt)) warp_arrive(&M->p_full[g]);
                 if (!ok) break;
             }
             u += n_all;
@@ -722,12 +717,21 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             }
             tc_fence_before();
         }
-        if (!ok && lane == 0) atomicOr(&g_kda_latent_prefill_error, kErrWait);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (*fail) {                          // a role gave up: nobody may have waited for the last copies
+        if (t == 0) atomicOr(&g_kda_latent_prefill_error, kErrWait);
+        if (warp == 9) {
+            land(&M->q_full[0], M->n_q[0], 1);
+            land(&M->q_full[1], M->n_q[1], 1);
+            land(M->k_full, M->n_k, 2);
+            land(M->v_full, M->n_v, 2);
+            land(&M->answer_full, M->asked, 1);
+        }
+    }
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
@@ -852,5 +856,9 @@ cudaError_t read_latent_prefill_error(unsigned int *code, bool reset) {
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(g_kda_latent_prefill_error, &zero, sizeof(unsigned int));
 }
+
+#ifdef KDA_DEBUG
+cudaError_t latent_prefill_leave_out(unsigned int tile) { return set_leave_out(tile); }
+#endif
 
 }  // namespace kda

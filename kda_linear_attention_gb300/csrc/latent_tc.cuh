@@ -122,10 +122,46 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, vol
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *fail) {
     return __all_sync(0xffffffffu, wait_or_fail(bar, parity, fail));
 }
+// The same for the copy warp, before it arms a copy's barrier again: a role
+// that has given up goes on to the end of its tile, and may release what a copy
+// it did not wait for is still on its way to.
+__device__ __forceinline__ bool warp_wait_free(uint64_t *bar, uint32_t parity, volatile int *fail) {
+    return __all_sync(0xffffffffu, wait_or_fail(bar, parity, fail) && !*fail);
+}
+// Ends a block's products before its tensor memory goes (one warp, the one
+// that issued them): they need nothing from the other roles, so this waits for
+// them whether a role has given up or not.
+__device__ __forceinline__ void end_products(uint64_t *done, volatile int *fail) {
+    if (elect_one()) mma_commit(done);
+    if (!mbar_wait(done, 0, kWaitLimit)) *fail = 1;
+    __syncwarp();
+}
+// Waits for the last copies to each of `bars` barriers that were armed `uses`
+// times in turn: a block ends only when nothing is written to its shared
+// memory any more.
+__device__ __forceinline__ void land(uint64_t *bar, uint32_t uses, uint32_t bars) {
+    for (uint32_t i = uses > bars ? uses - bars : 0; i < uses; ++i)
+        mbar_wait(bar + i % bars, (i / bars) & 1, kWaitLimit);
+}
 // A warp's arrival: one for its 32 lanes, after what each of them did.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// Debug builds can leave out one arrival, so that a test sees a wait of the
+// other roles run out: that of the first block's first softmax warp on the key
+// tile (of those it takes) that the host has set; none unless it has.
+#ifdef KDA_DEBUG
+static __device__ unsigned int g_leave_out = 0xffffffffu;
+inline cudaError_t set_leave_out(unsigned int tile) { return cudaMemcpyToSymbol(g_leave_out, &tile, sizeof(tile)); }
+#endif
+__device__ __forceinline__ bool left_out(uint32_t tile) {
+#ifdef KDA_DEBUG
+    return blockIdx.x == 0 && threadIdx.x < 32 && tile == g_leave_out;
+#else
+    return false;
+#endif
 }
 
 // Named barrier over `threads` threads; true if any of them passed `x`.

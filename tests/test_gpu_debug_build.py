@@ -61,3 +61,71 @@ def test_debug_build_is_clean_on_valid_inputs():
                        timeout=900)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
     assert "debug build clean" in r.stdout
+
+
+WAITS = r'''
+import time
+import numpy as np, torch
+import kda_linear_attention_gb300 as kda
+assert kda.library_path().endswith("libkda_gb300_debug.so"), kda.library_path()
+NONE = 0xffffffff
+torch.manual_seed(1)
+
+
+def normal(*shape):
+    return torch.randn(shape, device="cuda").to(torch.bfloat16)
+
+
+def run(name, call, drop):
+    kda.device_error(reset=True)
+    want = call()
+    torch.cuda.synchronize()
+    assert kda.device_error(reset=True) == 0
+    for tile in (0, 1, 3, 4, 5, 7):
+        assert drop(tile) == 0
+        start = time.time()
+        call()
+        torch.cuda.synchronize()
+        took = time.time() - start
+        assert drop(NONE) == 0
+        assert kda.device_error(reset=True) == 1, (name, tile)
+        assert took < 20, (name, tile, took)
+        for _ in range(2):
+            got = call()
+            torch.cuda.synchronize()
+            assert kda.device_error(reset=True) == 0
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (name, tile)
+        print(name, tile, "%.2f s" % took)
+
+
+# the first block has eight tiles of positions, of two sequences, in its units
+N, L, page = 200, 700, 64
+per = -(-L // page)
+cache, q = normal(N * per, page, 576), normal(N, 5, 576)
+table = torch.randperm(N * per, device="cuda").to(torch.int32).view(N, per)
+lens = torch.full((N,), L, dtype=torch.int32, device="cuda")
+drop = kda.lib().kda_debug_latent_leave_out
+drop.argtypes = [__import__("ctypes").c_uint] * 2
+run("decode", lambda: kda.latent_decode(q, cache, table, lens), lambda t: drop(t, NONE))
+# 320 work tiles of one to ten key tiles: the first block takes over further ones
+T, H = 1300, 64
+cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+pq, kv, pe = normal(T, H, 192), normal(T, H, 256), normal(T, 64)
+run("prefill", lambda: kda.latent_prefill(pq, kv, pe, cu), lambda t: drop(NONE, t))
+print("waits ran out in order")
+'''
+
+
+def test_latent_waits_that_run_out_end_in_order():
+    """One softmax warp leaves out its arrival, so the product warp's wait runs
+    out (the debug build's limit is a second): the call ends, the error word
+    says so, and the calls after it are right."""
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from kda_linear_attention_gb300 import build
+    build.build(debug=True)
+    env = dict(os.environ, KDA_GB300_DEBUG="1", PYTHONPATH=os.pathsep.join([ROOT, os.environ.get("PYTHONPATH", "")]))
+    r = subprocess.run([sys.executable, "-c", WAITS], cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
+    assert "waits ran out in order" in r.stdout
