@@ -454,8 +454,10 @@ int kda_latent_gather(const void *cache, const int32_t *block_table, const int32
  *              memory, 256-byte aligned, alive and unshared until the call's
  *              kernels finish; nothing in it has to be initialised
  * The rows of the positions that a token sees are finite (what lies behind a
- * sequence's end in its last page may be anything).  Returns KDA_OK or a
- * kda_status_t; T = 0 is a no-op.
+ * sequence's end in its last page may be anything).  A row of q that is not
+ * (NaN, infinities) has o = NaN where it sees anything, and lse = NaN, or -inf
+ * if each of its scores is; other rows are not touched by it.  Returns KDA_OK
+ * or a kda_status_t; T = 0 is a no-op.
  */
 int kda_latent_decode(const void *q, const void *cache, const int32_t *block_table,
                       const int32_t *seq_lens, const int32_t *cu_seqlens, float scale, void *o,
@@ -486,7 +488,8 @@ size_t kda_latent_decode_workspace_bytes(int N, int64_t T, int H, int d_latent, 
  *              finish; nothing in it has to be initialised.  Few queries over
  *              many keys need some (their keys are cut into pieces that are
  *              joined); NULL is accepted where the size is 0
- * The keys and values of every sequence are finite.  Returns KDA_OK or a
+ * The keys and values of every sequence are finite; a row of q that is not
+ * gives what kda_latent_decode gives for one.  Returns KDA_OK or a
  * kda_status_t; Tq = 0 is a no-op.
  */
 int kda_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t k_pe_stride,

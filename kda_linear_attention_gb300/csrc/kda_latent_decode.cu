@@ -82,7 +82,7 @@ struct Split {
     int32_t row;                          // first row (flat over [T * H])
     int32_t rows;                         // rows of the tile; 0: nothing
     int32_t pieces;                       // of it: here and in the CTAs `side` further on each
-    int32_t pad;
+    int32_t blind;                        // its first rows, which see nothing
 };
 
 template <int NR>
@@ -639,8 +639,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             bar_sync(bar, 128);
             if (quarter == 0 && lane < NC) {
                 const float sum = (M->red[g][0][lane] + M->red[g][1][lane]) + (M->red[g][2][lane] + M->red[g][3][lane]);
-                const float lg = sum > 0.f ? log2f(sum) - M->neg_m[g][lane] : -CUDART_INF_F;
-                M->f[g][lane] = sum > 0.f ? 1.f / sum : 0.f;
+                // A row that sees nothing has o = 0; one that sees positions has 1 / sum, NaN included,
+                // and 0 / 0 where each of its scores is -inf.  A piece may be without weight: the
+                // joining kernel tells
+                const bool none = whole ? M->seen[g][lane] <= 0 : sum == 0.f;
+                const float lg = none ? -CUDART_INF_F : log2f(sum) - M->neg_m[g][lane];
+                M->f[g][lane] = none ? 0.f : 1.f / sum;
                 if (col0 + lane < it.rows) {
                     if (!whole) a.ws_lse[slot * NR + col0 + lane] = lg;
                     else if (a.lse) a.lse[it.row + col0 + lane] = lg * 0.6931471805599453f;
@@ -679,7 +683,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             // the tile that starts here and goes on: who holds its last piece
             if (t == 0 && it.head && !it.tail) {
                 const long long last = it.unit + it.tiles - 1;
-                a.split[cta] = Split{it.row, it.rows, (int)(last / M->each) - group + 1, 0};
+                const int blind = min(it.rows, max(0, (1 - min(1, it.first_tok)) * a.H - it.row_in_seq));
+                a.split[cta] = Split{it.row, it.rows, (int)(last / M->each) - group + 1, blind};
             }
         }
     }
@@ -731,9 +736,11 @@ struct JoinArgs {
 };
 
 // Weights of a row's pieces, in each group of L lanes a lane's of piece L e +
-// lane, from their log2-sum-exp; returns the row's.
+// lane, from their log2-sum-exp; returns the row's.  NaN in a piece makes all of
+// them NaN; where none has any weight they are 0 for a blind row and NaN (0 / 0)
+// for one that sees positions, whose scores are all -inf.
 template <int L, int E>
-__device__ __forceinline__ float join_weights(float (&v)[E]) {
+__device__ __forceinline__ float join_weights(float (&v)[E], bool blind) {
     float mx = v[0], sum = 0.f;
 #pragma unroll
     for (int e = 1; e < E; ++e) mx = fmaxf(mx, v[e]);
@@ -741,15 +748,15 @@ __device__ __forceinline__ float join_weights(float (&v)[E]) {
     for (int off = L / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        v[e] = mx == -CUDART_INF_F ? 0.f : ex2_approx(v[e] - mx);
+        v[e] = ex2_approx(v[e] - (mx == -CUDART_INF_F ? 0.f : mx));
         sum += v[e];
     }
 #pragma unroll
     for (int off = L / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum != 0.f ? 1.f / sum : blind ? 0.f : CUDART_NAN_F;
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] *= inv;
-    return sum > 0.f ? mx + log2f(sum) : -CUDART_INF_F;
+    return sum != 0.f ? mx + log2f(sum) : -CUDART_INF_F;
 }
 __device__ __forceinline__ void add_scaled(float4 &acc, float w, const float4 &x) {
     acc.x = fmaf(w, x.x, acc.x);
@@ -785,7 +792,7 @@ __device__ __forceinline__ void join_row(const JoinArgs &a, int c, const Split &
             for (int q = 0; q < W; ++q)
                 x[k][q] = k0 + k < n ? src[row * (kLatent / 4) + 32 * q] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (k0 == 0) lg = join_weights<L>(v);                 // behind the first loads
+        if (k0 == 0) lg = join_weights<L>(v, r < sp.blind);                 // behind the first loads
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const float w = __shfl_sync(0xffffffffu, v[0], k0 + k);   // from the n-th on any: x is 0
@@ -870,7 +877,7 @@ latent_join_kernel(const JoinArgs a) {
                         const int k = 32 * e + lane;
                         v[e] = k < n ? a.ws_lse[k == 0 ? row0 : row1 + (k - 1) * stride] : -CUDART_INF_F;
                     }
-                    lg = join_weights<32>(v);
+                    lg = join_weights<32>(v, r < sp.blind);
 #pragma unroll
                     for (int e = 0; e < kMaxCtas / 32; ++e) weight[32 * e + lane] = v[e];
                 }

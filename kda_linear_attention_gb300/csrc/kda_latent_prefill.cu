@@ -674,8 +674,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 ++n_out;
                 tc_fence_after();
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            const float lg = l > 0.f ? log2f(l) - neg_m : -CUDART_INF_F;
+            // A row that sees nothing has o = 0; one that sees keys has 1 / l, NaN included, and 0 / 0
+            // where each of its scores is -inf.  A piece may be without weight: the joining kernel tells
+            const bool none = a.pieces > 1 ? l == 0.f : sees <= 0;
+            const float inv = none ? 0.f : 1.f / l;
+            const float lg = none ? -CUDART_INF_F : log2f(l) - neg_m;
             const size_t out = ((size_t)w.q0 + i_row) * a.H + w.h;
             const size_t at = (size_t)w.piece * a.Tq * a.H + out;   // in the workspace
 #pragma unroll
@@ -686,7 +689,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     tmem_wait_ld();
                 }
 #pragma unroll
-                for (int c = 0; c < 32; ++c) ov[c] = l > 0.f ? __float_as_uint(__uint_as_float(ov[c]) * inv) : 0u;
+                for (int c = 0; c < 32; ++c) ov[c] = none ? 0u : __float_as_uint(__uint_as_float(ov[c]) * inv);
                 if (row < rows) {
                     // a lane stores its own row: whole 32-byte sectors halve the store unit's work
                     if (a.pieces > 1) {
@@ -746,15 +749,20 @@ latent_prefill_join_kernel(const Args a) {
     const int lane = threadIdx.x & 31;
     let_next_begin();
     wait_for_previous();                      // the pieces are written
-    if (r >= rows || seq_of_token(a.cu_q, a.N, (int)(r / a.H)) < 0) return;   // behind the last sequence
+    const int tok = (int)min(r / a.H, (int64_t)a.Tq - 1), b = seq_of_token(a.cu_q, a.N, tok);
+    if (r >= rows || b < 0) return;           // behind the last sequence
     float v = lane < a.pieces ? a.ws_lse[lane * rows + r] : -CUDART_INF_F, mx = v;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    v = mx == -CUDART_INF_F ? 0.f : ex2_approx(v - mx);
-    float sum = v;
+    v = ex2_approx(v - (mx == -CUDART_INF_F ? 0.f : mx));
+    float sum = v;                            // NaN where a piece's is
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    float inv = 1.f / sum;
+    if (sum == 0.f) {                         // the row sees nothing, or only scores of -inf (0 / 0)
+        const int nk = a.cu_k[b + 1] - a.cu_k[b];
+        inv = (a.causal ? nk - (a.cu_q[b + 1] - tok) + 1 : nk) > 0 ? CUDART_NAN_F : 0.f;
+    }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = 0; k < a.pieces; ++k) {
@@ -766,7 +774,7 @@ latent_prefill_join_kernel(const Args a) {
         acc.w = fmaf(f, x.w, acc.w);
     }
     reinterpret_cast<uint2 *>(a.o + r * 128)[lane] = make_uint2(pack_bf2(acc.x, acc.y), pack_bf2(acc.z, acc.w));
-    if (a.lse && lane == 0) a.lse[r] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -CUDART_INF_F;
+    if (a.lse && lane == 0) a.lse[r] = sum == 0.f ? -CUDART_INF_F : (mx + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Work tiles there can be at most: n queries of a sequence are at most

@@ -825,3 +825,116 @@ def test_binding_refuses_wrong_tensors():
         kda.latent_decode(q, c.dev.view(-1, 8, 576), c.table_dev, c.lens_dev)
     with pytest.raises(kda.KDAError):
         kda.latent_decode(q, c.dev, c.table_dev, c.lens_dev, scale=-1.0)
+
+
+# ------------------------------------------------------------------ queries that are not finite
+KINDS = ["nan", "inf", "-inf", "both", "low", "high"]
+
+
+def _poison(qr, rows, channel):
+    """Copy of queries [T, H, d] whose rows (token, head) hold NaN or
+    infinities.  Keys are negative in `channel`, so +inf there makes every
+    score -inf ("low") and -inf every one +inf ("high")."""
+    qr = qr.copy()
+    for k, (t, h) in enumerate(rows):
+        kind = KINDS[k % len(KINDS)]
+        if kind == "nan":
+            qr[t, h, 3] = np.nan
+        elif kind == "both":
+            qr[t, h, 3], qr[t, h, 100] = np.inf, -np.inf
+        elif kind in ("inf", "-inf"):
+            qr[t, h, 60] = float(kind)
+        else:
+            qr[t, h, channel] = np.inf if kind == "low" else -np.inf
+    return qr
+
+
+def _check_poisoned(o, lse, r, rows, low, sees, what):
+    """Rows of finite queries as ever; the poisoned ones, where they see
+    anything, NaN in every channel, with a NaN log-sum-exp unless all of their
+    scores are -inf (ln 0); o = 0 and lse = -inf where they see nothing."""
+    bad = np.zeros(r.lse.shape, dtype=bool)
+    for t, h in rows:
+        bad[t, h] = True
+    part = ol.Result((1, 1), 1)
+    part.o, part.lse, part.absum, part.sqsum, part.mag = (getattr(r, n)[~bad] for n in
+                                                          ("o", "lse", "absum", "sqsum", "mag"))
+    clean = (~bad).tolist()
+    import torch
+    clean = torch.tensor(clean, device=o.device)
+    check(o[clean], lse[clean], part, what)
+    o, lse = _np(o), _np(lse)
+    for t, h in rows:
+        at = "%s: row (%d, %d)" % (what, t, h)
+        if sees[t] <= 0:
+            assert (o[t, h] == 0).all() and np.isneginf(lse[t, h]), at + " sees nothing"
+        else:
+            assert np.isnan(o[t, h]).all(), at + ": o"
+            assert np.isneginf(lse[t, h]) if (t, h) in low else np.isnan(lse[t, h]), at + ": lse"
+
+
+def _spread_rows(rng, T, H, n):
+    """n rows (token, head) in no order, the first and last token's among them."""
+    n = min(n, T * H)
+    flat = [0, T * H - 1] + [int(x) for x in rng.permutation(np.arange(1, T * H - 1))]
+    return [(x // H, x % H) for x in flat[:n]]
+
+
+@pytest.mark.parametrize("lens,news,H,page", [
+    ([40, 129, 700, 2, 128, 1], [4, 3, 5, 5, 1, 1], 4, 16),       # tiles in one piece and in several
+    ([300] * 200, [1] * 200, 5, 64), ([9001, 5000], [1, 1], 16, 64), ([20000], [2], 6, 128),
+    ([700, 200, 150], [1, 230, 2], 2, 64)])                       # rows that see nothing, of a tile in pieces
+def test_decode_of_queries_that_are_not_finite(lens, news, H, page):
+    import torch
+    c = Paged(61, lens, page)
+    c.ref[:, :, 7] = -np.abs(c.ref[:, :, 7]) - 0.5
+    c.ref = torch.from_numpy(c.ref).to(torch.bfloat16).double().numpy()
+    c.dev[:, :, 7] = torch.where(torch.isnan(c.dev[:, :, 7]), c.dev[:, :, 7],
+                                 torch.from_numpy(c.ref[:, :, 7]).to(torch.bfloat16).cuda())
+    cu = np.cumsum([0] + news)
+    _, qr = c.q(cu[-1], H)
+    rows = _spread_rows(c.rng, int(cu[-1]), H, 12)
+    rows += [(int(cu[b]), 0) for b in range(len(lens)) if news[b] > lens[b] and (int(cu[b]), 0) not in rows]
+    q, qr = _bf(_poison(qr, rows, 7))
+    o, lse = _decode(c, q, None if set(news) == {1} else cu)
+    _clear()
+    with np.errstate(all="ignore"):
+        r = ol.decode(qr, c.ref, c.table, lens, cu, SCALE)
+    sees = np.concatenate([m - n + 1 + np.arange(n) for m, n in zip(lens, news)])
+    low = {rows[k] for k in range(len(rows)) if KINDS[k % len(KINDS)] == "low"}
+    for t, h in rows:                                              # what a single score's sign leaves
+        if sees[t] > 0 and not np.isnan(qr[t, h]).any():
+            b = int(np.searchsorted(cu, t, side="right")) - 1
+            with np.errstate(all="ignore"):
+                s = ol.sequence_rows(c.ref, c.table[b], 0, int(sees[t])) @ qr[t, h]
+            if np.isneginf(s).all():
+                low.add((t, h))
+    _check_poisoned(o, lse, r, rows, low, sees, "decode")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk,H", [([40, 70, 300, 5, 1], [40, 200, 300, 2, 1], 3), ([5, 3], [9000, 1], 1),
+                                     ([1, 40, 0, 300], [700, 2500, 100, 300], 2), ([600], [500], 2)])
+def test_prefill_of_queries_that_are_not_finite(nq, nk, H, causal):
+    kda = _kda()
+    cu, cuk, _, (qr, kvr, per) = _prefill_inputs(62, nq, nk, H)
+    per = per.copy()
+    per[:, 2] = -np.abs(per[:, 2]) - 0.5
+    rng = _rng(63)
+    rows = _spread_rows(rng, int(cu[-1]), H, 12)
+    (q, qr), (kv, kvr), (pe, per) = _bf(_poison(qr, rows, 130)), _bf(kvr), _bf(per)
+    o, lse = kda.latent_prefill(q, kv, pe, _i32(cu), _i32(cuk), causal=causal)
+    _clear()
+    with np.errstate(all="ignore"):
+        r = ol.prefill(qr, kvr, per, cu, cuk, SCALE, causal)
+    sees = np.concatenate([m - n + 1 + np.arange(n) if causal else np.full(n, m) for m, n in zip(nk, nq)])
+    low = {rows[k] for k in range(len(rows)) if KINDS[k % len(KINDS)] == "low"}
+    for t, h in rows:
+        if sees[t] > 0 and not np.isnan(qr[t, h]).any():
+            b = int(np.searchsorted(cu, t, side="right")) - 1
+            k0 = int(cuk[b])
+            key = np.concatenate([kvr[k0:k0 + int(sees[t]), h, :128], per[k0:k0 + int(sees[t])]], 1)
+            with np.errstate(all="ignore"):
+                if np.isneginf(key @ qr[t, h]).all():
+                    low.add((t, h))
+    _check_poisoned(o, lse, r, rows, low, sees, "prefill")
