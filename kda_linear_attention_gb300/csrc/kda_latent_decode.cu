@@ -524,7 +524,10 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             if (quarter == 0 && lane < NC) {
                 const int r = it.row_in_seq + col0 + lane;   // several new tokens differ in what they see
                 M->seen[g][lane] = min(it.len, it.first_tok + r / a.H);
-                M->neg_m[g][lane] = 0.f;
+                // columns behind the tile's rows hold another sequence's queries, or what no sequence
+                // has: a maximum of infinity (their exponents are -inf or NaN, which fmaxf leaves out)
+                // takes them out of the vote below
+                M->neg_m[g][lane] = col0 + lane < it.rows ? 0.f : -CUDART_INF_F;
             }
             bar_sync(bar, 128);
             // from here on a tile needs masks: the first row's limit

@@ -639,7 +639,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     neg_m = mx == -CUDART_INF_F ? 0.f : -mx;
                 }
                 weigh();
-                if (__any_sync(0xffffffffu, top > kMoveAt)) {
+                // (lanes behind the half's queries hold another sequence's, or what no sequence
+                // has: they have no say)
+                if (__any_sync(0xffffffffu, top > kMoveAt && row < rows)) {
                     move();
                     weigh();
                 }

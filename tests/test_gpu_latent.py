@@ -938,3 +938,58 @@ def test_prefill_of_queries_that_are_not_finite(nq, nk, H, causal):
                 if np.isneginf(key @ qr[t, h]).all():
                     low.add((t, h))
     _check_poisoned(o, lse, r, rows, low, sees, "prefill")
+
+
+# ------------------------------------------------------------------ rows of others beside a sequence's
+def _others(q, at, seed):
+    """Contents for the queries `at`: zeros, scores that run by hundreds, infinities, NaN."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    for scale in (0.0, 30.0, -30.0, float("inf"), float("nan")):
+        wild = torch.randn(q[at].shape, generator=gen, device="cuda")
+        yield (wild * scale if abs(scale) < 100 else torch.full_like(wild, scale)).to(q.dtype)
+
+
+@pytest.mark.parametrize("H", [5, 20])
+@pytest.mark.parametrize("lens,news", [([700] * 200, [1] * 200), ([900, 30] * 150, [2, 1] * 150), ([9000], [1])])
+def test_decode_takes_nothing_from_other_rows(lens, news, H):
+    """A tile's columns that another sequence or none holds: their contents
+    leave a sequence's bits alone, however their scores run."""
+    import torch
+    c = Paged(64, lens, 64)
+    cu = np.cumsum([0] + news)
+    n = int(cu[-1])
+    q, _ = c.q(n + 3, H)
+    kept = [t for b in range(0, len(lens), 2) for t in range(cu[b], cu[b + 1])]
+    others = [t for t in range(n + 3) if t not in set(kept)]
+    for kept, others in ((kept, others), (list(range(n)), [n, n + 1, n + 2])):
+        kept, others = torch.tensor(kept, device="cuda"), torch.tensor(others, device="cuda")
+        want = None
+        for k, x in enumerate(_others(q, others, 70)):
+            q[others] = x
+            o, lse = _decode(c, q, cu)
+            _clear()
+            if want is None:
+                want = o[kept], lse[kept]
+            assert torch.equal(o[kept], want[0]) and torch.equal(lse[kept], want[1]), k
+        q[others] = torch.ones_like(q[others])
+
+
+@pytest.mark.parametrize("nq,nk,H", [([40], [380], 2), ([7, 130, 1], [350, 300, 200], 3), ([3], [9000], 1)])
+def test_prefill_takes_nothing_from_other_rows(nq, nk, H):
+    import torch
+    kda = _kda()
+    cu, cuk, (q, kv, pe), _ = _prefill_inputs(65, nq, nk, H, extra=20)
+    n = int(cu[-1])
+    for b in range(len(nq)):                                       # each sequence among others, then padding
+        kept = slice(int(cu[b]), int(cu[b + 1]))
+        others = torch.tensor([t for t in range(n + 20) if not cu[b] <= t < cu[b + 1]], device="cuda")
+        want = None
+        for k, x in enumerate(_others(q, others, 71)):
+            q[others] = x
+            o, lse = kda.latent_prefill(q, kv, pe, _i32(cu), _i32(cuk))
+            _clear()
+            if want is None:
+                want = o[kept].clone(), lse[kept].clone()
+            assert torch.equal(o[kept], want[0]) and torch.equal(lse[kept], want[1]), (b, k)
+        q[others] = torch.ones_like(q[others])
