@@ -384,7 +384,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         while (ok && walk.next(a, it)) {
             if (it.n == 0) continue;
             int rows = box_row(it, 0, true);
-            if (n_item > 0) ok = warp_wait_free(&M->x_empty, (n_item - 1) & 1, fail);
+            if (n_item > 0) ok = warp_wait(&M->x_empty, (n_item - 1) & 1, fail);
             if (!ok) break;
             ++n_x;
             if (lane == 0) {
@@ -397,7 +397,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 const int next_rows = i + 1 < it.n ? box_row(it, i + 1, true) : -1;
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t u = 4 * n_tile + j, slot = u % F::NP, use = u / F::NP;
-                    if (use > 0) ok = warp_wait_free(&M->empty_p[slot], (use - 1) & 1, fail);
+                    if (use > 0) ok = warp_wait(&M->empty_p[slot], (use - 1) & 1, fail);
                     if (!ok) break;
                     ++n_pair;
                     if (lane == 0) mbar_arrive_expect_tx(&M->full_p[slot], (uint32_t)live * brows * 256u);
@@ -408,7 +408,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 }
                 if (!ok) break;
                 const uint32_t slot = n_tile % F::NQ, use = n_tile / F::NQ;
-                if (use > 0) ok = warp_wait_free(&M->empty_r[slot], (use - 1) & 1, fail);
+                if (use > 0) ok = warp_wait(&M->empty_r[slot], (use - 1) & 1, fail);
                 if (!ok) break;
                 ++n_rope;
                 if (lane == 0) mbar_arrive_expect_tx(&M->full_r[slot], (uint32_t)live * brows * 128u);
@@ -477,7 +477,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                     for (int e = 0; e < 4; ++e)
                         mma_ss<true>(tmem + TM_S, rope + e * 32u, x_op + (8 * NR * 128u + e * 32u), id_s);
                     commit(s_full);
-                    if (i + 1 == it.n) mma_commit(&M->x_empty);
+                    if (i + 1 == it.n && ok) mma_commit(&M->x_empty);
                 }
                 __syncwarp();
                 // O^T += c^T P^T, a slot released as soon as its block is done (P's rows are one
@@ -493,9 +493,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                             if (e == 0) mma_ss<false>(tmem + TM_O + 64 * j, v, rope, id_o, i > 0);
                             else mma_ss<true>(tmem + TM_O + 64 * j, v + e * 4096u, rope + e * 2048u, id_o);
                         }
-                        commit(empty_p + 8 * at[j]);
+                        if (ok) commit(empty_p + 8 * at[j]);
                     }
-                    commit(empty_r + 8 * rslot);
+                    if (ok) commit(empty_r + 8 * rslot);
                     if (i + 1 == it.n) mma_commit(&M->o_full);
                 }
                 __syncwarp();
@@ -741,25 +741,25 @@ struct JoinArgs {
 // Weights of a row's pieces, in each group of L lanes a lane's of piece L e +
 // lane, from their log2-sum-exp; returns the row's.  NaN in a piece makes all of
 // them NaN; where none has any weight they are 0 for a blind row and NaN (0 / 0)
-// for one that sees positions, whose scores are all -inf.
+// for one that sees positions, whose scores are all -inf; ln 0 = -inf for both.
 template <int L, int E>
 __device__ __forceinline__ float join_weights(float (&v)[E], bool blind) {
-    float mx = v[0], sum = 0.f;
+    float mx = -kHuge, sum = 0.f;             // finite, so that no weight is -inf - -inf
 #pragma unroll
-    for (int e = 1; e < E; ++e) mx = fmaxf(mx, v[e]);
+    for (int e = 0; e < E; ++e) mx = fmaxf(mx, v[e]);
 #pragma unroll
     for (int off = L / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        v[e] = ex2_approx(v[e] - (mx == -CUDART_INF_F ? 0.f : mx));
+        v[e] = ex2_approx(v[e] - mx);
         sum += v[e];
     }
 #pragma unroll
     for (int off = L / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const float inv = sum != 0.f ? 1.f / sum : blind ? 0.f : CUDART_NAN_F;
+    const float inv = blind ? 0.f : 1.f / sum;
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] *= inv;
-    return sum != 0.f ? mx + log2f(sum) : -CUDART_INF_F;
+    return mx + log2f(sum);
 }
 __device__ __forceinline__ void add_scaled(float4 &acc, float w, const float4 &x) {
     acc.x = fmaf(w, x.x, acc.x);

@@ -365,7 +365,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             // half g's queries, once the tile before is done with theirs
             auto queries = [&](int g) {
                 if (w.n[g] == 0) return;
-                if (n_q[g] > 0) ok = ok && warp_wait_free(&M->q_empty[g], (n_q[g] - 1) & 1, fail);
+                if (n_q[g] > 0) ok = ok && warp_wait(&M->q_empty[g], (n_q[g] - 1) & 1, fail);
                 if (!ok) return;
                 ++n_q[g];
                 if (lane == 0) {
@@ -380,7 +380,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             for (int i = 0; ok && i < n; ++i) {
                 const int tok = w.k0 + (w.lo + i) * kTileK;
                 auto slot = [&](int c) { return sm + SM_RING + ((5 * n_v + c) % kSlots) * kSlot; };
-                if (u >= 2) ok = warp_wait_free(&M->v_empty[u & 1], ((u >> 1) - 1) & 1, fail);
+                if (u >= 2) ok = warp_wait(&M->v_empty[u & 1], ((u >> 1) - 1) & 1, fail);
                 if (!ok) break;
                 if (lane == 0) {
                     uint64_t *bar = &M->k_full[u & 1];
@@ -393,7 +393,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 ++u;
                 if (i == 0) queries(1);
                 if (!ok) break;
-                if (n_v >= 1) ok = warp_wait_free(&M->k_empty[(n_v - 1) & 1], ((n_v - 1) >> 1) & 1, fail);
+                if (n_v >= 1) ok = warp_wait(&M->k_empty[(n_v - 1) & 1], ((n_v - 1) >> 1) & 1, fail);
                 if (!ok) break;
                 if (lane == 0) {
                     uint64_t *bar = &M->v_full[n_v & 1];
@@ -461,7 +461,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             tc_fence_after();
             if (elect_one()) {
                 scores(0, tile);
-                if (n0 == 1) commit(q_empty);
+                if (n0 == 1 && ok) commit(q_empty);
             }
             __syncwarp();
         };
@@ -480,8 +480,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             tc_fence_after();
             if (elect_one()) {
                 if (n1 > 0) scores(1, u);
-                if (n1 == 1) commit(q_empty + 8);
-                commit(k_empty + 8 * (u & 1));
+                if (n1 == 1 && ok) commit(q_empty + 8);
+                if (ok) commit(k_empty + 8 * (u & 1));
             }
             __syncwarp();
             for (int i = 0; i < n; ++i, ++u) {
@@ -502,7 +502,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     tc_fence_after();
                     if (i + 1 < n0 && elect_one()) {
                         scores(0, x);
-                        if (i + 2 == n0) commit(q_empty);
+                        if (i + 2 == n0 && ok) commit(q_empty);
                     }
                     __syncwarp();
                 } else {
@@ -520,10 +520,10 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                         product(1, u, i > 0);
                         if (i + 1 == n1) commit(o_full + 8);
                     }
-                    commit(v_empty + 8 * (u & 1));
+                    if (ok) commit(v_empty + 8 * (u & 1));
                     if (i + 1 < n1) scores(1, x);
-                    if (i + 2 == n1) commit(q_empty + 8);
-                    if (i + 1 < n) commit(k_empty + 8 * (x & 1));
+                    if (i + 2 == n1 && ok) commit(q_empty + 8);
+                    if (i + 1 < n && ok) commit(k_empty + 8 * (x & 1));
                 }
                 __syncwarp();
             }
@@ -753,17 +753,18 @@ latent_prefill_join_kernel(const Args a) {
     wait_for_previous();                      // the pieces are written
     const int tok = (int)min(r / a.H, (int64_t)a.Tq - 1), b = seq_of_token(a.cu_q, a.N, tok);
     if (r >= rows || b < 0) return;           // behind the last sequence
-    float v = lane < a.pieces ? a.ws_lse[lane * rows + r] : -CUDART_INF_F, mx = v;
+    float v = lane < a.pieces ? a.ws_lse[lane * rows + r] : -CUDART_INF_F;
+    float mx = fmaxf(v, -kHuge);              // finite, so that no weight is -inf - -inf
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    v = ex2_approx(v - (mx == -CUDART_INF_F ? 0.f : mx));
+    v = ex2_approx(v - mx);
     float sum = v;                            // NaN where a piece's is
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     float inv = 1.f / sum;
-    if (sum == 0.f) {                         // the row sees nothing, or only scores of -inf (0 / 0)
+    if (sum == 0.f) {                         // the row sees nothing (0), or only scores of -inf (0 / 0)
         const int nk = a.cu_k[b + 1] - a.cu_k[b];
-        inv = (a.causal ? nk - (a.cu_q[b + 1] - tok) + 1 : nk) > 0 ? CUDART_NAN_F : 0.f;
+        if ((a.causal ? nk - (a.cu_q[b + 1] - tok) + 1 : nk) <= 0) inv = 0.f;
     }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -776,7 +777,7 @@ latent_prefill_join_kernel(const Args a) {
         acc.w = fmaf(f, x.w, acc.w);
     }
     reinterpret_cast<uint2 *>(a.o + r * 128)[lane] = make_uint2(pack_bf2(acc.x, acc.y), pack_bf2(acc.z, acc.w));
-    if (a.lse && lane == 0) a.lse[r] = sum == 0.f ? -CUDART_INF_F : (mx + log2f(sum)) * 0.6931471805599453f;
+    if (a.lse && lane == 0) a.lse[r] = (mx + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Work tiles there can be at most: n queries of a sequence are at most

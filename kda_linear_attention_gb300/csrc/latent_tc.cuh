@@ -11,6 +11,8 @@
 namespace kda {
 namespace tc {
 
+constexpr float kHuge = 3.402823466e38f;   // the largest finite number
+
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v) {
     uint32_t r[8];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -122,12 +124,10 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t *bar, uint32_t parity, vol
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *fail) {
     return __all_sync(0xffffffffu, wait_or_fail(bar, parity, fail));
 }
-// The same for the copy warp, before it arms a copy's barrier again: a role
-// that has given up goes on to the end of its tile, and may release what a copy
-// it did not wait for is still on its way to.
-__device__ __forceinline__ bool warp_wait_free(uint64_t *bar, uint32_t parity, volatile int *fail) {
-    return __all_sync(0xffffffffu, wait_or_fail(bar, parity, fail) && !*fail);
-}
+// A product warp that has given up goes on to the end of its key tile, but
+// releases nothing (the lane that issues asks its own verdict): the copy warp
+// would arm a barrier again whose last copy may be on its way.
+//
 // Ends a block's products before its tensor memory goes (one warp, the one
 // that issued them): they need nothing from the other roles, so this waits for
 // them whether a role has given up or not.
