@@ -15,12 +15,15 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
+// T tokens (>= 0) of H heads (>= 1): rows that 32 bits number.
+bool rows_in_32_bits(int64_t T, int H) { return T < (int64_t(1) << 31) && T * H < (int64_t(1) << 31); }
+
 // Sizes shared by the calls on a paged latent cache.
 int latent_cache_dims(int N, int64_t T, int64_t P, int page, int max_pages, int d_latent, int d_pe) {
     if (d_latent != kda::kLatentDim || d_pe != kda::kLatentPeDim) return KDA_ERR_DIM;
     if (N < 1 || T < 0 || T >= (int64_t(1) << 31) || P < 1 || max_pages < 1) return KDA_ERR_DIM;
     if (page < 16 || page > 1024 || (page & (page - 1)) != 0) return KDA_ERR_DIM;
-    if (P * page >= (int64_t(1) << 31) || P >= (int64_t(1) << 31)) return KDA_ERR_DIM;
+    if (P >= (int64_t(1) << 31) || P * page >= (int64_t(1) << 31)) return KDA_ERR_DIM;
     return KDA_OK;
 }
 
@@ -323,7 +326,7 @@ int kda_latent_gather(const void *cache, const int32_t *block_table, const int32
 
 size_t kda_latent_decode_workspace_bytes(int N, int64_t T, int H, int d_latent, int d_pe) {
     if (d_latent != kda::kLatentDim || d_pe != kda::kLatentPeDim || N < 1 || T < 1 || H < 1 ||
-        T * H >= (int64_t(1) << 31))
+        !rows_in_32_bits(T, H))
         return 0;
     return kda::latent_decode_workspace_bytes(N, T, H);
 }
@@ -334,7 +337,7 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
                       int d_latent, int d_pe, void *workspace, size_t ws_bytes, void *stream) {
     const int d = latent_cache_dims(N, T, P, page, max_pages, d_latent, d_pe);
     if (d != KDA_OK) return d;
-    if (H < 1 || T * H >= (int64_t(1) << 31) || (!cu_seqlens && T != N)) return KDA_ERR_DIM;
+    if (H < 1 || !rows_in_32_bits(T, H) || (!cu_seqlens && T != N)) return KDA_ERR_DIM;
     if (!(scale > 0.f) || scale - scale != 0.f) return KDA_ERR_VALUE;
     if (T == 0) return KDA_OK;
     if (!q || !cache || !block_table || !seq_lens || !o) return KDA_ERR_NULL;
@@ -351,7 +354,7 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
 
 size_t kda_latent_prefill_workspace_bytes(int N, int64_t Tq, int64_t Tk, int H, int d_nope, int d_pe, int dv) {
     if (d_nope != kda::kDK || d_pe != kda::kLatentPeDim || dv != kda::kDV || N < 1 || H < 1 || Tq < 1 || Tk < 0 ||
-        Tq * H >= (int64_t(1) << 31) || Tk * H >= (int64_t(1) << 31))
+        !rows_in_32_bits(Tq, H) || !rows_in_32_bits(Tk, H))
         return 0;
     return kda::latent_prefill_workspace_bytes(N, Tq, Tk, H);
 }
@@ -361,8 +364,7 @@ int kda_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t 
                        int causal, void *o, float *lse, int N, int64_t Tq, int64_t Tk, int H,
                        int d_nope, int d_pe, int dv, void *workspace, size_t ws_bytes, void *stream) {
     if (d_nope != kda::kDK || d_pe != kda::kLatentPeDim || dv != kda::kDV) return KDA_ERR_DIM;
-    if (N < 1 || H < 1 || Tq < 0 || Tk < 0 || Tq * H >= (int64_t(1) << 31) ||
-        Tk * H >= (int64_t(1) << 31))
+    if (N < 1 || H < 1 || Tq < 0 || Tk < 0 || !rows_in_32_bits(Tq, H) || !rows_in_32_bits(Tk, H))
         return KDA_ERR_DIM;
     if (k_pe_stride < d_pe || k_pe_stride % 8 != 0 || k_pe_stride >= (int64_t(1) << 31)) return KDA_ERR_DIM;
     if (!(scale > 0.f) || scale - scale != 0.f || (causal != 0 && causal != 1)) return KDA_ERR_VALUE;

@@ -135,3 +135,14 @@ def test_binding_fails_loudly_without_cuda_tensors():
     with pytest.raises(ValueError):
         kda.latent_prefill(torch.zeros(1, 2, 192, dtype=bf), torch.zeros(1, 2, 256, dtype=bf),
                            torch.zeros(1, 64, dtype=bf), cu)
+
+
+@pytest.mark.parametrize("T", [1 << 31, 1 << 33, 1 << 61, 1 << 62, (1 << 63) - 1])
+def test_lengths_past_32_bits_are_refused(L, T):
+    """Token counts whose product with the heads leaves 64 bits, too."""
+    for H in (1, 2, 4, 8):
+        assert _decode(L, T=T, H=H, cu=GOOD) == 2
+        assert _prefill(L, Tq=T, H=H) == 2 and _prefill(L, Tk=T, H=H) == 2 and _prefill(L, Tq=T, Tk=T, H=H) == 2
+        assert L.kda_latent_decode_workspace_bytes(2, T, H, 512, 64) == 0
+        assert L.kda_latent_prefill_workspace_bytes(1, T, 9000, H, 128, 64, 128) == 0
+        assert L.kda_latent_prefill_workspace_bytes(1, 16, T, H, 128, 64, 128) == 0
