@@ -993,3 +993,70 @@ def test_prefill_takes_nothing_from_other_rows(nq, nk, H):
                 want = o[kept].clone(), lse[kept].clone()
             assert torch.equal(o[kept], want[0]) and torch.equal(lse[kept], want[1]), (b, k)
         q[others] = torch.ones_like(q[others])
+
+
+# ------------------------------------------------------------------ wide pages, uncut key loops
+@pytest.mark.parametrize("page", [256, 512, 1024])
+def test_pages_wider_than_a_tile_of_positions(page):
+    """Append, gather and both forms of decode on pages that hold several
+    tiles of positions, lengths around the tiles' and the pages' borders."""
+    import torch
+    kda = _kda()
+    lens = [1, 127, 129, page - 1, page, page + 1, 2 * page + 130, 5 * page // 2, 0]
+    news = [1, 3, 0, 2, 129, 2, 131, 1, 0]
+    c = Paged(66, lens, page, nan=False)
+    cu = np.cumsum([0] + news)
+    n = int(cu[-1])
+    x, xr = _bf(c.rng.normal(size=(n, ol.ROW)))
+    c.ref = ol.append(xr, c.ref, c.table, lens, cu)
+    kda.latent_append(x, c.dev, c.table_dev, c.lens_dev, _i32(cu))
+    _clear()
+    assert np.array_equal(_np(c.dev), c.ref)
+    held = np.zeros((c.P, page), dtype=bool)
+    for b, m in enumerate(lens):
+        p = np.arange(m)
+        held[c.table[b, p // page], p % page] = True
+    c.dev[torch.from_numpy(~held).cuda()] = float("nan")
+    cuk = np.cumsum([0] + lens)
+    rows = kda.latent_gather(c.dev, c.table_dev, _i32(cuk), total=int(cuk[-1]))
+    _clear()
+    assert np.array_equal(_np(rows), np.concatenate([ol.sequence_rows(c.ref, c.table[b], 0, m)
+                                                     for b, m in enumerate(lens)]))
+    for H, offsets in ((5, cu), (16, None), (70, None)):
+        at = np.arange(len(lens) + 1) if offsets is None else offsets
+        q, qr = c.q(int(at[-1]), H)
+        o, lse = _decode(c, q, offsets)
+        _clear()
+        check(o, lse, ol.decode(qr, c.ref, c.table, lens, at, SCALE), "page %d, H=%d" % (page, H))
+
+
+@pytest.mark.parametrize("lens,ctx,H", [([4096], 0, 96), ([1024, 1000], 8192, 32), ([1, 700, 260, 1300], 0, 64),
+                                        ([300, 257], 2500, 96)])
+def test_prefill_uncut_against_the_oracle(lens, ctx, H):
+    """Many work tiles of many key tiles, taken over by running blocks, heads
+    in several groups: rows of first, middle and last tokens and heads."""
+    import torch
+    kda = _kda()
+    gen = torch.Generator(device="cuda").manual_seed(67)
+    cu, cuk = np.cumsum([0] + lens), np.cumsum([0] + [m + ctx for m in lens])
+
+    def normal(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+    q, kv, pe = normal(cu[-1], H, 192), normal(cuk[-1], H, 256), normal(cuk[-1], 64)
+    assert kda.latent_prefill_workspace_bytes(len(lens), int(cu[-1]), int(cuk[-1]), H) == 0
+    o, lse = kda.latent_prefill(q, kv, pe, _i32(cu), _i32(cuk))
+    _clear()
+    per = _np(pe)
+    for h in (0, 1, H // 2 - 1, H // 2, H - 2, H - 1):
+        qh, kvh = _np(q[:, h]), _np(kv[:, h])
+        for b, m in enumerate(lens):
+            k0 = int(cuk[b])
+            key = np.concatenate([kvh[k0:k0 + m + ctx, :128], per[k0:k0 + m + ctx]], 1)
+            value = kvh[k0:k0 + m + ctx, 128:]
+            toks = sorted({i for i in (0, 1, 127, 128, 255, 256, m // 2, m - 257, m - 2, m - 1) if 0 <= i < m})
+            r = ol.Result((len(toks), 1), 128)
+            for k, i in enumerate(toks):
+                r.put(k, 0, qh[cu[b] + i], key[:ctx + i + 1], value[:ctx + i + 1], SCALE)
+            at = torch.tensor([int(cu[b]) + i for i in toks], device="cuda")
+            check(o[at, h:h + 1], lse[at, h:h + 1], r, "uncut, head %d, sequence %d" % (h, b))
