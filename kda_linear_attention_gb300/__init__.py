@@ -547,8 +547,15 @@ def _refuse(dev, *tensors):
     raise ValueError("unsupported arguments")
 
 
+# torch's inner names of what its public calls wrap; a torch without them is
+# served by the public ones.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                       or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+
+
 def _raw_stream(dev, stream):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, like, stream):
@@ -563,9 +570,25 @@ def _empty(shape, dtype, like, stream):
 # around it (10 MB as a tensor add 7 us to a call's host time, as plain memory
 # 2 us).  It belongs to the stream (or to the graph being captured on it), so
 # that giving it back right after the launches is safe: what the stream does
-# later may have it next.
-_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)     # none in a torch without CUDA
+# later may have it next.  (A torch without these names gives a tensor.)
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
 _raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+
+
+def _take_workspace(nbytes, like, stream, raw_stream):
+    """(address, what holds it) of a call's own workspace, for _give_back."""
+    if not nbytes:
+        return None, None
+    if _raw_alloc is None or _raw_free is None:
+        t = _empty((nbytes,), torch.uint8, like, stream)
+        return t.data_ptr(), t
+    p = _raw_alloc(nbytes, raw_stream)
+    return p, p
+
+
+def _give_back(own):
+    if type(own) is int:          # a tensor goes with its last name
+        _raw_free(own)
 
 
 def _given_workspace(t, dev):
@@ -587,7 +610,7 @@ def latent_append(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     the latent part is RMS-normalised.  Returns cache.
     """
     dev = _device(x)
-    if dev != torch._C._cuda_getDevice():       # a launch goes to the current device
+    if dev != _current_device():       # a launch goes to the current device
         with torch.cuda.device(dev):
             return latent_append(x, cache, block_table, seq_lens, cu_seqlens, norm_w, eps, stream)
     N, xs, cs, ts = seq_lens.numel(), x.shape, cache.shape, block_table.shape
@@ -616,7 +639,7 @@ def latent_gather(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: to
     (``kda_latent_gather``).  total: the packed length cu_seqlens[N] (where
     ``out`` [total, 576] bf16 is not given).  Returns out."""
     dev = _device(cache)
-    if dev != torch._C._cuda_getDevice():       # a launch goes to the current device
+    if dev != _current_device():       # a launch goes to the current device
         with torch.cuda.device(dev):
             return latent_gather(cache, block_table, cu_seqlens, total, out, stream)
     if out is None:
@@ -659,7 +682,7 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
     one is given.
     """
     dev = _device(q)
-    if dev != torch._C._cuda_getDevice():       # a launch goes to the current device
+    if dev != _current_device():       # a launch goes to the current device
         with torch.cuda.device(dev):
             return latent_decode(q, cache, block_table, seq_lens, cu_seqlens, scale, o, lse, workspace, stream)
     N, qs, cs, ts = seq_lens.numel(), q.shape, cache.shape, block_table.shape
@@ -685,15 +708,14 @@ def latent_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tenso
         ws, nbytes = _given_workspace(workspace, dev)
     else:
         nbytes = latent_decode_workspace_bytes(N, T, H)
-        ws = own = _raw_alloc(nbytes, s) if nbytes else None
+        ws, own = _take_workspace(nbytes, q, stream, s)
     try:
         rc = lib().kda_latent_decode(
             q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
             None if cu_seqlens is None else cu_seqlens.data_ptr(), scale, o.data_ptr(), lse.data_ptr(),
             N, T, H, cs[0], cs[1], ts[1], LATENT, LATENT_PE, ws, nbytes, s)
     finally:
-        if own:
-            _raw_free(own)
+        _give_back(own)
     if rc != 0:
         raise KDAError(rc, "kda_latent_decode")
     return o, lse
@@ -722,7 +744,7 @@ def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seq
     comes from torch's allocator unless one is given.
     """
     dev = _device(q)
-    if dev != torch._C._cuda_getDevice():       # a launch goes to the current device
+    if dev != _current_device():       # a launch goes to the current device
         with torch.cuda.device(dev):
             return latent_prefill(q, kv, k_pe, cu_seqlens, cu_seqlens_k, scale, causal, o, lse, workspace, stream)
     if cu_seqlens_k is None:
@@ -756,15 +778,14 @@ def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seq
         ws, nbytes = _given_workspace(workspace, dev)
     else:
         nbytes = latent_prefill_workspace_bytes(N, Tq, Tk, H)
-        ws = own = _raw_alloc(nbytes, s) if nbytes else None
+        ws, own = _take_workspace(nbytes, q, stream, s)
     try:
         rc = lib().kda_latent_prefill(
             q.data_ptr(), kv.data_ptr(), k_pe.data_ptr(), pe_stride, cu_seqlens.data_ptr(),
             cu_seqlens_k.data_ptr(), scale, 1 if causal else 0, o.data_ptr(), lse.data_ptr(), N, Tq, Tk, H,
             DK, LATENT_PE, DV, ws, nbytes, s)
     finally:
-        if own:
-            _raw_free(own)
+        _give_back(own)
     if rc != 0:
         raise KDAError(rc, "kda_latent_prefill")
     return o, lse

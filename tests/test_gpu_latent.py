@@ -1060,3 +1060,32 @@ def test_prefill_uncut_against_the_oracle(lens, ctx, H):
                 r.put(k, 0, qh[cu[b] + i], key[:ctx + i + 1], value[:ctx + i + 1], SCALE)
             at = torch.tensor([int(cu[b]) + i for i in toks], device="cuda")
             check(o[at, h:h + 1], lse[at, h:h + 1], r, "uncut, head %d, sequence %d" % (h, b))
+
+
+def test_calls_without_torchs_inner_names(monkeypatch):
+    """Workspaces as tensors and torch's public names: the same bits, on
+    another stream and in a graph too."""
+    import torch
+    kda = _kda()
+    c = Paged(68, [3000, 300], 64)
+    q, _ = c.q(2, 16)
+    cu, cuk, (pq, kv, pe), _ = _prefill_inputs(69, [5], [9000], 2)
+    cu, cuk = _i32(cu), _i32(cuk)
+    want = _decode(c, q, None) + kda.latent_prefill(pq, kv, pe, cu, cuk)
+    monkeypatch.setattr(kda, "_raw_alloc", None)
+    monkeypatch.setattr(kda, "_raw_free", None)
+    monkeypatch.setattr(kda, "_current_device", torch.cuda.current_device)
+    monkeypatch.setattr(kda, "_current_raw_stream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = [_decode(c, q, None, stream=t) + kda.latent_prefill(pq, kv, pe, cu, cuk, stream=t)
+           for t in (None, s, s, None)]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        got.append(_decode(c, q, None) + kda.latent_prefill(pq, kv, pe, cu, cuk))
+    g.replay()
+    _clear()
+    for some in got:
+        for a, b in zip(some, want):
+            assert torch.equal(a, b)

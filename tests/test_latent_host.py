@@ -146,3 +146,30 @@ def test_lengths_past_32_bits_are_refused(L, T):
         assert L.kda_latent_decode_workspace_bytes(2, T, H, 512, 64) == 0
         assert L.kda_latent_prefill_workspace_bytes(1, T, 9000, H, 128, 64, 128) == 0
         assert L.kda_latent_prefill_workspace_bytes(1, 16, T, H, 128, 64, 128) == 0
+
+
+def test_binding_loads_in_a_torch_without_its_inner_names():
+    """The names that the latent calls take from torch._C for speed have
+    public stand-ins."""
+    import os
+    import subprocess
+    import sys
+    pytest.importorskip("torch")
+    script = """
+import torch
+for n in ("_cuda_cudaCachingAllocator_raw_alloc", "_cuda_cudaCachingAllocator_raw_delete", "_cuda_getDevice",
+          "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, n):
+        delattr(torch._C, n)
+import kda_linear_attention_gb300 as kda
+assert kda._raw_alloc is None and kda._raw_free is None
+assert kda._current_device is torch.cuda.current_device and callable(kda._current_raw_stream)
+address, own = kda._take_workspace(100, torch.zeros(1), None, 0)
+assert address == own.data_ptr() and own.numel() == 100 and own.dtype is torch.uint8
+kda._give_back(own)
+assert kda._take_workspace(0, torch.zeros(1), None, 0) == (None, None)
+kda._give_back(None)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
