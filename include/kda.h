@@ -446,7 +446,11 @@ int kda_latent_gather(const void *cache, const int32_t *block_table, const int32
  *
  *   q          [T, H, 576] bf16
  *   seq_lens   [N] int32: lengths with the new tokens counted in
- *   cu_seqlens [N + 1] int32, or NULL: one new token a sequence (then T = N)
+ *   cu_seqlens [N + 1] int32, or NULL: one new token a sequence (then T = N).
+ *              For 65 to 512 heads NULL is the faster way to say so: a
+ *              sequence's tiles of heads are then taken at the same time
+ *              (64 sequences of 2,000-4,096 tokens at 96 heads: 75 us, 91 us
+ *              with offsets)
  *   scale      > 0, finite
  *   o          [T, H, 512] bf16, written
  *   lse        [T, H] fp32, written, or NULL

@@ -19,7 +19,11 @@
 // else; p = exp2(s scale log2 e - m) with the m of the tile before, and only
 // when a score passes m by more than 8 (a factor 256, which fp32 sums and bf16
 // probabilities hold without loss) does the row take a new maximum, is O_g
-// rescaled in TMEM and the tile's p computed again.
+// rescaled in TMEM and the tile's p computed again.  p is rounded to bf16, the
+// product's operand type, after the fp32 sum has taken it: 2^-8 of each weight at
+// most, independent of the others', beside the bf16 output's own rounding
+// (against 64 bits 1.9e-3 to 2.3e-3 in the 2-norm; the output's rounding alone
+// makes 1.6e-3 to 1.7e-3).
 //
 // Few work tiles over many keys (a short chunk behind a long context) would
 // leave SMs idle: then the keys of each are cut into pieces, each a work tile
@@ -37,9 +41,9 @@
 // accumulators, and the waits between a half's product and its next scores; the
 // softmax (1,200 cycles a half) hides under the other half.  (Handing P over in
 // two halves of 64 keys, so that P V begins earlier, changed nothing: 394 us.)
-// Measured: 4,096 tokens at 96 heads 390 us (1.32 PFLOP/s of the causal
+// Measured: 4,096 tokens at 96 heads 392 us (1.32 PFLOP/s of the causal
 // multiply-adds, 70 % of the measured dense rate); 1,024 and 1,000 tokens
-// behind 8,192 at 32 heads 285 us (67 %: 256 equal work tiles on 152 SMs, two
+// behind 8,192 at 32 heads 286 us (67 %: 256 equal work tiles on 152 SMs, two
 // rounds).
 #include <algorithm>
 #include <type_traits>
@@ -125,9 +129,10 @@ __device__ __forceinline__ int queries_of(const Args &a, int b, bool flag) {
 }
 
 // Work tile `id` of the grid.  Heads are listed in groups whose keys and
-// values fit in L2 together; in a group, from the tiles of the last queries
-// (which see the most keys) to those of the first, so that what is handed out
-// last is short.
+// values fit in L2 together; in a group, the packed queries' tiles from the last
+// to the first: within a sequence what is handed out last sees the fewest keys.
+// (Over several the order is the batch's: a long sequence that comes first in it
+// is begun last.)
 __device__ __forceinline__ void get_work(const Args &a, const Misc *M, int id, Work &w) {
     const int tiles = M->tiles;
     w.valid = id >= 0 && (unsigned)id / a.pieces < (unsigned)tiles * (unsigned)a.H;
@@ -794,7 +799,11 @@ int64_t most_tiles(int N, int64_t Tq, int H) {
 // 131 KB written and read.  Measured against one piece, us a call: 1 head, 100
 // queries behind 4,000: 17 / 54; 256 behind 20,000: 25 / 283; 8 heads, 1,024
 // behind 8,192: 60 / 137; 2 heads, 4,096: 29 / 62; and where the count keeps
-// one: 16 heads, 300 behind 300: 16, two pieces 19.
+// one: 16 heads, 300 behind 300: 16, two pieces 19.  The host knows the average
+// alone: one long context among short ones is cut too little or not at all.  16
+// heads, 15 queries behind 300 each and 512 behind 65,536: one piece, 970 us (an
+// even share of the SMs would be 210); 8 chunks of 256, one of them behind
+// 100,000: three pieces, 535 us (160).
 int pieces_of(int N, int64_t Tq, int64_t Tk, int H) {
     const int64_t tiles = most_tiles(N, Tq, H);
     const double keys = (double)((Tk / N + kTileK - 1) / kTileK);
