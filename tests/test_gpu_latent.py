@@ -1089,3 +1089,59 @@ def test_calls_without_torchs_inner_names(monkeypatch):
     for some in got:
         for a, b in zip(some, want):
             assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """Caches, queries, outputs, keys and values of more than 4 GB, with the
+    rows that are used at their ends."""
+    import torch
+    kda = _kda()
+    rng, bf = _rng(72), torch.bfloat16
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of free device memory")
+    page, P, L = 64, 70_000, 300                                   # 5.2 GB
+    cache = torch.empty((P, page, ol.ROW), dtype=bf, device="cuda")
+    table = np.array([[P - 1 - 3 * i for i in range(5)], [P - 2 - 3 * i for i in range(5)]])
+    x, xr = _bf(rng.normal(size=(2 * L, ol.ROW)))
+    kda.latent_append(x, cache, _i32(table), _i32([L, L]), _i32([0, L, 2 * L]))
+    assert torch.equal(kda.latent_gather(cache, _i32(table), _i32([0, L, 2 * L]), total=2 * L), x)
+    T, H = 45_000, 96                                              # 5.0 GB of queries, 4.4 GB of outputs
+    q = torch.empty((T, H, ol.ROW), dtype=bf, device="cuda")
+    held, heldr = _bf(rng.normal(size=(3, H, ol.ROW)))
+    q[-3:] = held
+    o = torch.full((T, H, 512), 7.0, dtype=bf, device="cuda")
+    o, lse = kda.latent_decode(q, cache, _i32(table), _i32([L, L]), _i32([T - 3, T - 2, T]), o=o)
+    _clear()
+    r = ol.Result((3, H), 512)
+    for t, (b, n) in enumerate(((0, L), (1, L - 1), (1, L))):
+        for h in range(H):
+            r.put(t, h, heldr[t, h], xr[b * L:b * L + n], xr[b * L:b * L + n, :512], SCALE)
+    check(o[-3:], lse[-3:], r, "decode")
+    assert (o[:10] == 7.0).all() and (o[-13:-3] == 7.0).all()
+    del q, o, cache
+    Tq, Tk, nq, nk = 120_000, 100_000, 40, 400                     # 4.4 GB of queries, 4.9 GB of keys and values
+    q = torch.empty((Tq, H, 192), dtype=bf, device="cuda")
+    kv = torch.empty((Tk, H, 256), dtype=bf, device="cuda")
+    pe = torch.empty((Tk, 64), dtype=bf, device="cuda")
+    (hq, hqr), (hkv, hkvr), (hpe, hper) = (_bf(rng.normal(size=s)) for s in ((nq, H, 192), (nk, H, 256), (nk, 64)))
+    q[-nq:], kv[-nk:], pe[-nk:] = hq, hkv, hpe
+    o = torch.full((Tq, H, 128), 7.0, dtype=bf, device="cuda")
+    o, lse = kda.latent_prefill(q, kv, pe, _i32([Tq - nq, Tq]), _i32([Tk - nk, Tk]), o=o)
+    _clear()
+    check(o[-nq:], lse[-nq:], ol.prefill(hqr, hkvr, hper, [0, nq], [0, nk], SCALE), "prefill")
+    assert (o[:10] == 7.0).all() and (o[-nq - 10:-nq] == 7.0).all()
+
+
+def test_decode_of_few_tokens_among_many_sequences():
+    """Far more sequences than new tokens: tiles of 16 rows, several a token."""
+    kda = _kda()
+    N, H, lens = 400, 96, [(13 * i) % 90 for i in range(400)]
+    lens[7], lens[399] = 700, 260
+    news = [0] * N
+    news[7], news[100], news[399] = 2, 1, 1
+    c = Paged(73, lens, 16)
+    cu = np.cumsum([0] + news)
+    q, qr = c.q(int(cu[-1]), H)
+    o, lse = _decode(c, q, cu)
+    _clear()
+    check(o, lse, ol.decode(qr, c.ref, c.table, lens, cu, SCALE), "few tokens")
