@@ -154,7 +154,9 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
 // tile (of those it takes) that the host has set; none unless it has.
 #ifdef KDA_DEBUG
 static __device__ unsigned int g_leave_out = 0xffffffffu;
-inline cudaError_t set_leave_out(unsigned int tile) { return cudaMemcpyToSymbol(g_leave_out, &tile, sizeof(tile)); }
+static inline cudaError_t set_leave_out(unsigned int tile) {   // this translation unit's
+    return cudaMemcpyToSymbol(g_leave_out, &tile, sizeof(tile));
+}
 #endif
 __device__ __forceinline__ bool left_out(uint32_t tile) {
 #ifdef KDA_DEBUG
