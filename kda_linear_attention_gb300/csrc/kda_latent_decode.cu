@@ -22,10 +22,10 @@
 // row tile for what it costs beside them; with W units on G CTAs (one an SM)
 // each takes the next ceil(W / G), whatever the lengths are.  (The row tiles
 // of one token of many heads are taken side by side, by groups of CTAs that
-// share the units' numbering, where the call gives no offsets.)  A CTA's first and last row tile may be pieces
-// of longer ones: pieces are written normalised in fp32 with their
-// log2-sum-exp into the workspace, and a second kernel joins them in the order
-// of the positions (no atomics: the same bits every time).
+// share the units' numbering, where the call gives no offsets.)  A CTA's first
+// and last row tile may be pieces of longer ones: pieces are written normalised
+// in fp32 with their log2-sum-exp into the workspace, and a second kernel joins
+// them in the order of the positions (no atomics: the same bits every time).
 //
 // Roles: a copy warp (TMA boxes of one page each, and L2 prefetch of the next
 // tile's pages, whose rows are contiguous), an MMA warp, two groups of four
@@ -797,7 +797,7 @@ __device__ __forceinline__ void join_row(const JoinArgs &a, int c, const Split &
             for (int q = 0; q < W; ++q)
                 x[k][q] = k0 + k < n ? src[row * (kLatent / 4) + 32 * q] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (k0 == 0) lg = join_weights<L>(v, r < sp.blind);                 // behind the first loads
+        if (k0 == 0) lg = join_weights<L>(v, r < sp.blind);   // behind the first loads
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const float w = __shfl_sync(0xffffffffu, v[0], k0 + k);   // from the n-th on any: x is 0

@@ -128,6 +128,13 @@ __device__ __forceinline__ int queries_of(const Args &a, int b, bool flag) {
     return bad ? 0 : t1 - t0;
 }
 
+// First token of sequence b's keys, and keys (none of a range that leaves [0, Tk]).
+__device__ __forceinline__ void keys_of(const Args &a, int b, int &k0, int &nk) {
+    k0 = a.cu_k[b];
+    nk = a.cu_k[b + 1] - k0;
+    if (k0 < 0 || nk < 0 || k0 > a.Tk - nk) k0 = nk = 0;
+}
+
 // Work tile `id` of the grid.  Heads are listed in groups whose keys and
 // values fit in L2 together; in a group, the packed queries' tiles from the last
 // to the first: within a sequence what is handed out last sees the fewest keys.
@@ -159,9 +166,7 @@ __device__ __forceinline__ void get_work(const Args &a, const Misc *M, int id, W
         nq = queries_of(a, ++b, false);
     }
     w.q0 = a.cu_q[b];
-    w.k0 = a.cu_k[b];
-    w.nk = a.cu_k[b + 1] - w.k0;
-    if (w.k0 < 0 || w.nk < 0 || w.k0 > a.Tk - w.nk) w.k0 = w.nk = 0;
+    keys_of(a, b, w.k0, w.nk);
     w.i0 = k * kTileQ;
     w.first = w.nk - nq + 1;
 #pragma unroll
@@ -768,7 +773,8 @@ latent_prefill_join_kernel(const Args a) {
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     float inv = 1.f / sum;
     if (sum == 0.f) {                         // the row sees nothing (0), or only scores of -inf (0 / 0)
-        const int nk = a.cu_k[b + 1] - a.cu_k[b];
+        int k0, nk;
+        keys_of(a, b, k0, nk);
         if ((a.causal ? nk - (a.cu_q[b + 1] - tok) + 1 : nk) <= 0) inv = 0.f;
     }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -1145,3 +1145,15 @@ def test_decode_of_few_tokens_among_many_sequences():
     o, lse = _decode(c, q, cu)
     _clear()
     check(o, lse, ol.decode(qr, c.ref, c.table, lens, cu, SCALE), "few tokens")
+
+
+@pytest.mark.parametrize("nq,Tk", [(5, 9000), (40, 200)])
+def test_prefill_over_a_broken_range_of_keys_sees_nothing(nq, Tk):
+    """In pieces and whole: a flagged key range counts as none."""
+    kda = _kda()
+    cu, _, (q, kv, pe), _ = _prefill_inputs(74, [nq], [Tk], 2)
+    assert (kda.latent_prefill_workspace_bytes(1, nq, Tk, 2) > 0) == (Tk == 9000)
+    for bad in ([0, Tk + 1], [-1, Tk], [Tk, 5]):
+        o, lse = kda.latent_prefill(q, kv, pe, _i32(cu), _i32(bad))
+        _clear(1)
+        assert (o == 0).all() and np.isneginf(_np(lse)).all(), bad
