@@ -505,6 +505,105 @@ int kda_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t 
  * invalid sizes). */
 size_t kda_latent_prefill_workspace_bytes(int N, int64_t Tq, int64_t Tk, int H, int d_nope, int d_pe, int dv);
 
+/* ---------------------------------------------------------------------------
+ * Positions rotated into queries and rows, for latent-attention layers that
+ * have them (the model's own do without).  The 64 shared key channels, and the
+ * queries' channels against them, are d / 2 pairs; pair i of a token at
+ * position p is turned by the angle p f_i:
+ *     y_a = amplitude (x_a cos - x_b sin),   y_b = amplitude (x_b cos + x_a sin)
+ * with (a, b) = (i, i + d / 2) for KDA_ROTARY_HALF, (2 i, 2 i + 1) for
+ * KDA_ROTARY_INTERLEAVED.  The frequencies come as turns[i] = f_i / (2 pi) in
+ * whole 2^-64ths of a turn a position (int64, wrapping): p turns[i] is the
+ * angle's part of a turn exactly, at any position, so that positions far out
+ * lose nothing.  Scaled frequencies and amplitudes (for contexts longer than
+ * those trained on) are only other numbers in turns and amplitude.
+ *
+ * Token i of sequence b's n new ones is at position seq_lens[b] - n + i, the
+ * place that kda_latent_append gives its row.  A token before position 0 raises
+ * bit 0 of the device error word and is left as it was.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Rotate the d channels that x's rows point at.
+ *
+ *   x, out     T x H rows of d channels, a row's channels side by side; strides
+ *              in elements between tokens and heads, multiples of 16 bytes.  A
+ *              part of a head is given by its first channel's address.  out may
+ *              be x (with x's strides) and does not overlap it otherwise
+ *   turns      [d / 2] int64
+ *   seq_lens   [N] int32: lengths with the new tokens counted in
+ *   cu_seqlens [N + 1] int32, or NULL: one new token a sequence (then T = N)
+ *   amplitude  finite
+ *   inverse    1: by the opposite angles, with the same amplitude: the
+ *              transpose, which takes the gradient of out to that of x
+ *   d          a multiple of 16, 16 to 256
+ *   dtype      KDA_BF16 or KDA_F32, of x and out; the arithmetic is fp32, with
+ *              one rounding
+ * Rows that no sequence holds are not written.  Returns KDA_OK or a
+ * kda_status_t; T = 0 is a no-op.
+ */
+#define KDA_ROTARY_HALF 0
+#define KDA_ROTARY_INTERLEAVED 1
+int kda_latent_rotate(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *out,
+                      int64_t out_token_stride, int64_t out_head_stride, const int64_t *turns,
+                      const int32_t *seq_lens, const int32_t *cu_seqlens, float amplitude, int layout,
+                      int inverse, int N, int64_t T, int H, int d, int dtype, void *stream);
+
+/*
+ * kda_latent_append with the shared part rotated to the row's position on the
+ * way (one rounding to bf16).  turns [d_pe / 2] int64; amplitude and layout as
+ * for kda_latent_rotate; all else as for kda_latent_append.
+ */
+int kda_latent_append_rotated(const void *x, void *cache, const int32_t *block_table,
+                              const int32_t *seq_lens, const int32_t *cu_seqlens, const float *norm_w,
+                              float eps, const int64_t *turns, float amplitude, int layout, int N,
+                              int64_t T, int64_t P, int page, int max_pages, int d_latent, int d_pe,
+                              void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The latent cache in 4 bits: 416 bytes a token instead of 1,152,
+ *     row = [codes (256) | r (128, 64 bf16) | scales (32)].
+ * The 512 latent channels are e2m1 codes, two a byte (the even channel in the
+ * low half), in groups of 16 with an e4m3 scale each; a channel stands for
+ * code * scale * 2^exponent, which bf16 holds exactly.  The exponent, -32 to 32,
+ * is one number for a cache: group maxima below 6 * 2^-10 * 2^exponent are
+ * stored as zeros and magnitudes above 2688 * 2^exponent saturate, so the
+ * default 0 is right for latents of ordinary size.  The shared part keeps its
+ * bits.  The cache is [P, page, 416] bytes; pages, block tables, offsets and
+ * errors are those of the bf16 cache.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Write new tokens' rows: the row that kda_latent_append (turns NULL) or
+ * kda_latent_append_rotated would store, in bf16, and then in 4 bits: a
+ * group's scale is its largest magnitude over 6 rounded to e4m3, its codes are
+ * the channels over that scale rounded to e2m1 (both to nearest even).  A group
+ * with a NaN reads back as NaN; infinities saturate.
+ */
+int kda_latent4_append(const void *x, void *cache, const int32_t *block_table, const int32_t *seq_lens,
+                       const int32_t *cu_seqlens, const float *norm_w, float eps, const int64_t *turns,
+                       float amplitude, int layout, int exponent, int N, int64_t T, int64_t P, int page,
+                       int max_pages, int d_latent, int d_pe, void *stream);
+
+/* kda_latent_gather from a 4-bit cache: out [T, 576] bf16 holds what the rows
+ * stand for. */
+int kda_latent4_gather(const void *cache, const int32_t *block_table, const int32_t *cu_seqlens,
+                       void *out, int exponent, int N, int64_t T, int64_t P, int page, int max_pages,
+                       int d_latent, int d_pe, void *stream);
+
+/*
+ * kda_latent_decode over a 4-bit cache: the same arguments, outputs and rules,
+ * with what the rows stand for in the rows' place.  workspace:
+ * kda_latent4_decode_workspace_bytes(N, T, H, ...) bytes.
+ */
+int kda_latent4_decode(const void *q, const void *cache, const int32_t *block_table,
+                       const int32_t *seq_lens, const int32_t *cu_seqlens, float scale, int exponent,
+                       void *o, float *lse, int N, int64_t T, int H, int64_t P, int page, int max_pages,
+                       int d_latent, int d_pe, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace of kda_latent4_decode (0 for invalid sizes). */
+size_t kda_latent4_decode_workspace_bytes(int N, int64_t T, int H, int d_latent, int d_pe);
+
 /*
  * Gives back the memory that the library's workspace pool on the current
  * device keeps between kda_prefill_chunked / _events / _gated /

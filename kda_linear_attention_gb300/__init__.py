@@ -28,6 +28,16 @@ The hybrid model's other token mixer, latent attention over a paged cache
     rows = latent_gather(cache, block_table, cu_seqlens_k, total)          # rows back, to expand
     o, lse = latent_prefill(q, kv, k_pe, cu_seqlens_q, cu_seqlens_k)       # expanded, causal
 
+Positions rotated into its queries and rows, and the same cache in 4 bits
+(416 bytes a token, uint8 [P, page, 416]):
+
+    turns, amplitude = rotary_turns(64, base=1e4, method="yarn", factor=8, trained_length=4096)
+    latent_rotate(q[..., 128:], turns, seq_lens, cu_seqlens, amplitude=amplitude)   # in place
+    latent_append_rotated(x, cache, block_table, seq_lens, turns, cu_seqlens, amplitude=amplitude)
+    latent4_append(x, cache4, block_table, seq_lens, cu_seqlens, norm_w=w, turns=turns, amplitude=amplitude)
+    o, lse = latent4_decode(q, cache4, block_table, seq_lens, cu_seqlens)
+    rows = latent4_gather(cache4, block_table, cu_seqlens_k, total)
+
 Shapes of the recurrence (token-major): q, k, g [T, H, 128]; v [T, H, 128]; beta [T, H];
 S [N, H, 128, 128] fp32; q/k/v bf16 or fp32, g/beta fp32.
 """
@@ -35,6 +45,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from typing import Optional, Tuple
 
@@ -45,6 +56,8 @@ __all__ = ["prefill_chunked", "prefill_chunked_noalloc", "prefill_chunked_events
            "decode_step_pool", "conv_prologue", "prefill_chunked_gated", "prefill_layer",
            "decode_layer_step", "latent_append", "latent_gather", "latent_decode",
            "latent_decode_workspace_bytes", "latent_prefill", "latent_prefill_workspace_bytes",
+           "rotary_turns", "latent_rotate", "latent_append_rotated", "latent4_append", "latent4_gather",
+           "latent4_decode", "latent4_decode_workspace_bytes",
            "device_error", "lib",
            "KDAError", "KDA_BF16", "KDA_F32", "library_path"]
 
@@ -134,6 +147,22 @@ def lib() -> ctypes.CDLL:
         L.kda_latent_prefill.restype = i32
         L.kda_latent_prefill_workspace_bytes.argtypes = [i32, i64, i64, i32, i32, i32, i32]
         L.kda_latent_prefill_workspace_bytes.restype = ctypes.c_size_t
+        L.kda_latent_rotate.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, vp, f32, i32, i32, i32, i64, i32, i32,
+                                        i32, vp]
+        L.kda_latent_rotate.restype = i32
+        L.kda_latent_append_rotated.argtypes = [vp, vp, vp, vp, vp, vp, f32, vp, f32, i32, i32, i64, i64, i32, i32,
+                                                i32, i32, vp]
+        L.kda_latent_append_rotated.restype = i32
+        L.kda_latent4_append.argtypes = [vp, vp, vp, vp, vp, vp, f32, vp, f32, i32, i32, i32, i64, i64, i32, i32,
+                                         i32, i32, vp]
+        L.kda_latent4_append.restype = i32
+        L.kda_latent4_gather.argtypes = [vp, vp, vp, vp, i32, i32, i64, i64, i32, i32, i32, i32, vp]
+        L.kda_latent4_gather.restype = i32
+        L.kda_latent4_decode.argtypes = [vp, vp, vp, vp, vp, f32, i32, vp, vp, i32, i64, i32, i64, i32, i32, i32,
+                                         i32, vp, ctypes.c_size_t, vp]
+        L.kda_latent4_decode.restype = i32
+        L.kda_latent4_decode_workspace_bytes.argtypes = L.kda_latent_decode_workspace_bytes.argtypes
+        L.kda_latent4_decode_workspace_bytes.restype = ctypes.c_size_t
         L.kda_workspace_release.argtypes = []
         L.kda_workspace_release.restype = i32
         L.kda_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint), i32]
@@ -791,6 +820,277 @@ def latent_prefill(q: torch.Tensor, kv: torch.Tensor, k_pe: torch.Tensor, cu_seq
         _give_back(own)
     if rc != 0:
         raise KDAError(rc, "kda_latent_prefill")
+    return o, lse
+
+
+# ------------------------------------------------------- positions and the 4-bit cache
+LATENT4_ROW = LATENT // 2 + 2 * LATENT_PE + LATENT // 16   # bytes of a 4-bit row
+_I64, _U8 = torch.int64, torch.uint8
+
+
+def rotary_turns(d: int = LATENT_PE, base: float = 10000.0, method: Optional[str] = None, factor: float = 1.0,
+                 trained_length: Optional[int] = None, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 frequencies=None, device="cuda") -> Tuple[torch.Tensor, float]:
+    """The rotation of d channels for the calls below: (turns, amplitude).
+
+    turns [d / 2] int64 holds each pair's frequency in 2^-64ths of a turn a
+    position.  The frequencies are base^(-2 i / d) radians a position, or
+    ``frequencies`` (d / 2 numbers, taken as they are), changed for contexts
+    ``factor`` times as long as those trained on by ``method``:
+
+      None      not
+      "linear"  all divided by factor
+      "ntk"     of the base times factor^(d / (d - 2))
+      "yarn"    divided by factor where a pair makes fewer than beta_slow turns
+                in trained_length positions, kept where it makes more than
+                beta_fast, between by a ramp over the pairs; amplitude
+                0.1 ln(factor) + 1
+    """
+    if d < 2 or d % 2 or d > 256:
+        raise ValueError("d must be even, 2 to 256")
+    if not (math.isfinite(factor) and factor > 0 and math.isfinite(base) and base > 0):
+        raise ValueError("base and factor must be positive and finite")
+    if method not in (None, "linear", "ntk", "yarn"):
+        raise ValueError("method must be None, 'linear', 'ntk' or 'yarn'")
+    amplitude = 1.0
+    if frequencies is not None:
+        if method is not None:
+            raise ValueError("frequencies are taken as they are: give no method with them")
+        f = [float(x) for x in frequencies]
+        if len(f) != d // 2 or not all(math.isfinite(x) for x in f):
+            raise ValueError("frequencies must be %d finite numbers" % (d // 2))
+    else:
+        if method == "ntk":
+            if d == 2:
+                raise ValueError("'ntk' needs d > 2")
+            base = base * factor ** (d / (d - 2))
+        f = [base ** (-2.0 * i / d) for i in range(d // 2)]
+        if method == "linear":
+            f = [x / factor for x in f]
+        elif method == "yarn":
+            if not trained_length or trained_length < 1:
+                raise ValueError("'yarn' needs trained_length")
+            if base == 1.0 or not beta_fast > beta_slow > 0:
+                raise ValueError("'yarn' needs a base other than 1 and beta_fast > beta_slow > 0")
+
+            def pair_of(turns):       # the (fractional) pair that makes so many turns in trained_length
+                return d * math.log(trained_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+            lo = max(0, math.floor(pair_of(beta_fast)))
+            hi = min(d - 1, math.ceil(pair_of(beta_slow)))
+            ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3))) for i in range(d // 2)]
+            f = [x / factor * r + x * (1 - r) for x, r in zip(f, ramp)]
+            amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    whole = [round(x / (2 * math.pi) * 2.0 ** 64) & (2 ** 64 - 1) for x in f]
+    turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in whole], dtype=_I64)
+    return turns.to(device), amplitude
+
+
+def _turns_ok(t, n, dev) -> bool:
+    return isinstance(t, _Tensor) and t.shape == (n,) and _plain(t, _I64, dev)
+
+
+def latent_rotate(x: torch.Tensor, turns: torch.Tensor, seq_lens: torch.Tensor,
+                  cu_seqlens: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  amplitude: float = 1.0, interleaved: bool = False, inverse: bool = False,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Rotate rows by their tokens' positions (``kda_latent_rotate``).
+
+    x [T, H, d] bf16 or fp32 with dense channels, tokens and heads any multiple
+    of 16 bytes apart, so that a part of a head is given as ``q[..., 128:]``;
+    turns [d / 2] int64 (``rotary_turns``); seq_lens [N] (the new tokens counted
+    in) and cu_seqlens [N + 1] int32 (None: one new token a sequence).  Pairs are
+    channels (i, i + d / 2), or (2 i, 2 i + 1) with interleaved.  inverse: by the
+    opposite angles, which takes the gradient of out to that of x.  Writes and
+    returns out (a tensor like x that shares no memory with it), or x itself
+    where none is given.
+    """
+    dev = _device(x)
+    if dev != _current_device():       # a launch goes to the current device
+        with torch.cuda.device(dev):
+            return latent_rotate(x, turns, seq_lens, cu_seqlens, out, amplitude, interleaved, inverse, stream)
+    if out is None:
+        out = x
+    N, xs = seq_lens.numel(), x.shape
+    if not (len(xs) == 3 and x.dtype in (_BF16, _F32) and _turns_ok(turns, xs[2] // 2, dev)
+            and seq_lens.dim() == 1 and _plain(seq_lens, _I32, dev)
+            and (cu_seqlens is None or cu_seqlens.shape == (N + 1,) and _plain(cu_seqlens, _I32, dev))):
+        if not isinstance(x, _Tensor) or x.dim() != 3 or x.dtype not in (_BF16, _F32):
+            raise ValueError("x must be [T, H, d] bfloat16 or float32")
+        _refuse(dev, ("turns", turns, _I64, (xs[2] // 2,)), ("seq_lens", seq_lens, _I32, (N,)),
+                ("cu_seqlens", cu_seqlens, _I32, (N + 1,)))
+    T, H, d = xs
+    if out is not x and not (isinstance(out, _Tensor) and out.shape == xs and out.dtype is x.dtype
+                             and out.get_device() == dev):
+        raise ValueError("out must be a tensor like x: %s %s on %s" % (tuple(xs), x.dtype, x.device))
+    # the stride of a dimension of one row means nothing
+    st, so = x.stride(), out.stride()
+    if (st[2] != 1 or so[2] != 1) and T * H > 0:
+        raise ValueError("the channels of x and out must lie side by side")
+    rc = lib().kda_latent_rotate(
+        x.data_ptr(), st[0] if T > 1 else 0, st[1] if H > 1 else 0, out.data_ptr(), so[0] if T > 1 else 0,
+        so[1] if H > 1 else 0, turns.data_ptr(), seq_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), amplitude, 1 if interleaved else 0,
+        1 if inverse else 0, N, T, H, d, KDA_BF16 if x.dtype is _BF16 else KDA_F32, _raw_stream(dev, stream))
+    if rc != 0:
+        raise KDAError(rc, "kda_latent_rotate")
+    return out
+
+
+def _append_args(dev, row, x, cache, cache_dtype, block_table, seq_lens, cu_seqlens, norm_w, turns):
+    """N of an append call whose tensors are right; the others raise."""
+    N, xs, cs, ts = seq_lens.numel(), x.shape, cache.shape, block_table.shape
+    if not (len(xs) == 2 and xs[1] == LATENT_ROW and _plain(x, _BF16, dev)
+            and len(cs) == 3 and cs[2] == row and _plain(cache, cache_dtype, dev)
+            and len(ts) == 2 and ts[0] == N and _plain(block_table, _I32, dev)
+            and seq_lens.dim() == 1 and _plain(seq_lens, _I32, dev)
+            and (cu_seqlens is None or cu_seqlens.shape == (N + 1,) and _plain(cu_seqlens, _I32, dev))
+            and (norm_w is None or norm_w.shape == (LATENT,) and _plain(norm_w, _F32, dev))
+            and (turns is None or _turns_ok(turns, LATENT_PE // 2, dev))):
+        _refuse(dev, ("x", x, _BF16, (-1, LATENT_ROW)), ("cache", cache, cache_dtype, (-1, -1, row)),
+                ("block_table", block_table, _I32, (N, -1)), ("seq_lens", seq_lens, _I32, (N,)),
+                ("cu_seqlens", cu_seqlens, _I32, (N + 1,)), ("norm_w", norm_w, _F32, (LATENT,)),
+                ("turns", turns, _I64, (LATENT_PE // 2,)))
+    return N
+
+
+def latent_append_rotated(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                          seq_lens: torch.Tensor, turns: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None,
+                          norm_w: Optional[torch.Tensor] = None, eps: float = NORM_EPS, amplitude: float = 1.0,
+                          interleaved: bool = False, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``latent_append`` with the rows' shared part rotated to their positions
+    on the way (``kda_latent_append_rotated``).  turns [32] int64 and amplitude
+    from ``rotary_turns``.  Returns cache."""
+    dev = _device(x)
+    if dev != _current_device():       # a launch goes to the current device
+        with torch.cuda.device(dev):
+            return latent_append_rotated(x, cache, block_table, seq_lens, turns, cu_seqlens, norm_w, eps, amplitude,
+                                         interleaved, stream)
+    if turns is None:
+        raise ValueError("turns must be a tensor of 1 dimensions")
+    N = _append_args(dev, LATENT_ROW, x, cache, _BF16, block_table, seq_lens, cu_seqlens, norm_w, turns)
+    P, page, _ = cache.shape
+    rc = lib().kda_latent_append_rotated(
+        x.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), None if norm_w is None else norm_w.data_ptr(),
+        eps, turns.data_ptr(), amplitude, 1 if interleaved else 0, N, x.shape[0], P, page, block_table.shape[1],
+        LATENT, LATENT_PE, _raw_stream(dev, stream))
+    if rc != 0:
+        raise KDAError(rc, "kda_latent_append_rotated")
+    return cache
+
+
+def latent4_append(x: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                   cu_seqlens: Optional[torch.Tensor] = None, norm_w: Optional[torch.Tensor] = None,
+                   eps: float = NORM_EPS, turns: Optional[torch.Tensor] = None, amplitude: float = 1.0,
+                   interleaved: bool = False, exponent: int = 0, stream: Optional[torch.cuda.Stream] = None
+                   ) -> torch.Tensor:
+    """Write new tokens' rows into the 4-bit latent cache (``kda_latent4_append``):
+    what ``latent_append``, or with turns ``latent_append_rotated``, would store,
+    its latent part in e2m1 codes with an e4m3 scale for 16 channels.
+
+    x [T, 576] bf16; cache [P, page, 416] uint8, updated in place; the other
+    arguments as for ``latent_append_rotated``.  exponent: the cache's unit,
+    2^exponent (the same number in every call on a cache).  Returns cache.
+    """
+    dev = _device(x)
+    if dev != _current_device():       # a launch goes to the current device
+        with torch.cuda.device(dev):
+            return latent4_append(x, cache, block_table, seq_lens, cu_seqlens, norm_w, eps, turns, amplitude,
+                                  interleaved, exponent, stream)
+    N = _append_args(dev, LATENT4_ROW, x, cache, _U8, block_table, seq_lens, cu_seqlens, norm_w, turns)
+    P, page, _ = cache.shape
+    rc = lib().kda_latent4_append(
+        x.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), None if norm_w is None else norm_w.data_ptr(),
+        eps, None if turns is None else turns.data_ptr(), amplitude, 1 if interleaved else 0, exponent, N,
+        x.shape[0], P, page, block_table.shape[1], LATENT, LATENT_PE, _raw_stream(dev, stream))
+    if rc != 0:
+        raise KDAError(rc, "kda_latent4_append")
+    return cache
+
+
+def latent4_gather(cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                   total: Optional[int] = None, out: Optional[torch.Tensor] = None, exponent: int = 0,
+                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """``latent_gather`` from a 4-bit cache [P, page, 416] uint8: what its rows
+    stand for, in bf16, which holds it exactly (``kda_latent4_gather``).  Returns
+    out [total, 576]."""
+    dev = _device(cache)
+    if dev != _current_device():       # a launch goes to the current device
+        with torch.cuda.device(dev):
+            return latent4_gather(cache, block_table, cu_seqlens, total, out, exponent, stream)
+    if out is None:
+        if total is None:
+            raise ValueError("give the packed length (total) or the output (out)")
+        out = _empty((total, LATENT_ROW), _BF16, cache, stream)
+    N, os, cs, ts = cu_seqlens.numel() - 1, out.shape, cache.shape, block_table.shape
+    if not (len(os) == 2 and os[1] == LATENT_ROW and _plain(out, _BF16, dev)
+            and len(cs) == 3 and cs[2] == LATENT4_ROW and _plain(cache, _U8, dev)
+            and len(ts) == 2 and ts[0] == N and _plain(block_table, _I32, dev)
+            and cu_seqlens.dim() == 1 and _plain(cu_seqlens, _I32, dev)):
+        _refuse(dev, ("cache", cache, _U8, (-1, -1, LATENT4_ROW)), ("block_table", block_table, _I32, (N, -1)),
+                ("cu_seqlens", cu_seqlens, _I32, (N + 1,)), ("out", out, _BF16, (-1, LATENT_ROW)))
+    rc = lib().kda_latent4_gather(cache.data_ptr(), block_table.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(),
+                                  exponent, N, os[0], cs[0], cs[1], ts[1], LATENT, LATENT_PE, _raw_stream(dev, stream))
+    if rc != 0:
+        raise KDAError(rc, "kda_latent4_gather")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def latent4_decode_workspace_bytes(N: int, T: int, H: int) -> int:
+    """Bytes of workspace of ``latent4_decode`` (``kda_latent4_decode_workspace_bytes``)."""
+    return int(lib().kda_latent4_decode_workspace_bytes(int(N), int(T), int(H), LATENT, LATENT_PE))
+
+
+def latent4_decode(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                   cu_seqlens: Optional[torch.Tensor] = None, scale: float = LATENT_SCALE, exponent: int = 0,
+                   o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+                   ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``latent_decode`` over a 4-bit cache [P, page, 416] uint8
+    (``kda_latent4_decode``): the same arguments, outputs and rules.  The
+    workspace (``latent4_decode_workspace_bytes``) comes from torch's allocator
+    unless one is given."""
+    dev = _device(q)
+    if dev != _current_device():       # a launch goes to the current device
+        with torch.cuda.device(dev):
+            return latent4_decode(q, cache, block_table, seq_lens, cu_seqlens, scale, exponent, o, lse, workspace,
+                                  stream)
+    N, qs, cs, ts = seq_lens.numel(), q.shape, cache.shape, block_table.shape
+    if not (len(qs) == 3 and qs[2] == LATENT_ROW and _plain(q, _BF16, dev)
+            and len(cs) == 3 and cs[2] == LATENT4_ROW and _plain(cache, _U8, dev)
+            and len(ts) == 2 and ts[0] == N and _plain(block_table, _I32, dev)
+            and seq_lens.dim() == 1 and _plain(seq_lens, _I32, dev)
+            and (cu_seqlens is None or cu_seqlens.shape == (N + 1,) and _plain(cu_seqlens, _I32, dev))):
+        _refuse(dev, ("q", q, _BF16, (-1, -1, LATENT_ROW)), ("cache", cache, _U8, (-1, -1, LATENT4_ROW)),
+                ("block_table", block_table, _I32, (N, -1)), ("seq_lens", seq_lens, _I32, (N,)),
+                ("cu_seqlens", cu_seqlens, _I32, (N + 1,)))
+    T, H, _ = qs
+    if o is None:
+        o = _empty((T, H, LATENT), _BF16, q, stream)
+    elif not (o.shape == (T, H, LATENT) and _plain(o, _BF16, dev)):
+        _refuse(dev, ("o", o, _BF16, (T, H, LATENT)))
+    if lse is None:
+        lse = _empty((T, H), _F32, q, stream)
+    elif not (lse.shape == (T, H) and _plain(lse, _F32, dev)):
+        _refuse(dev, ("lse", lse, _F32, (T, H)))
+    s, own = _raw_stream(dev, stream), None
+    if workspace is not None:
+        ws, nbytes = _given_workspace(workspace, dev)
+    else:
+        nbytes = latent4_decode_workspace_bytes(N, T, H)
+        ws, own = _take_workspace(nbytes, q, stream, s)
+    try:
+        rc = lib().kda_latent4_decode(
+            q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            None if cu_seqlens is None else cu_seqlens.data_ptr(), scale, exponent, o.data_ptr(), lse.data_ptr(),
+            N, T, H, cs[0], cs[1], ts[1], LATENT, LATENT_PE, ws, nbytes, s)
+    finally:
+        _give_back(own)
+    if rc != 0:
+        raise KDAError(rc, "kda_latent4_decode")
     return o, lse
 
 

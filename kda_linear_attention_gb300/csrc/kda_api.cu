@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int kVersion = 300;   // 0.3.0: latent attention over a paged cache
+constexpr int kVersion = 400;   // 0.4.0: rotary positions, the latent cache in 4 bits
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -25,6 +25,24 @@ int latent_cache_dims(int N, int64_t T, int64_t P, int page, int max_pages, int 
     if (page < 16 || page > 1024 || (page & (page - 1)) != 0) return KDA_ERR_DIM;
     if (P >= (int64_t(1) << 31) || P * page >= (int64_t(1) << 31)) return KDA_ERR_DIM;
     return KDA_OK;
+}
+
+// The numbers of a rotation.
+int rotation_status(float amplitude, int layout) {
+    if (amplitude - amplitude != 0.f || (layout != KDA_ROTARY_HALF && layout != KDA_ROTARY_INTERLEAVED))
+        return KDA_ERR_VALUE;
+    return KDA_OK;
+}
+
+int exponent_status(int exponent) {
+    return exponent < -kda::kLatent4Exponent || exponent > kda::kLatent4Exponent ? KDA_ERR_VALUE : KDA_OK;
+}
+
+// Strides of rows of d elements of e bytes: rows apart by whole 16 bytes, and
+// all of T x H rows within 63 bits of bytes.
+bool row_strides(int64_t token, int64_t head, int64_t e) {
+    const int64_t most = int64_t(1) << 31;
+    return token >= 0 && head >= 0 && token < most && head < most && token * e % 16 == 0 && head * e % 16 == 0;
 }
 
 }  // namespace
@@ -382,21 +400,135 @@ int kda_latent_prefill(const void *q, const void *kv, const void *k_pe, int64_t 
                                                   static_cast<cudaStream_t>(stream)));
 }
 
+int kda_latent_rotate(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *out,
+                      int64_t out_token_stride, int64_t out_head_stride, const int64_t *turns,
+                      const int32_t *seq_lens, const int32_t *cu_seqlens, float amplitude, int layout,
+                      int inverse, int N, int64_t T, int H, int d, int dtype, void *stream) {
+    if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_DTYPE;
+    if (N < 1 || T < 0 || H < 1 || H > (1 << 24) || !rows_in_32_bits(T, H)) return KDA_ERR_DIM;
+    if (d < 16 || d > 256 || d % 16 != 0 || (!cu_seqlens && T != N)) return KDA_ERR_DIM;
+    const int64_t e = dtype == KDA_BF16 ? 2 : 4;
+    if (!row_strides(x_token_stride, x_head_stride, e) || !row_strides(out_token_stride, out_head_stride, e))
+        return KDA_ERR_DIM;
+    const int r = rotation_status(amplitude, layout);
+    if (r != KDA_OK) return r;
+    if (inverse != 0 && inverse != 1) return KDA_ERR_VALUE;
+    if (T == 0) return KDA_OK;
+    if (!x || !out || !turns || !seq_lens) return KDA_ERR_NULL;
+    const void *ptrs[] = {x, out, turns, seq_lens, cu_seqlens};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_latent_rotate(
+        x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride,
+        kda::Rotation{turns, amplitude, layout == KDA_ROTARY_INTERLEAVED}, inverse != 0, seq_lens, cu_seqlens, N, T, H, d,
+        dtype == KDA_BF16, static_cast<cudaStream_t>(stream)));
+}
+
+int kda_latent_append_rotated(const void *x, void *cache, const int32_t *block_table,
+                              const int32_t *seq_lens, const int32_t *cu_seqlens, const float *norm_w,
+                              float eps, const int64_t *turns, float amplitude, int layout, int N,
+                              int64_t T, int64_t P, int page, int max_pages, int d_latent, int d_pe,
+                              void *stream) {
+    const int d = latent_cache_dims(N, T, P, page, max_pages, d_latent, d_pe);
+    if (d != KDA_OK) return d;
+    if (!cu_seqlens && T != N) return KDA_ERR_DIM;
+    if (!(eps >= 0.f)) return KDA_ERR_VALUE;
+    const int r = rotation_status(amplitude, layout);
+    if (r != KDA_OK) return r;
+    if (T == 0) return KDA_OK;
+    if (!x || !cache || !block_table || !seq_lens || !turns) return KDA_ERR_NULL;
+    const void *ptrs[] = {x, cache, block_table, seq_lens, cu_seqlens, norm_w, turns};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_latent_append_rotated(
+        x, cache, block_table, seq_lens, cu_seqlens, norm_w, eps,
+        kda::Rotation{turns, amplitude, layout == KDA_ROTARY_INTERLEAVED}, N, T, P, page, max_pages,
+        static_cast<cudaStream_t>(stream)));
+}
+
+int kda_latent4_append(const void *x, void *cache, const int32_t *block_table, const int32_t *seq_lens,
+                       const int32_t *cu_seqlens, const float *norm_w, float eps, const int64_t *turns,
+                       float amplitude, int layout, int exponent, int N, int64_t T, int64_t P, int page,
+                       int max_pages, int d_latent, int d_pe, void *stream) {
+    const int d = latent_cache_dims(N, T, P, page, max_pages, d_latent, d_pe);
+    if (d != KDA_OK) return d;
+    if (!cu_seqlens && T != N) return KDA_ERR_DIM;
+    if (!(eps >= 0.f)) return KDA_ERR_VALUE;
+    const int r = rotation_status(amplitude, layout);
+    if (r != KDA_OK) return r;
+    if (exponent_status(exponent) != KDA_OK) return KDA_ERR_VALUE;
+    if (T == 0) return KDA_OK;
+    if (!x || !cache || !block_table || !seq_lens) return KDA_ERR_NULL;
+    const void *ptrs[] = {x, cache, block_table, seq_lens, cu_seqlens, norm_w, turns};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_latent4_append(
+        x, cache, block_table, seq_lens, cu_seqlens, norm_w, eps,
+        kda::Rotation{turns, amplitude, layout == KDA_ROTARY_INTERLEAVED}, exponent, N, T, P, page, max_pages,
+        static_cast<cudaStream_t>(stream)));
+}
+
+int kda_latent4_gather(const void *cache, const int32_t *block_table, const int32_t *cu_seqlens,
+                       void *out, int exponent, int N, int64_t T, int64_t P, int page, int max_pages,
+                       int d_latent, int d_pe, void *stream) {
+    const int d = latent_cache_dims(N, T, P, page, max_pages, d_latent, d_pe);
+    if (d != KDA_OK) return d;
+    if (exponent_status(exponent) != KDA_OK) return KDA_ERR_VALUE;
+    if (T == 0) return KDA_OK;
+    if (!cache || !block_table || !cu_seqlens || !out) return KDA_ERR_NULL;
+    const void *ptrs[] = {cache, block_table, cu_seqlens, out};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_latent4_gather(cache, block_table, cu_seqlens, out, exponent, N, T, P, page,
+                                                  max_pages, static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_latent4_decode_workspace_bytes(int N, int64_t T, int H, int d_latent, int d_pe) {
+    if (d_latent != kda::kLatentDim || d_pe != kda::kLatentPeDim || N < 1 || T < 1 || H < 1 ||
+        !rows_in_32_bits(T, H))
+        return 0;
+    return kda::latent4_decode_workspace_bytes(N, T, H);
+}
+
+int kda_latent4_decode(const void *q, const void *cache, const int32_t *block_table,
+                       const int32_t *seq_lens, const int32_t *cu_seqlens, float scale, int exponent,
+                       void *o, float *lse, int N, int64_t T, int H, int64_t P, int page, int max_pages,
+                       int d_latent, int d_pe, void *workspace, size_t ws_bytes, void *stream) {
+    const int d = latent_cache_dims(N, T, P, page, max_pages, d_latent, d_pe);
+    if (d != KDA_OK) return d;
+    if (H < 1 || !rows_in_32_bits(T, H) || (!cu_seqlens && T != N)) return KDA_ERR_DIM;
+    if (!(scale > 0.f) || scale - scale != 0.f || exponent_status(exponent) != KDA_OK) return KDA_ERR_VALUE;
+    if (T == 0) return KDA_OK;
+    if (!q || !cache || !block_table || !seq_lens || !o) return KDA_ERR_NULL;
+    const void *ptrs[] = {q, cache, block_table, seq_lens, cu_seqlens, o, lse};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_ALIGN;
+    const size_t need = kda::latent4_decode_workspace_bytes(N, T, H);
+    if (need > 0 && (!workspace || ws_bytes < need)) return KDA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_ALIGN;
+    return cuda_status(kda::launch_latent4_decode(q, cache, block_table, seq_lens, cu_seqlens, scale, exponent, o,
+                                                  lse, N, T, H, P, page, max_pages, workspace,
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
 int kda_workspace_release(void) { return cuda_status(kda::release_workspace_pool()); }
 
 int kda_device_error(unsigned int *code, int reset) {
     if (!code) return KDA_ERR_NULL;
-    unsigned int a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0;
-    const cudaError_t e1 = kda::read_device_error(&a, reset != 0);
-    const cudaError_t e2 = kda::read_decode_error(&b, reset != 0);
-    const cudaError_t e3 = kda::read_layer_error(&c, reset != 0);
-    const cudaError_t e4 = kda::read_simt_error(&d, reset != 0);
-    const cudaError_t e5 = kda::read_latent_error(&f, reset != 0);
-    const cudaError_t e6 = kda::read_latent_prefill_error(&g, reset != 0);
-    const cudaError_t e7 = kda::read_latent_decode_error(&h, reset != 0);
-    *code = a | b | c | d | f | g | h;
-    for (const cudaError_t e : {e1, e2, e3, e4, e5, e6, e7})
-        if (e != cudaSuccess) return cuda_status(e);
+    cudaError_t (*const words[])(unsigned int *, bool) = {
+        kda::read_device_error, kda::read_decode_error,         kda::read_layer_error,
+        kda::read_simt_error,   kda::read_latent_error,         kda::read_latent_prefill_error,
+        kda::read_latent_decode_error, kda::read_rotary_error,  kda::read_latent4_error,
+        kda::read_latent4_decode_error};
+    cudaError_t first = cudaSuccess;
+    *code = 0;
+    for (const auto read : words) {
+        unsigned int w = 0;
+        const cudaError_t e = read(&w, reset != 0);
+        *code |= w;
+        if (first == cudaSuccess) first = e;
+    }
+    if (first != cudaSuccess) return cuda_status(first);
     return KDA_OK;
 }
 

@@ -168,6 +168,43 @@ cudaError_t launch_latent_prefill(const void *q, const void *kv, const void *k_p
                                   cudaStream_t stream);
 size_t latent_prefill_workspace_bytes(int N, int64_t Tq, int64_t Tk, int H);
 cudaError_t read_latent_prefill_error(unsigned int *code, bool reset);
+
+// A rotation of channel pairs by their token's position (kda.h): turns in
+// 2^-64ths of a turn a position.  turns == nullptr: none.
+struct Rotation {
+    const int64_t *turns;
+    float amplitude;
+    bool interleaved;
+};
+// ... of any part of the heads' rows (kda_rotary.cu); strides in elements.
+cudaError_t launch_latent_rotate(const void *x, int64_t x_token, int64_t x_head, void *out, int64_t out_token,
+                                 int64_t out_head, const Rotation &rot, bool inverse, const int32_t *seq_lens,
+                                 const int32_t *cu, int N, int64_t T, int H, int d, bool bf16,
+                                 cudaStream_t stream);
+cudaError_t read_rotary_error(unsigned int *code, bool reset);
+// ... of the shared part of rows on their way into the cache (kda_latent.cu).
+cudaError_t launch_latent_append_rotated(const void *x, void *cache, const int32_t *table,
+                                         const int32_t *seq_lens, const int32_t *cu, const float *norm_w,
+                                         float eps, const Rotation &rot, int N, int64_t T, int64_t P,
+                                         int page, int max_pages, cudaStream_t stream);
+// The latent cache in 4 bits (kda_latent4.cu, kda_latent4_decode.cu): rows of
+// kLatent4Row bytes, channels that stand for code * scale * 2^exponent.
+constexpr int kLatent4Row = kLatentDim / 2 + kLatentPeDim * 2 + kLatentDim / 16;
+constexpr int kLatent4Exponent = 32;   // largest magnitude of the exponent
+cudaError_t launch_latent4_append(const void *x, void *cache, const int32_t *table, const int32_t *seq_lens,
+                                  const int32_t *cu, const float *norm_w, float eps, const Rotation &rot,
+                                  int exponent, int N, int64_t T, int64_t P, int page, int max_pages,
+                                  cudaStream_t stream);
+cudaError_t launch_latent4_gather(const void *cache, const int32_t *table, const int32_t *cu, void *out,
+                                  int exponent, int N, int64_t T, int64_t P, int page, int max_pages,
+                                  cudaStream_t stream);
+cudaError_t read_latent4_error(unsigned int *code, bool reset);
+size_t latent4_decode_workspace_bytes(int N, int64_t T, int H);
+cudaError_t launch_latent4_decode(const void *q, const void *cache, const int32_t *table,
+                                  const int32_t *seq_lens, const int32_t *cu, float scale, int exponent,
+                                  void *o, float *lse, int N, int64_t T, int H, int64_t P, int page,
+                                  int max_pages, void *ws, cudaStream_t stream);
+cudaError_t read_latent4_decode_error(unsigned int *code, bool reset);
 #ifdef KDA_DEBUG
 // The key tile whose arrival the kernel leaves out (latent_tc.cuh).
 cudaError_t latent_decode_leave_out(unsigned int tile);

@@ -1,0 +1,97 @@
+// Pieces shared by the kernels that write and read cached rows: the offsets'
+// check, the latent part's RMS norm, the rotation of the shared part.
+#pragma once
+
+#include "latent_tc.cuh"
+
+namespace kda {
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+}
+
+// Block 0 raises bit 0 of its file's error word for offsets that decrease or leave [0, T] (the rest of
+// the kernel stays inside its buffers whatever they are).
+__device__ __forceinline__ void check_offsets(const int32_t *cu, int N, int T, unsigned int *error) {
+    if (!cu || blockIdx.x != 0) return;
+    bool bad = false;
+    for (int b = threadIdx.x; b < N; b += blockDim.x) bad |= cu[b] < 0 || cu[b + 1] < cu[b] || cu[b + 1] > T;
+    if (bad) atomicOr(error, kErrWait);
+}
+
+// ---- the RMS norm of a row's latent part, eight channels at a time
+__device__ __forceinline__ float sumsq8(uint4 u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = bf2_to_f2(w[e]);
+        s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
+    }
+    return s;
+}
+__device__ __forceinline__ uint4 scale8(uint4 u, float n, const float *w) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(w));
+    const float4 b = __ldg(reinterpret_cast<const float4 *>(w) + 1);
+    const float2 x0 = bf2_to_f2(u.x), x1 = bf2_to_f2(u.y), x2 = bf2_to_f2(u.z), x3 = bf2_to_f2(u.w);
+    return make_uint4(f2_to_bf2(make_float2(x0.x * n * a.x, x0.y * n * a.y)),
+                      f2_to_bf2(make_float2(x1.x * n * a.z, x1.y * n * a.w)),
+                      f2_to_bf2(make_float2(x2.x * n * b.x, x2.y * n * b.y)),
+                      f2_to_bf2(make_float2(x3.x * n * b.z, x3.y * n * b.w)));
+}
+
+// ---- rotation
+// cos and sin (times the amplitude) of the angle of `pair` at position pos >= 0.
+// pos * turns wraps at whole turns, so what is left is the angle's part of a turn
+// to 2^-64 of its frequency's rounding; its upper 32 bits, signed, go on in fp32
+// (2^-25 of a half turn).
+__device__ __forceinline__ float2 rotation_of(const Rotation &rot, int pair, int pos) {
+    const uint64_t turn = (uint64_t)pos * (uint64_t)rot.turns[pair];
+    const int32_t half_turns = (int32_t)((turn + 0x80000000ull) >> 32);   // in 2^-31 of a half turn
+    float s, c;
+    sincospif((float)half_turns * 0x1p-31f, &s, &c);
+    return make_float2(c * rot.amplitude, s * rot.amplitude);
+}
+__device__ __forceinline__ float2 rotated(float a, float b, float2 cs) {
+    return make_float2(a * cs.x - b * cs.y, b * cs.x + a * cs.y);
+}
+// The shared part of a row by one warp, a pair a lane: read ...
+__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *pe, int lane, bool interleaved) {
+    if (interleaved) return bf2_to_f2(reinterpret_cast<const uint32_t *>(pe)[lane]);
+    return make_float2(__bfloat162float(pe[lane]), __bfloat162float(pe[lane + kLatentPeDim / 2]));
+}
+// ... and written with one rounding.
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *pe, int lane, bool interleaved, float2 v) {
+    if (interleaved) {
+        reinterpret_cast<uint32_t *>(pe)[lane] = f2_to_bf2(v);
+    } else {
+        pe[lane] = __float2bfloat16_rn(v.x);
+        pe[lane + kLatentPeDim / 2] = __float2bfloat16_rn(v.y);
+    }
+}
+static_assert(kLatentPeDim == 64, "a pair a lane");
+
+// Where a new token's row goes: its position and cache row; a row of -1 for a
+// token that no sequence holds, and for a bad place, whose bit it raises.
+struct NewRow {
+    int pos;
+    int64_t row;
+};
+__device__ __forceinline__ NewRow new_row(const PagedRows &pages, const int32_t *seq_lens, const int32_t *cu, int N,
+                                          int t, int lane, unsigned int *error) {
+    const int s = seq_of_token(cu, N, t);
+    if (s < 0) return NewRow{0, -1};       // behind the last sequence
+    const int start = cu ? cu[s] : s, count = cu ? cu[s + 1] - start : 1;
+    const long long pos = (long long)seq_lens[s] - count + (t - start);
+    if (pos < 0 || pos >= pages.max_len()) {
+        if (lane == 0) atomicOr(error, kErrWait);
+        return NewRow{0, -1};
+    }
+    const int64_t row = pages.row(s, (int)pos);
+    if (row < 0 && lane == 0) atomicOr(error, kErrSlot);
+    return NewRow{(int)pos, row};
+}
+
+}  // namespace kda
