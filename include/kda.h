@@ -569,8 +569,8 @@ int kda_latent_append_rotated(const void *x, void *cache, const int32_t *block_t
  * is one number for a cache: group maxima below 6 * 2^-10 * 2^exponent are
  * stored as zeros and magnitudes above 2688 * 2^exponent saturate, so the
  * default 0 is right for latents of ordinary size.  The shared part keeps its
- * bits.  The cache is [P, page, 416] bytes; pages, block tables, offsets and
- * errors are those of the bf16 cache.
+ * bits.  The cache is [P, page, 416] bytes, 32-byte aligned; pages, block tables,
+ * offsets and errors are those of the bf16 cache.
  * ------------------------------------------------------------------------- */
 
 /*

@@ -12,6 +12,8 @@ namespace {
 constexpr int kVersion = 400;   // 0.4.0: rotary positions, the latent cache in 4 bits
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// 4-bit rows are read in sectors of 32 bytes.
+bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
@@ -57,7 +59,7 @@ const char *kda_status_string(int status) {
         case KDA_ERR_NULL: return "a required pointer is NULL";
         case KDA_ERR_DIM: return "unsupported or inconsistent sizes (dk = dv = 128, N >= 1, H >= 1; latent rows 512 + 64, page a power of two)";
         case KDA_ERR_CHUNK: return "chunk must be 16, 32 or 64";
-        case KDA_ERR_ALIGN: return "a pointer is not 16-byte aligned";
+        case KDA_ERR_ALIGN: return "a pointer is not aligned (16 bytes; 32 for a 4-bit cache; 256 for a workspace)";
         case KDA_ERR_DTYPE: return "dtype must be KDA_BF16 or KDA_F32";
         case KDA_ERR_WORKSPACE: return "workspace could not be allocated or is too small";
         case KDA_ERR_CUDA: return "CUDA launch error";
@@ -462,6 +464,7 @@ int kda_latent4_append(const void *x, void *cache, const int32_t *block_table, c
     const void *ptrs[] = {x, cache, block_table, seq_lens, cu_seqlens, norm_w, turns};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_ALIGN;
+    if (!aligned32(cache)) return KDA_ERR_ALIGN;
     return cuda_status(kda::launch_latent4_append(
         x, cache, block_table, seq_lens, cu_seqlens, norm_w, eps,
         kda::Rotation{turns, amplitude, layout == KDA_ROTARY_INTERLEAVED}, exponent, N, T, P, page, max_pages,
@@ -479,6 +482,7 @@ int kda_latent4_gather(const void *cache, const int32_t *block_table, const int3
     const void *ptrs[] = {cache, block_table, cu_seqlens, out};
     for (const void *p : ptrs)
         if (!aligned16(p)) return KDA_ERR_ALIGN;
+    if (!aligned32(cache)) return KDA_ERR_ALIGN;
     return cuda_status(kda::launch_latent4_gather(cache, block_table, cu_seqlens, out, exponent, N, T, P, page,
                                                   max_pages, static_cast<cudaStream_t>(stream)));
 }
@@ -503,6 +507,7 @@ int kda_latent4_decode(const void *q, const void *cache, const int32_t *block_ta
     const void *ptrs[] = {q, cache, block_table, seq_lens, cu_seqlens, o, lse};
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return KDA_ERR_ALIGN;
+    if (!aligned32(cache)) return KDA_ERR_ALIGN;
     const size_t need = kda::latent4_decode_workspace_bytes(N, T, H);
     if (need > 0 && (!workspace || ws_bytes < need)) return KDA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return KDA_ERR_ALIGN;

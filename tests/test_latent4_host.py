@@ -10,6 +10,7 @@ import pytest
 
 GOOD = ctypes.c_void_p(0x10000)   # aligned, never dereferenced
 OFF4 = ctypes.c_void_p(0x10004)
+OFF16 = ctypes.c_void_p(0x10010)  # not in whole sectors
 NAN, INF = float("nan"), float("inf")
 
 
@@ -90,13 +91,14 @@ def test_append_rotated_rejects_bad_arguments(L, kw, status):
 
 @pytest.mark.parametrize("kw,status", BAD_CACHE + BAD_ROTATION + BAD_EXPONENT + [
     (dict(T=3), 2), (dict(eps=-1.0), 8), (dict(x=None), 1), (dict(cache=None), 1), (dict(table=None), 1),
-    (dict(lens=None), 1), (dict(x=OFF4), 4), (dict(cache=OFF4), 4), (dict(turns=OFF4), 4)])
+    (dict(lens=None), 1), (dict(x=OFF4), 4), (dict(cache=OFF16), 4), (dict(turns=OFF4), 4)])
 def test_append4_rejects_bad_arguments(L, kw, status):
     assert _append4(L, **kw) == status
 
 
 @pytest.mark.parametrize("kw,status", BAD_CACHE + BAD_EXPONENT + [
-    (dict(cache=None), 1), (dict(table=None), 1), (dict(cu=None), 1), (dict(out=None), 1), (dict(out=OFF4), 4)])
+    (dict(cache=None), 1), (dict(table=None), 1), (dict(cu=None), 1), (dict(out=None), 1), (dict(out=OFF4), 4),
+    (dict(cache=OFF16), 4)])
 def test_gather4_rejects_bad_arguments(L, kw, status):
     assert _gather4(L, **kw) == status
 
@@ -105,7 +107,7 @@ def test_gather4_rejects_bad_arguments(L, kw, status):
     (dict(T=3), 2), (dict(H=0), 2), (dict(H=1 << 30), 2), (dict(scale=0.0), 8), (dict(scale=-1.0), 8),
     (dict(scale=INF), 8), (dict(scale=NAN), 8), (dict(q=None), 1), (dict(cache=None), 1), (dict(o=None), 1),
     (dict(table=None), 1), (dict(lens=None), 1), (dict(q=OFF4), 4), (dict(lse=OFF4), 4), (dict(o=OFF4), 4),
-    (dict(ws=ctypes.c_void_p(0x10010)), 4)])
+    (dict(ws=OFF16), 4), (dict(cache=OFF16), 4)])
 def test_decode4_rejects_bad_arguments(L, kw, status):
     assert _decode4(L, **kw) == status
 
