@@ -15,17 +15,30 @@
 // 2^16, and what lies under fp16's normal numbers is below 2^-21 of the row's
 // largest weight.  Sums are fp32, of the unrounded probabilities.
 //
-// Work is dealt out and pieces are joined as in latent_walk.cuh says.  Roles: an
-// MMA warp, two groups of four softmax warps that each take half of the rows,
-// and eight producer warps.  A producer thread has one position and half of its
-// channels: it reads them straight from the pages (a whole sector a load, the
-// next tile's as soon as a register is free, so a tile's time hides HBM), turns
-// codes into fp16 once and writes them twice: into the 32 KB slot that the
-// second product reads MN-major, and, as the first product's operand A, into
-// TMEM, whose reads cost no shared-memory bandwidth.  TMEM holds S (up to 64
-// columns), O (4 blocks), the shared channels (32) and as many blocks of 128
-// channels (64 columns each) as fit beside them; the others are read K-major
-// from their slot.
+// Work is dealt out and pieces are joined as latent_walk.cuh says.  Sixteen
+// warps, which leaves a thread 128 registers:
+//   - two groups of four softmax warps that each take half of the rows.  The
+//     first of them issues the products: between a tile's P and the next tile's
+//     scores it has nothing else to do;
+//   - two groups of four producer warps, one for the even blocks of 128 channels
+//     and one for the odd ones.  Four lanes take a position's 64 bytes of codes of
+//     a block, turn them into fp16 and write them into the block's 32 KB slot,
+//     which is both products' operand A, K-major for the first, MN-major for the
+//     second.
+// A slot is free as soon as its block of the second product is done, and a
+// block's scores begin as soon as it is written; a block is turned into fp16
+// before its slot is free.
+//
+// A producer thread copies what it will read next into 64 bytes of its own
+// (cp.async, which needs no register and no line of the first-level cache:
+// beside 227 KB of shared memory that holds some 200, and plain loads a tile
+// ahead took two to three times as long), and reads it when its block's turn
+// comes; the rows are on their way from HBM to L2 a tile before.
+// The shared-memory writes of all roles are ordered before the tensor core's
+// reads by the warp that issues the products, between having seen the arrivals
+// and issuing: a fence in the writing threads would wait for their copies in
+// flight.  The roles' code is kept small for the instruction cache, and nothing
+// of a tile's is spilled.
 #include "latent4.cuh"
 #include "latent_walk.cuh"
 
@@ -41,34 +54,66 @@ __device__ unsigned int g_kda_latent4_decode_error = 0;
 namespace {
 
 constexpr int kSoftWarps = 8, kFeedWarps = 8;
-constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps + 1);
+constexpr int kThreads = 32 * (kSoftWarps + kFeedWarps);
 constexpr uint32_t kSlot = 32768;         // 128 positions x 128 channels: [16 groups][2 blocks][8 rows][128 B]
-constexpr uint32_t kProbs = 16384;        // P [128][64]
+constexpr uint32_t kProbs = 16384;        // P [128][64], the shared channels [128][64]
 constexpr float kLift = 7.f;              // log2 of what a row's largest weight is held at
 constexpr float kMoveAt = 15.f;           // ... of what a weight may reach
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kMisc = 4096;
+
+constexpr uint32_t TM_S = 0, TM_O = 64;   // S^T: 64 columns; O^T: 4 blocks of 64
+
+constexpr uint32_t kAhead = 64 * 32 * kFeedWarps;   // 64 bytes a producer thread
+constexpr uint32_t kScales = 1024 * kFeedWarps;     // of 32 rows, a warp
 
 template <int NR>
 struct Cfg {
-    // TMEM columns, every part at a multiple of 32
-    static constexpr uint32_t S = 0, O = 64, OB = NR <= 32 ? 32 : 64, R = O + 4 * OB, K = R + 32;
-    static constexpr int KB = NR <= 32 ? 4 : 2;                  // blocks of K in TMEM
-    static_assert(K + 64 * KB <= kTmemCols, "tensor memory");
-    // shared memory
     static constexpr uint32_t X = 0;
     static constexpr uint32_t C = NR * 1152u;
-    static constexpr uint32_t P = C + 4 * kSlot;
-    static constexpr uint32_t MISC = P + kProbs;
-    static constexpr uint32_t BYTES = MISC + 4096;
+    static constexpr uint32_t P = C + 4 * kSlot;                 // the shared channels, then P
+    static constexpr uint32_t RAW = P + kProbs;
+    static constexpr uint32_t SC = RAW + kAhead;
+    static constexpr uint32_t MISC = SC + kScales;
+    static constexpr uint32_t BYTES = MISC + kMisc;
     static_assert(BYTES + 1024 <= 232448, "shared memory of an SM");
 };
 
+// A producer warp's walk over the row tiles, which lies in shared memory: it is
+// looked at once a row tile, and a thread's registers are for what a tile needs.
+// Lane 0 walks.
+struct Steps {
+    alignas(16) unsigned char walk[64];   // a Walk<NR>
+    Item it;
+};
+template <int NR>
+__device__ __forceinline__ void begin_steps(Steps *s, const Batch &a, const Begin &b) {
+    static_assert(sizeof(Walk<NR>) <= sizeof(s->walk), "room for a walk");
+    if ((threadIdx.x & 31) == 0) *reinterpret_cast<Walk<NR> *>(s->walk) = Walk<NR>(a, b);
+    __syncwarp();
+}
+template <int NR>
+__device__ __forceinline__ bool next_step(Steps *s, const Batch &a) {
+    int more = 0;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        Walk<NR> w = *reinterpret_cast<Walk<NR> *>(s->walk);
+        Item it;
+        more = w.next(a, it);
+        *reinterpret_cast<Walk<NR> *>(s->walk) = w;
+        if (more) s->it = it;
+    }
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, more, 0) != 0;
+}
+
 struct Misc {
-    uint64_t full[4], empty[4];           // a slot and its block of K
-    uint64_t x_full, x_empty, s_full, p_full, o_full, done;
+    uint64_t full[4], empty[4];           // a slot
+    uint64_t r_full, s_full, p_full, o_full, x_full, done;   // (the first ten in this order: Products)
     uint32_t tmem;
     int fail;
     Begin begin;                          // this CTA's units
+    Steps steps[kFeedWarps];              // by producer warp
     alignas(16) float factor[2][64];      // of a row's scores, log2 units; row tiles in turn
     // per column (row of the tile), by softmax group
     float red[2][4][32];                  // cross-warp reductions
@@ -77,7 +122,7 @@ struct Misc {
     alignas(16) float f[2][32];           // rescale factor, then the unit / sum
     alignas(16) int seen[2][32];          // positions it may see
 };
-static_assert(sizeof(Misc) <= 4096, "control block");
+static_assert(sizeof(Misc) <= kMisc, "control block");
 
 struct Args : Batch {
     const __nv_bfloat16 *q;
@@ -91,26 +136,11 @@ struct Args : Batch {
     float *ws_o;                          // [2 G][NR][512]
 };
 
-// A sector (32 bytes) of global memory.
-struct Sector {
-    uint32_t w[8];
-};
-__device__ __forceinline__ void load_sector(Sector &s, const uint8_t *p, bool there) {
-    if (there) {
-        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(s.w[0]), "=r"(s.w[1]), "=r"(s.w[2]), "=r"(s.w[3]), "=r"(s.w[4]), "=r"(s.w[5]),
-                       "=r"(s.w[6]), "=r"(s.w[7])
-                     : "l"(p));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s.w[i] = 0u;
-    }
+// 16 bytes global -> shared past the first-level cache; zeros where `there` is not.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t *v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Biased exponent of the largest magnitude of eight bf16 (255: not finite).
 __device__ __forceinline__ uint32_t top8(uint4 u) {
@@ -127,6 +157,22 @@ __device__ __forceinline__ uint4 to_half8(uint4 u, float f) {
     for (int i = 0; i < 8; ++i) x[i] *= f;
     return pack_h8(x);
 }
+// The codes of a word times their scale.  The conversions take a word's bytes as
+// they are: with the multiplications a word costs 9 instructions (shifts and masks
+// that build fp16 numbers: 19).
+__device__ __forceinline__ uint4 values8(uint32_t w, __half2 s) {
+    uint32_t a, b, c, d;
+    asm("{\n\t.reg .b8 p, q, r, t;\n\t"
+        "mov.b32 {p, q, r, t}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, p;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, q;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, r;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, t;\n\t}"
+        : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+        : "r"(w));
+    return make_uint4(h2_bits(__hmul2(h2_of(a), s)), h2_bits(__hmul2(h2_of(b), s)), h2_bits(__hmul2(h2_of(c), s)),
+                      h2_bits(__hmul2(h2_of(d), s)));
+}
 __device__ __forceinline__ uint4 scaled8(uint4 u, float f, float g) {
     float x[8];
     unpack_bf8(u, x);
@@ -135,30 +181,99 @@ __device__ __forceinline__ uint4 scaled8(uint4 u, float f, float g) {
     return pack_bf8(x);
 }
 
+// The products of a tile, issued by one lane of a warp that stays together.  The
+// operands are laid down once: a product is issued every 40 cycles or so.
+template <int NR>
+struct Products {
+    using F = Cfg<NR>;
+    Operand x, k, v, p;
+    uint32_t tmem, bars;                  // bars: full, empty, r_full, s_full, p_full, o_full
+    volatile int *fail;
+
+    __device__ __forceinline__ Products(uint8_t *sm, Misc *M, uint32_t tm)
+        : x(operand(sm + F::X, 16, 1024)), k(operand(sm + F::C, 16, 2048)), v(operand(sm + F::C, 1024, 2048)),
+          p(operand(sm + F::P, 16, 1024)), tmem(tm), bars(smem_u32(M->full)), fail(&M->fail) {}
+    static constexpr uint32_t kFull = 0, kEmpty = 32, kR = 64, kS = 72, kP = 80, kO = 88;
+
+    __device__ __forceinline__ bool seen(uint32_t bar, uint32_t n) const {
+        const bool ok = wait_or_fail(bars + bar, n & 1, fail);
+        tc_fence_after();
+        return ok;
+    }
+    // S^T of tile n, block by block as they are written, the shared channels last.
+    __device__ __forceinline__ bool scores(uint32_t n) const {
+        constexpr uint32_t id = instr_desc(kFmtF16, 128, NR, 0, 0), id_r = instr_desc(kFmtBF16, 128, NR, 0, 0);
+        bool ok = true;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            ok &= seen(kFull + 8 * j, n);
+            if (elect_one()) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const Operand ke = k + (j * kSlot + (e >> 2) * 1024u + (e & 3) * 32u);
+                    const Operand xe = x + ((2 * j + (e >> 2)) * NR * 128u + (e & 3) * 32u);
+                    if (j == 0 && e == 0) mma_ss<false>(tmem + TM_S, ke, xe, id, false);
+                    else mma_ss<true>(tmem + TM_S, ke, xe, id);
+                }
+            }
+            __syncwarp();
+        }
+        ok &= seen(kR, n);
+        if (elect_one()) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mma_ss<true>(tmem + TM_S, p + e * 32u, x + (8 * NR * 128u + e * 32u), id_r);
+            commit(bars + kS);
+        }
+        __syncwarp();
+        return __all_sync(0xffffffffu, ok);
+    }
+    // O^T += c^T P^T, a slot released as soon as its block is done (P's rows are one 128-byte atom
+    // wide, 16 rows a step).
+    __device__ __forceinline__ bool output(uint32_t n, bool acc, bool last) const {
+        constexpr uint32_t id = instr_desc(kFmtF16, 128, NR, 1, 1);
+        const bool ok = __all_sync(0xffffffffu, seen(kP, n));
+        if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const Operand vj = v + j * kSlot;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (e == 0) mma_ss<false>(tmem + TM_O + 64 * j, vj, p, id, acc);
+                    else mma_ss<true>(tmem + TM_O + 64 * j, vj + e * 4096u, p + e * 2048u, id);
+                }
+                if (ok) commit(bars + kEmpty + 8 * j);
+            }
+            if (last) commit(bars + kO);
+        }
+        __syncwarp();
+        return ok;
+    }
+};
+
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1)
-latent4_decode_kernel(const Args a) {
+latent4_decode_kernel(const __grid_constant__ Args a) {
     using F = Cfg<NR>;
     constexpr int NC = NR / 2;                // columns of a softmax group
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Misc *M = reinterpret_cast<Misc *>(sm + F::MISC);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int cta = blockIdx.x, group = cta / a.side;   // groups of CTAs side by side
+    const int cta = blockIdx.x;
 
     // ---- barriers and tensor memory, under the end of the kernel before this one
     if (t == 0) {
         M->fail = 0;
-        for (int i = 0; i < 4; ++i) { mbar_init(&M->full[i], kFeedWarps); mbar_init(&M->empty[i], 1); }
+        for (int i = 0; i < 4; ++i) { mbar_init(&M->full[i], kFeedWarps / 2); mbar_init(&M->empty[i], 1); }
+        mbar_init(&M->r_full, kFeedWarps);
         mbar_init(&M->x_full, kFeedWarps);
-        mbar_init(&M->x_empty, 1);
         mbar_init(&M->s_full, 1);
         mbar_init(&M->p_full, kSoftWarps);
         mbar_init(&M->o_full, 1);
         mbar_init(&M->done, 1);
         fence_mbar_init();
     }
-    if (warp == kThreads / 32 - 1) tmem_alloc(&M->tmem, kTmemCols);
+    if (warp == 0) tmem_alloc(&M->tmem, kTmemCols);
     wait_for_previous();
     if (t == 0) a.split[cta] = Split{0, 0, 0, 0};
     find_units<NR, kThreads>(a, &M->begin, &g_kda_latent4_decode_error);
@@ -168,125 +283,89 @@ latent4_decode_kernel(const Args a) {
     tc_fence_after();
     const uint32_t tmem = M->tmem;
     volatile int *fail = &M->fail;
-    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;   // a warp's 32 TMEM lanes, lane field at bit 16
 
-    if (warp == kThreads / 32 - 1) {
-        // ================================================= matrix products
-        // the whole warp walks and waits, one lane issues
-        Walk<NR> walk(a, M->begin);
-        Item it;
-        uint32_t n_tile = 0, n_item = 0;
-        bool ok = true;
-        constexpr uint32_t id_s = instr_desc(kFmtF16, 128, NR, 0, 0);
-        constexpr uint32_t id_r = instr_desc(kFmtBF16, 128, NR, 0, 0);
-        constexpr uint32_t id_o = instr_desc(kFmtF16, 128, NR, 1, 1);
-        const Operand x_op = operand(sm + F::X, 16, 1024), k_op = operand(sm + F::C, 16, 2048);
-        const Operand v_op = operand(sm + F::C, 1024, 2048), p_op = operand(sm + F::P, 16, 1024);
-        const uint32_t full = smem_u32(M->full), empty = smem_u32(M->empty);
-        const uint32_t s_full = smem_u32(&M->s_full), p_full = smem_u32(&M->p_full);
-        while (ok && walk.next(a, it)) {
-            if (it.n == 0) continue;
-            ok &= wait_or_fail(&M->x_full, n_item & 1, fail);
-            for (int i = 0; i < it.n; ++i, ++n_tile) {
-                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                // S^T: the shared channels, which come with the first block, then the latent ones
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ok &= wait_or_fail(full + 8 * j, n_tile & 1, fail);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        if (j == 0) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                mma_ts(tmem + F::S, tmem + F::R + 8 * e, x_op + (8 * NR * 128u + e * 32u), id_r, e > 0);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const Operand xe = x_op + ((2 * j + (e >> 2)) * NR * 128u + (e & 3) * 32u);
-                            if (j < F::KB)
-                                mma_ts(tmem + F::S, tmem + F::K + 64 * j + 8 * e, xe, id_s, true);
-                            else
-                                mma_ss<true>(tmem + F::S, k_op + (j * kSlot + (e >> 2) * 1024u + (e & 3) * 32u), xe, id_s);
-                        }
-                    }
-                    __syncwarp();
-                }
-                if (elect_one()) {
-                    commit(s_full);
-                    if (i + 1 == it.n && ok) mma_commit(&M->x_empty);
-                }
-                __syncwarp();
-                // O^T += c^T P^T, a slot released as soon as its block is done (P's rows are one
-                // 128-byte atom wide, 16 rows a step)
-                ok &= wait_or_fail(p_full, n_tile & 1, fail);
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const Operand v = v_op + j * kSlot;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if (e == 0) mma_ss<false>(tmem + F::O + F::OB * j, v, p_op, id_o, i > 0);
-                            else mma_ss<true>(tmem + F::O + F::OB * j, v + e * 4096u, p_op + e * 2048u, id_o);
-                        }
-                        if (ok) commit(empty + 8 * j);
-                    }
-                    if (i + 1 == it.n) mma_commit(&M->o_full);
-                }
-                __syncwarp();
-            }
-            ok = __all_sync(0xffffffffu, ok);         // one verdict, so that the warp stays together
-            ++n_item;
-        }
-        // nothing of this CTA's products is in flight when its TMEM goes
-        end_products(&M->done, fail);
-    } else if (warp >= kSoftWarps) {
+    if (warp >= kSoftWarps) {
         // ================================================= producers
-        const int w = warp - kSoftWarps, half = w >> 2;           // which 64 channels of each block
-        const int p = 32 * (w & 3) + lane;                        // position in the tile, TMEM lane
-        // the tiles, one in front of what is being written: its registers are loaded as they get free
-        Walk<NR> walk(a, M->begin);
-        Item it;
-        int i = 0;
-        it.n = it.tile = it.len = 0;
-        bool more = true;
-        const uint8_t *row = nullptr;                             // this thread's row; nullptr: none
-        auto advance = [&]() {
-            ++i;
-            while (more && i >= it.n) {
-                more = walk.next(a, it);
-                i = 0;
-            }
-            row = nullptr;
-            const int pos = (it.tile + i) * kTile + p;
-            if (more && pos < it.len) {
-                const int64_t r = a.pages.row(it.b, pos);
-                if (r >= 0) row = a.cache + (size_t)r * kLatent4Row;
-                else atomicOr(&g_kda_latent4_decode_error, kErrSlot);
-            }
-        };
-        Sector codes[4], pe[2], scales;
-        auto load_codes = [&](int j) { load_sector(codes[j], row + 64 * j + 32 * half, row != nullptr); };
-        auto load_rest = [&]() {
-            load_sector(scales, row + k4Scales, row != nullptr);
-            load_sector(pe[0], row + k4Pe + 64 * half, row != nullptr);
-            load_sector(pe[1], row + k4Pe + 64 * half + 32, row != nullptr);
-        };
-        i = -1;
-        advance();
-        if (more) {
-            load_rest();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) load_codes(j);
-        }
-        uint32_t n_tile = 0, n_item = 0;
+        const int w = warp - kSoftWarps;
+        // Four warps a block, the first four the even ones: rows 32 (w % 4) + 8 k + pr of a tile, 32 of the
+        // block's channels
+        const int half = w >> 2, row0 = 32 * (w & 3) + (lane >> 2), pr = lane >> 2, pc = lane & 3;
         bool ok = true;
-        while (more && ok) {
-            if (i == 0) {
-                // ---- a new row tile's queries: a warp a row
-                if (n_item > 0) ok = warp_wait(&M->x_empty, (n_item - 1) & 1, fail);
+        uint32_t n_tile = 0, n_item = 0;
+        // ---- the tiles: tile `at` of row tile `it` is the next one, whose rows are copied ahead
+        Steps *const steps = &M->steps[w];
+        begin_steps<NR>(steps, a, M->begin);
+        const Item &it = steps->it;
+        int at = -1, tiles = 0;
+        bool more = true;
+        int mine = -1, rows[4];                         // the cache rows of a lane's row, of this thread's; -1: none
+        auto look = [&]() {
+            ++at;
+            while (more && at >= tiles) {
+                more = next_step<NR>(steps, a);
+                tiles = more ? it.n : 0;
+                at = 0;
+            }
+            if (!more) return;
+            // a lane a row, of this tile and of the one behind it in the row tile, which is asked into L2
+            // (a page holds 16 rows in a row at least)
+            const int pos = (it.tile + at) * kTile + 32 * (w & 3) + lane;
+            mine = -1;
+            if (pos < it.len) {
+                mine = (int)a.pages.row(it.b, pos);
+                if (mine < 0 && half == 0 && (lane & 15) == 0) atomicOr(&g_kda_latent4_decode_error, kErrSlot);
+            }
+            if (half == 0 && (lane & 15) == 0 && at + 1 < tiles && pos + kTile < it.len) {
+                const int64_t r = a.pages.row(it.b, pos + kTile);
+                if (r >= 0) bulk_prefetch_l2(a.cache + (size_t)r * kLatent4Row, 16 * kLatent4Row);
+            }
+        };
+        auto turn_to = [&]() {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) rows[k] = __shfl_sync(0xffffffffu, mine, 8 * k + pr);
+        };
+        const uint32_t ahead = smem_u32(sm + F::RAW) + t % (32 * kFeedWarps) * 16u, scales_at = smem_u32(sm + F::SC) + w * 1024u;
+        // 16 bytes of each of this thread's four rows, `from` their beginning
+        auto copy = [&](int from) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                copy16(ahead + k * (kAhead / 4), a.cache + (size_t)(rows[k] < 0 ? 0 : rows[k]) * kLatent4Row + from + 16 * pc,
+                       rows[k] >= 0);
+        };
+        auto copy_scales = [&]() {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (pc < 2)
+                    copy16(scales_at + (8 * k + pr) * 32u + 16 * pc,
+                           a.cache + (size_t)(rows[k] < 0 ? 0 : rows[k]) * kLatent4Row + k4Scales + 16 * pc, rows[k] >= 0);
+        };
+        auto take = [&](uint4 (&x)[4]) {
+            copies_done();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
+                             : "r"(ahead + k * (kAhead / 4)));
+        };
+        // The upper 64 channels' lanes take their words in another order, so that eight lanes that write
+        // together meet in no bank.
+        const bool turn = pc & 2;
+        const uint8_t *const my_scales = sm + F::SC + w * 1024u + pr * 32u + 2 * pc;
+        uint8_t *const my_slot = sm + F::C + (row0 >> 3) * 2048u + (pc >> 1) * 1024u + pr * 128u;
+        uint8_t *const my_shared = sm + F::P + row0 * 128u;
+        look();
+        bool now = more, fresh = more;                  // there is a tile at hand; it is its row tile's first
+        if (more) {
+            turn_to();
+            copy_scales();
+            copy(64 * half);
+        }
+        while (now && ok) {
+            if (fresh) {
+                // ---- a new row tile's queries, a warp a row; the last one's scores are done
+                if (n_tile > 0) ok = warp_wait(&M->s_full, (n_tile - 1) & 1, fail);
                 if (!ok) break;
-#pragma unroll 2
+#pragma unroll 1
                 for (int r = w; r < NR; r += kFeedWarps) {
                     uint4 u[3] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
                     if (r < it.rows) {
@@ -318,59 +397,73 @@ latent4_decode_kernel(const Args a) {
                 warp_arrive(&M->x_full);
                 ++n_item;
             }
-            uint32_t s4[4];
+            uint4 c[4];
+            take(c);
+            __syncwarp();                               // the warp's scales
+            copy(64 * half + 128);                      // what comes next: this warp's other block
+            look();
+            // ---- its blocks, each in fp16 before its slot is free.  One copy of this code and not four:
+            // unrolled, the roles' code does not fit the instruction cache, which takes twice the time
+#pragma unroll 1
+            for (int j = half; j < 4; j += 2) {
+                uint4 v[4][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s4[j] = half ? scales.w[2 * j + 1] : scales.w[2 * j];
-            uint32_t r16[16];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) { r16[k] = pe[0].w[k]; r16[8 + k] = pe[1].w[k]; }
-            advance();                                            // the row that is loaded from here on
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (n_tile > 0) ok = warp_wait(&M->empty[j], (n_tile - 1) & 1, fail);
-                if (!ok) break;
-                tc_fence_after();
-                if (j == 0) {
-                    tmem_st8u(tmem + lane_base + F::R + 16 * half, r16);
-                    tmem_st8u(tmem + lane_base + F::R + 16 * half + 8, r16 + 8);
-                    if (more) load_rest();
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t two = *reinterpret_cast<const uint16_t *>(my_scales + 256 * k + 8 * j);
+                    const __half2 s = scales2(two);
+                    const __half2 s0 = turn ? __high2half2(s) : __low2half2(s), s1 = turn ? __low2half2(s) : __high2half2(s);
+                    v[k][0] = values8(turn ? c[k].z : c[k].x, s0);
+                    v[k][1] = values8(turn ? c[k].w : c[k].y, s0);
+                    v[k][2] = values8(turn ? c[k].x : c[k].z, s1);
+                    v[k][3] = values8(turn ? c[k].y : c[k].w, s1);
                 }
-                uint8_t *dst = sm + F::C + j * kSlot + (p >> 3) * 2048u + half * 1024u + (p & 7) * 128u;
-                const __half2 s01 = scales2(s4[j] & 0xffffu), s23 = scales2(s4[j] >> 16);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {                     // 16 channels of one scale
-                    const __half2 s = g == 0   ? __half2half2(__low2half(s01))
-                                      : g == 1 ? __half2half2(__high2half(s01))
-                                      : g == 2 ? __half2half2(__low2half(s23))
-                                               : __half2half2(__high2half(s23));
-                    uint32_t v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        v[e] = h2_bits(__hmul2(codes2((codes[j].w[2 * g + (e >> 2)] >> (8 * (e & 3))) & 0xffu), s));
-                    if (j < F::KB) tmem_st8u(tmem + lane_base + F::K + 64 * j + 32 * half + 8 * g, v);
-                    *reinterpret_cast<uint4 *>(dst + (((2 * g) ^ (p & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                    *reinterpret_cast<uint4 *>(dst + (((2 * g + 1) ^ (p & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
+                take(c);                                // the next block, or a half of the shared channels
+                if (j < 2) {
+                    copy(k4Pe + 64 * half);
+                } else {                                // the next tile's rows, scales and first block
+                    __syncwarp();
+                    fresh = at == 0;
+                    now = more;
+                    if (more) {
+                        turn_to();
+                        copy_scales();
+                        copy(64 * half);
+                    }
                 }
-                if (more) load_codes(j);
-                tmem_wait_st();
+                if (n_tile > 0) ok &= warp_wait(&M->empty[j], (n_tile - 1) & 1, fail);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4 *>(my_slot + j * kSlot + k * 2048u +
+                                                   (((4 * (pc & 1) + (e ^ (turn ? 2 : 0))) ^ pr) << 4)) = v[k][e];
                 fence_proxy_async_smem();
-                tc_fence_before();
                 warp_arrive(&M->full[j]);
             }
+            // the shared channels, where P was
+            if (n_tile > 0) ok &= warp_wait(&M->empty[3], (n_tile - 1) & 1, fail);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                *reinterpret_cast<uint4 *>(my_shared + k * 1024u + (((4 * half + pc) ^ pr) << 4)) = c[k];
+            fence_proxy_async_smem();
+            warp_arrive(&M->r_full);
             ++n_tile;
         }
     } else {
-        // ================================================= softmax, output
+        // ================================================= softmax, output; warp 0 issues the products
+        const Products<NR> mma(sm, M, tmem);
         const int g = warp >> 2, quarter = warp & 3;
         const int col0 = g * NC;                        // this group's columns
         const int bar = 1 + g;
-        const int pos_in_tile = quarter * 32 + lane;
-        Walk<NR> walk(a, M->begin);
-        Item it;
+        const int p = quarter * 32 + lane;              // position in a tile, TMEM lane
+        const uint32_t lanes = tmem + ((uint32_t)quarter << 21);   // 32 lanes a quarter, lane field at bit 16
         uint32_t n_tile = 0, n_item = 0;
         bool ok = true;
-        const float unit = pow2(a.exponent);
-        while (ok && walk.next(a, it)) {
+        bool lost = false;                              // the group's verdict: a warp's own `ok` ends nothing alone
+        Walk<NR> walk(a, M->begin);
+        Item it;
+        while (!lost && walk.next(a, it)) {
+            const int n = it.n;
             float2 l[NC / 2];
 #pragma unroll
             for (int c = 0; c < NC / 2; ++c) l[c] = make_float2(0.f, 0.f);
@@ -385,12 +478,16 @@ latent4_decode_kernel(const Args a) {
             // from here on a tile needs masks: the first row's limit
             const int all_see = min(it.len, it.first_tok + it.row_in_seq / a.H);
             const float *factor = M->factor[n_item & 1] + col0;
-            for (int i = 0; i < it.n; ++i, ++n_tile) {
-                const int p0 = (it.tile + i) * kTile;
-                ok = warp_wait(&M->s_full, n_tile & 1, fail);
+            int p0 = it.tile * kTile;
+            for (int i = 0; i < n; ++i, ++n_tile, p0 += kTile) {
+                if (warp == 0) {
+                    if (i == 0) ok &= warp_wait(&M->x_full, n_item & 1, fail);
+                    ok &= mma.scores(n_tile);
+                }
+                ok &= warp_wait(&M->s_full, n_tile & 1, fail);
                 tc_fence_after();
                 float s[NC];
-                tmem_ldn<NC>(tmem + lane_base + F::S + col0, s);
+                tmem_ldn<NC>(lanes + TM_S + col0, s);
                 tmem_wait_ld();
                 // s <- s scale log2 e - m, with each row's factor
 #pragma unroll
@@ -404,7 +501,7 @@ latent4_decode_kernel(const Args a) {
                 if (p0 + kTile > all_see) {
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
-                        if (p0 + pos_in_tile >= M->seen[g][c]) s[c] = -CUDART_INF_F;
+                        if (p0 + p >= M->seen[g][c]) s[c] = -CUDART_INF_F;
                 }
                 float top = s[0];
 #pragma unroll
@@ -413,7 +510,7 @@ latent4_decode_kernel(const Args a) {
                     // a new maximum for every column of the group
                     const float mx = lanes_reduce<NC, true>(s, lane);
                     if (lane < NC) M->red[g][quarter][lane] = mx;
-                    if (bar_any(bar, 128, !ok)) { ok = false; break; }
+                    if (bar_any(bar, 128, !ok)) { lost = true; break; }
                     if (quarter == 0 && lane < NC) {
                         float up = fmaxf(fmaxf(M->red[g][0][lane], M->red[g][1][lane]),
                                          fmaxf(M->red[g][2][lane], M->red[g][3][lane])) - kLift;
@@ -440,7 +537,7 @@ latent4_decode_kernel(const Args a) {
                         for (int j = 0; j < 4; ++j) {
 #pragma unroll 1
                             for (int c0 = 0; c0 < NC; c0 += 8) {
-                                const uint32_t at = tmem + lane_base + F::O + F::OB * j + col0 + c0;
+                                const uint32_t at = lanes + TM_O + 64 * j + col0 + c0;
                                 float ov[8];
                                 tmem_ldn<8>(at, ov);
                                 tmem_wait_ld();
@@ -452,28 +549,28 @@ latent4_decode_kernel(const Args a) {
                         tmem_wait_st();
                     }
                 }
-                uint8_t *pr = sm + F::P + pos_in_tile * 128u;
+                uint8_t *dst = sm + F::P + p * 128u;
 #pragma unroll
                 for (int c = 0; c < NC; c += 8) {
-                    float p[8];
+                    float e[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = ex2_approx(s[c + e]);
+                    for (int k = 0; k < 8; ++k) e[k] = ex2_approx(s[c + k]);
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2)
-                        l[(c + e) / 2] = __fadd2_rn(l[(c + e) / 2], make_float2(p[e], p[e + 1]));
-                    *reinterpret_cast<uint4 *>(pr + ((((col0 + c) >> 3) ^ (pos_in_tile & 7)) << 4)) = pack_h8(p);
+                    for (int k = 0; k < 8; k += 2) l[(c + k) / 2] = __fadd2_rn(l[(c + k) / 2], make_float2(e[k], e[k + 1]));
+                    *reinterpret_cast<uint4 *>(dst + ((((col0 + c) >> 3) ^ (p & 7)) << 4)) = pack_h8(e);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 if (!left_out(n_tile)) warp_arrive(&M->p_full);
+                if (warp == 0) ok &= mma.output(n_tile, i > 0, i + 1 == n);
             }
-            if (!ok) break;
+            if (lost) break;
             // ---- the row tile's (piece's) output
             const bool whole = it.head && it.tail;
             const int slot = 2 * cta + (it.head ? 1 : 0);      // a piece that starts here goes on behind
-            if (it.n > 0) {
-                ok = warp_wait(&M->o_full, n_item & 1, fail);
-                if (bar_any(bar, 128, !ok)) { ok = false; break; }
+            if (n > 0) {
+                ok &= warp_wait(&M->o_full, n_item & 1, fail);
+                if (bar_any(bar, 128, !ok)) break;
                 tc_fence_after();
                 ++n_item;
             }
@@ -490,28 +587,29 @@ latent4_decode_kernel(const Args a) {
                 // joining kernel tells
                 const bool none = whole ? M->seen[g][lane] <= 0 : sum == 0.f;
                 const float lg = none ? -CUDART_INF_F : log2f(sum) - M->neg_m[g][lane];
-                M->f[g][lane] = none ? 0.f : unit / sum;
+                M->f[g][lane] = none ? 0.f : pow2(a.exponent) / sum;
                 if (col0 + lane < it.rows) {
                     if (!whole) a.ws_lse[slot * NR + col0 + lane] = lg;
                     else if (a.lse) a.lse[it.row + col0 + lane] = lg * 0.6931471805599453f;
                 }
             }
             bar_sync(bar, 128);
+            const int rows = it.rows;
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {
                 float ov[NC];
-                if (it.n > 0) {
-                    tmem_ldn<NC>(tmem + lane_base + F::O + F::OB * j + col0, ov);
+                if (n > 0) {
+                    tmem_ldn<NC>(lanes + TM_O + 64 * j + col0, ov);
                     tmem_wait_ld();
                 }
-                const int ch = 128 * j + pos_in_tile;
+                const int ch = 128 * j + p;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) ov[c] = it.n > 0 ? ov[c] * M->f[g][c] : 0.f;
+                for (int c = 0; c < NC; ++c) ov[c] = n > 0 ? ov[c] * M->f[g][c] : 0.f;
                 if (!whole) {
                     float *dst = a.ws_o + ((size_t)slot * NR + col0) * kLatent + ch;
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
-                        if (col0 + c < it.rows) dst[(size_t)c * kLatent] = ov[c];
+                        if (col0 + c < rows) dst[(size_t)c * kLatent] = ov[c];
                 } else {
                     // pairs of channels: even lanes store column c, odd lanes column c + 1
                     __nv_bfloat16 *dst = a.o + ((size_t)it.row + col0) * kLatent + (ch & ~1);
@@ -520,7 +618,7 @@ latent4_decode_kernel(const Args a) {
                     for (int c = 0; c < NC; c += 2) {
                         const float got = __shfl_xor_sync(0xffffffffu, odd ? ov[c] : ov[c + 1], 1);
                         const uint32_t two = odd ? pack_bf2(got, ov[c + 1]) : pack_bf2(ov[c], got);
-                        if (col0 + c + odd < it.rows)
+                        if (col0 + c + odd < rows)
                             *reinterpret_cast<uint32_t *>(dst + (size_t)(c + odd) * kLatent) = two;
                     }
                 }
@@ -529,17 +627,19 @@ latent4_decode_kernel(const Args a) {
             // the tile that starts here and goes on: who holds its last piece
             if (t == 0 && it.head && !it.tail) {
                 const long long last = it.unit + it.tiles - 1;
-                const int blind = min(it.rows, max(0, (1 - min(1, it.first_tok)) * a.H - it.row_in_seq));
-                a.split[cta] = Split{it.row, it.rows, (int)(last / M->begin.each) - group + 1, blind};
+                const int blind = min(rows, max(0, (1 - min(1, it.first_tok)) * a.H - it.row_in_seq));
+                a.split[cta] = Split{it.row, rows, (int)(last / M->begin.each) - cta / a.side + 1, blind};
             }
         }
+        // nothing of this CTA's products is in flight when its TMEM goes
+        if (warp == 0) end_products(&M->done, fail);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (*fail && t == 0) atomicOr(&g_kda_latent4_decode_error, kErrWait);   // a role gave up
-    if (warp == kThreads / 32 - 1) tmem_dealloc(tmem, kTmemCols);
+    if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
 template <int NR>
@@ -558,13 +658,25 @@ cudaError_t launch(const Args &a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t latent4_decode_workspace_bytes(int N, int64_t T, int H) { return pieces_bytes(rows_of_tile(N, T, H)); }
+namespace {
+
+// Rows of a tile: as for the bf16 cache (rows_of_tile), but at most 48, beside
+// which there is room for the pieces' ring.
+int rows_of_tile4(int N, int64_t T, int H) {
+    const int64_t rows = T == N ? H : (T * H + N - 1) / N * 4 / 3;
+    const int64_t tiles = (rows + 47) / 48;
+    return (int)std::min<int64_t>(48, std::max<int64_t>(1, ((rows + tiles - 1) / tiles + 15) / 16) * 16);
+}
+
+}  // namespace
+
+size_t latent4_decode_workspace_bytes(int N, int64_t T, int H) { return pieces_bytes(rows_of_tile4(N, T, H)); }
 
 cudaError_t launch_latent4_decode(const void *q, const void *cache, const int32_t *table,
                                   const int32_t *seq_lens, const int32_t *cu, float scale, int exponent,
                                   void *o, float *lse, int N, int64_t T, int H, int64_t P, int page,
                                   int max_pages, void *ws, cudaStream_t stream) {
-    const int NR = rows_of_tile(N, T, H);
+    const int NR = rows_of_tile4(N, T, H);
     uint8_t *w = static_cast<uint8_t *>(ws);
     Args a;
     a.pages = paged_rows(table, P, page, max_pages);
@@ -577,7 +689,7 @@ cudaError_t launch_latent4_decode(const void *q, const void *cache, const int32_
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.cache = static_cast<const uint8_t *>(cache);
     a.exponent = exponent;
-    a.scale_log2 = scale * 1.4426950408889634f * pow2(exponent);
+    a.scale_log2 = scale * 1.4426950408889634f * pow2(a.exponent);
     a.o = static_cast<__nv_bfloat16 *>(o);
     a.lse = lse;
     a.split = reinterpret_cast<Split *>(w);
@@ -586,8 +698,7 @@ cudaError_t launch_latent4_decode(const void *q, const void *cache, const int32_
     switch (NR) {
         case 16: return launch<16>(a, stream);
         case 32: return launch<32>(a, stream);
-        case 48: return launch<48>(a, stream);
-        default: return launch<64>(a, stream);
+        default: return launch<48>(a, stream);
     }
 }
 
