@@ -72,16 +72,19 @@ struct Cfg {
     static constexpr uint32_t X = 0;
     static constexpr uint32_t C = NR * 1152u;
     static constexpr uint32_t P = C + 4 * kSlot;                 // the shared channels, then P
+    // what is copied ahead has a place in shared memory where the queries leave one, else registers
+    static constexpr bool STAGED = NR <= 48;
     static constexpr uint32_t RAW = P + kProbs;
-    static constexpr uint32_t SC = RAW + kAhead;
-    static constexpr uint32_t MISC = SC + kScales;
-    static constexpr uint32_t BYTES = MISC + kMisc;
+    static constexpr uint32_t SC = RAW + (STAGED ? kAhead : 0);
+    static constexpr uint32_t MISC = SC + (STAGED ? kScales : 0);
+    static constexpr uint32_t STEPS = MISC + kMisc;   // the softmax warps' walks, where registers are short
+    static constexpr uint32_t BYTES = STEPS + (STAGED ? 0 : kSoftWarps * 128u);
     static_assert(BYTES + 1024 <= 232448, "shared memory of an SM");
 };
 
-// A producer warp's walk over the row tiles, which lies in shared memory: it is
-// looked at once a row tile, and a thread's registers are for what a tile needs.
-// Lane 0 walks.
+// A warp's walk over the row tiles, which lies in shared memory: it is looked at
+// once a row tile, and a thread's registers are for what a tile needs.  Lane 0
+// walks.
 struct Steps {
     alignas(16) unsigned char walk[64];   // a Walk<NR>
     Item it;
@@ -109,7 +112,7 @@ __device__ __forceinline__ bool next_step(Steps *s, const Batch &a) {
 
 struct Misc {
     uint64_t full[4], empty[4];           // a slot
-    uint64_t r_full, s_full, p_full, o_full, x_full, done;   // (the first ten in this order: Products)
+    uint64_t s_full, p_full, o_full, x_full, done;   // (up to o_full in this order: Products)
     uint32_t tmem;
     int fail;
     Begin begin;                          // this CTA's units
@@ -141,6 +144,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool th
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void load16(uint4 &v, const uint8_t *p, bool there) {
+    v = make_uint4(0u, 0u, 0u, 0u);
+    if (there)
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+}
+__device__ __forceinline__ void load2(uint32_t &v, const uint8_t *p, bool there) {
+    uint16_t two = 0;
+    if (there) asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(two) : "l"(p));
+    v = two;
+}
 
 // Biased exponent of the largest magnitude of eight bf16 (255: not finite).
 __device__ __forceinline__ uint32_t top8(uint4 u) {
@@ -187,26 +200,27 @@ template <int NR>
 struct Products {
     using F = Cfg<NR>;
     Operand x, k, v, p;
-    uint32_t tmem, bars;                  // bars: full, empty, r_full, s_full, p_full, o_full
+    uint32_t tmem, bars;                  // bars: full, empty, s_full, p_full, o_full
     volatile int *fail;
 
     __device__ __forceinline__ Products(uint8_t *sm, Misc *M, uint32_t tm)
         : x(operand(sm + F::X, 16, 1024)), k(operand(sm + F::C, 16, 2048)), v(operand(sm + F::C, 1024, 2048)),
           p(operand(sm + F::P, 16, 1024)), tmem(tm), bars(smem_u32(M->full)), fail(&M->fail) {}
-    static constexpr uint32_t kFull = 0, kEmpty = 32, kR = 64, kS = 72, kP = 80, kO = 88;
+    static constexpr uint32_t kFull = 0, kEmpty = 32, kS = 64, kP = 72, kO = 80;
 
-    __device__ __forceinline__ bool seen(uint32_t bar, uint32_t n) const {
-        const bool ok = wait_or_fail(bars + bar, n & 1, fail);
+    __device__ __forceinline__ bool seen(uint32_t bar, uint32_t n) const { return wait_or_fail(bars + bar, n & 1, fail); }
+    __device__ __forceinline__ void ordered() const {
+        fence_proxy_async_smem();
         tc_fence_after();
-        return ok;
     }
-    // S^T of tile n, block by block as they are written, the shared channels last.
+    // S^T of tile n, block by block as they are written; the shared channels come with the last two.
     __device__ __forceinline__ bool scores(uint32_t n) const {
         constexpr uint32_t id = instr_desc(kFmtF16, 128, NR, 0, 0), id_r = instr_desc(kFmtBF16, 128, NR, 0, 0);
         bool ok = true;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             ok &= seen(kFull + 8 * j, n);
+            ordered();
             if (elect_one()) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -215,16 +229,14 @@ struct Products {
                     if (j == 0 && e == 0) mma_ss<false>(tmem + TM_S, ke, xe, id, false);
                     else mma_ss<true>(tmem + TM_S, ke, xe, id);
                 }
+                if (j == 3) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mma_ss<true>(tmem + TM_S, p + e * 32u, x + (8 * NR * 128u + e * 32u), id_r);
+                    commit(bars + kS);
+                }
             }
             __syncwarp();
         }
-        ok &= seen(kR, n);
-        if (elect_one()) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mma_ss<true>(tmem + TM_S, p + e * 32u, x + (8 * NR * 128u + e * 32u), id_r);
-            commit(bars + kS);
-        }
-        __syncwarp();
         return __all_sync(0xffffffffu, ok);
     }
     // O^T += c^T P^T, a slot released as soon as its block is done (P's rows are one 128-byte atom
@@ -232,6 +244,7 @@ struct Products {
     __device__ __forceinline__ bool output(uint32_t n, bool acc, bool last) const {
         constexpr uint32_t id = instr_desc(kFmtF16, 128, NR, 1, 1);
         const bool ok = __all_sync(0xffffffffu, seen(kP, n));
+        ordered();
         if (elect_one()) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -265,7 +278,6 @@ latent4_decode_kernel(const __grid_constant__ Args a) {
     if (t == 0) {
         M->fail = 0;
         for (int i = 0; i < 4; ++i) { mbar_init(&M->full[i], kFeedWarps / 2); mbar_init(&M->empty[i], 1); }
-        mbar_init(&M->r_full, kFeedWarps);
         mbar_init(&M->x_full, kFeedWarps);
         mbar_init(&M->s_full, 1);
         mbar_init(&M->p_full, kSoftWarps);
@@ -298,7 +310,11 @@ latent4_decode_kernel(const __grid_constant__ Args a) {
         const Item &it = steps->it;
         int at = -1, tiles = 0;
         bool more = true;
-        int mine = -1, rows[4];                         // the cache rows of a lane's row, of this thread's; -1: none
+        // pages of a lane's row 32 (w % 4) + lane of it, and of that of the tile behind it in the row tile
+        // (-1: none); asked for by look(), waited for in turn_to()
+        int page_of = 0, page_ahead = 0, rows[4];       // rows: this thread's rows in the cache, -1: none
+        bool there = false, there_ahead = false;
+        auto place = [&]() { return (it.tile + at) * kTile + 32 * (w & 3) + lane; };
         auto look = [&]() {
             ++at;
             while (more && at >= tiles) {
@@ -307,58 +323,79 @@ latent4_decode_kernel(const __grid_constant__ Args a) {
                 at = 0;
             }
             if (!more) return;
-            // a lane a row, of this tile and of the one behind it in the row tile, which is asked into L2
-            // (a page holds 16 rows in a row at least)
-            const int pos = (it.tile + at) * kTile + 32 * (w & 3) + lane;
-            mine = -1;
-            if (pos < it.len) {
-                mine = (int)a.pages.row(it.b, pos);
-                if (mine < 0 && half == 0 && (lane & 15) == 0) atomicOr(&g_kda_latent4_decode_error, kErrSlot);
-            }
-            if (half == 0 && (lane & 15) == 0 && at + 1 < tiles && pos + kTile < it.len) {
-                const int64_t r = a.pages.row(it.b, pos + kTile);
-                if (r >= 0) bulk_prefetch_l2(a.cache + (size_t)r * kLatent4Row, 16 * kLatent4Row);
-            }
+            const int pos = place();
+            const int32_t *const table = a.pages.table + (size_t)it.b * a.pages.max_pages;
+            there = pos < it.len;
+            there_ahead = half == 0 && (lane & 15) == 0 && at + 1 < tiles && pos + kTile < it.len;
+            if (there) page_of = table[pos >> a.pages.page_log2];
+            if (there_ahead) page_ahead = table[(pos + kTile) >> a.pages.page_log2];
         };
         auto turn_to = [&]() {
+            const int in_page = place() & ((1 << a.pages.page_log2) - 1);
+            const bool good = there && page_of >= 0 && page_of < a.pages.P;
+            if (there && !good && half == 0) atomicOr(&g_kda_latent4_decode_error, kErrSlot);
+            const int mine = good ? (page_of << a.pages.page_log2) + in_page : -1;
 #pragma unroll
             for (int k = 0; k < 4; ++k) rows[k] = __shfl_sync(0xffffffffu, mine, 8 * k + pr);
+            // its rows on their way to L2: a page holds 16 in a row at least
+            if (there_ahead && page_ahead >= 0 && page_ahead < a.pages.P) {
+                const size_t r = ((size_t)page_ahead << a.pages.page_log2) + ((place() + kTile) & ((1 << a.pages.page_log2) - 1));
+                bulk_prefetch_l2(a.cache + r * kLatent4Row, 16 * kLatent4Row);
+            }
         };
-        const uint32_t ahead = smem_u32(sm + F::RAW) + t % (32 * kFeedWarps) * 16u, scales_at = smem_u32(sm + F::SC) + w * 1024u;
-        // 16 bytes of each of this thread's four rows, `from` their beginning
+        // what comes next, 16 bytes of each of this thread's rows (codes of a block, then shared channels),
+        // and the scales
+        uint4 next[4];
+        uint32_t scales[4];
+        const uint32_t ahead = smem_u32(sm + F::RAW) + (t - 32 * kSoftWarps) * 16u;
+        const uint32_t scales_at = smem_u32(sm + F::SC) + w * 1024u;
+        auto row = [&](int k) { return a.cache + (size_t)(rows[k] < 0 ? 0 : rows[k]) * kLatent4Row; };
         auto copy = [&](int from) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                copy16(ahead + k * (kAhead / 4), a.cache + (size_t)(rows[k] < 0 ? 0 : rows[k]) * kLatent4Row + from + 16 * pc,
-                       rows[k] >= 0);
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (F::STAGED) copy16(ahead + k * (kAhead / 4), row(k) + from + 16 * pc, rows[k] >= 0);
+                else load16(next[k], row(k) + from + 16 * pc, rows[k] >= 0);
+            }
         };
-        auto copy_scales = [&]() {
+        auto copy_scales = [&](int j) {                 // of block j; staged ones of all blocks with the first
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (pc < 2)
-                    copy16(scales_at + (8 * k + pr) * 32u + 16 * pc,
-                           a.cache + (size_t)(rows[k] < 0 ? 0 : rows[k]) * kLatent4Row + k4Scales + 16 * pc, rows[k] >= 0);
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (F::STAGED) {
+                    if (pc < 2 && j < 2) copy16(scales_at + (8 * k + pr) * 32u + 16 * pc, row(k) + k4Scales + 16 * pc, rows[k] >= 0);
+                } else {
+                    load2(scales[k], row(k) + k4Scales + 8 * j + 2 * pc, rows[k] >= 0);
+                }
+            }
         };
-        auto take = [&](uint4 (&x)[4]) {
-            copies_done();
+        auto take = [&]() {
+            if constexpr (F::STAGED) {
+                copies_done();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
-                             : "r"(ahead + k * (kAhead / 4)));
+                for (int k = 0; k < 4; ++k)
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(next[k].x), "=r"(next[k].y), "=r"(next[k].z), "=r"(next[k].w)
+                                 : "r"(ahead + k * (kAhead / 4)));
+            }
+        };
+        auto take_scales = [&](int j) {
+            if constexpr (F::STAGED) {
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    scales[k] = *reinterpret_cast<const uint16_t *>(sm + F::SC + w * 1024u + (8 * k + pr) * 32u + 8 * j + 2 * pc);
+            }
         };
         // The upper 64 channels' lanes take their words in another order, so that eight lanes that write
         // together meet in no bank.
         const bool turn = pc & 2;
-        const uint8_t *const my_scales = sm + F::SC + w * 1024u + pr * 32u + 2 * pc;
         uint8_t *const my_slot = sm + F::C + (row0 >> 3) * 2048u + (pc >> 1) * 1024u + pr * 128u;
         uint8_t *const my_shared = sm + F::P + row0 * 128u;
         look();
         bool now = more, fresh = more;                  // there is a tile at hand; it is its row tile's first
         if (more) {
             turn_to();
-            copy_scales();
             copy(64 * half);
+            copy_scales(half);
         }
         while (now && ok) {
             if (fresh) {
@@ -393,60 +430,57 @@ latent4_decode_kernel(const __grid_constant__ Args a) {
                             scaled8(u[2], pow2(er1), pow2(er - er1));
                     if (lane == 0) M->factor[n_item & 1][r] = a.scale_log2 * pow2(-e);
                 }
-                fence_proxy_async_smem();
                 warp_arrive(&M->x_full);
                 ++n_item;
             }
-            uint4 c[4];
-            take(c);
-            __syncwarp();                               // the warp's scales
-            copy(64 * half + 128);                      // what comes next: this warp's other block
+            take();
+            if (F::STAGED) copy(64 * half + 128);       // what comes next: this warp's other block
             look();
             // ---- its blocks, each in fp16 before its slot is free.  One copy of this code and not four:
             // unrolled, the roles' code does not fit the instruction cache, which takes twice the time
 #pragma unroll 1
             for (int j = half; j < 4; j += 2) {
                 uint4 v[4][4];
+                take_scales(j);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t two = *reinterpret_cast<const uint16_t *>(my_scales + 256 * k + 8 * j);
-                    const __half2 s = scales2(two);
+                    const uint4 c = next[k];
+                    const __half2 s = scales2(scales[k]);
                     const __half2 s0 = turn ? __high2half2(s) : __low2half2(s), s1 = turn ? __low2half2(s) : __high2half2(s);
-                    v[k][0] = values8(turn ? c[k].z : c[k].x, s0);
-                    v[k][1] = values8(turn ? c[k].w : c[k].y, s0);
-                    v[k][2] = values8(turn ? c[k].x : c[k].z, s1);
-                    v[k][3] = values8(turn ? c[k].y : c[k].w, s1);
+                    v[k][0] = values8(turn ? c.z : c.x, s0);
+                    v[k][1] = values8(turn ? c.w : c.y, s0);
+                    v[k][2] = values8(turn ? c.x : c.z, s1);
+                    v[k][3] = values8(turn ? c.y : c.w, s1);
                 }
-                take(c);                                // the next block, or a half of the shared channels
-                if (j < 2) {
-                    copy(k4Pe + 64 * half);
-                } else {                                // the next tile's rows, scales and first block
-                    __syncwarp();
-                    fresh = at == 0;
-                    now = more;
-                    if (more) {
-                        turn_to();
-                        copy_scales();
-                        copy(64 * half);
-                    }
+                if constexpr (F::STAGED) {
+                    take();                             // the other block, then a half of the shared channels
+                    if (j < 2) copy(k4Pe + 64 * half);
+                } else {
+                    copy(j < 2 ? 64 * j + 128 : k4Pe + 64 * half);
+                    if (j < 2) copy_scales(j + 2);
                 }
-                if (n_tile > 0) ok &= warp_wait(&M->empty[j], (n_tile - 1) & 1, fail);
+                if (n_tile > 0) ok &= warp_wait(&M->empty[j < 2 ? j : 3], (n_tile - 1) & 1, fail);   // with 3, P's place
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         *reinterpret_cast<uint4 *>(my_slot + j * kSlot + k * 2048u +
                                                    (((4 * (pc & 1) + (e ^ (turn ? 2 : 0))) ^ pr) << 4)) = v[k][e];
-                fence_proxy_async_smem();
+                if (j >= 2) {                           // a half of the shared channels, where P was
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4 *>(my_shared + k * 1024u + (((4 * half + pc) ^ pr) << 4)) = next[k];
+                }
                 warp_arrive(&M->full[j]);
             }
-            // the shared channels, where P was
-            if (n_tile > 0) ok &= warp_wait(&M->empty[3], (n_tile - 1) & 1, fail);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<uint4 *>(my_shared + k * 1024u + (((4 * half + pc) ^ pr) << 4)) = c[k];
-            fence_proxy_async_smem();
-            warp_arrive(&M->r_full);
+            fresh = at == 0;                            // the next tile
+            now = more;
+            if (more) {
+                __syncwarp();                           // the warp's scales have been read
+                turn_to();
+                copy(64 * half);
+                copy_scales(half);
+            }
             ++n_tile;
         }
     } else {
@@ -460,9 +494,16 @@ latent4_decode_kernel(const __grid_constant__ Args a) {
         uint32_t n_tile = 0, n_item = 0;
         bool ok = true;
         bool lost = false;                              // the group's verdict: a warp's own `ok` ends nothing alone
+        Steps *const steps = reinterpret_cast<Steps *>(sm + F::STEPS) + warp;
+        if constexpr (!F::STAGED) begin_steps<NR>(steps, a, M->begin);
         Walk<NR> walk(a, M->begin);
-        Item it;
-        while (!lost && walk.next(a, it)) {
+        Item own;
+        const Item &it = F::STAGED ? own : steps->it;
+        auto next = [&]() {
+            if constexpr (F::STAGED) return walk.next(a, own);
+            else return next_step<NR>(steps, a);
+        };
+        while (!lost && next()) {
             const int n = it.n;
             float2 l[NC / 2];
 #pragma unroll
@@ -559,7 +600,6 @@ latent4_decode_kernel(const __grid_constant__ Args a) {
                     for (int k = 0; k < 8; k += 2) l[(c + k) / 2] = __fadd2_rn(l[(c + k) / 2], make_float2(e[k], e[k + 1]));
                     *reinterpret_cast<uint4 *>(dst + ((((col0 + c) >> 3) ^ (p & 7)) << 4)) = pack_h8(e);
                 }
-                fence_proxy_async_smem();
                 tc_fence_before();
                 if (!left_out(n_tile)) warp_arrive(&M->p_full);
                 if (warp == 0) ok &= mma.output(n_tile, i > 0, i + 1 == n);
@@ -658,25 +698,13 @@ cudaError_t launch(const Args &a, cudaStream_t stream) {
 
 }  // namespace
 
-namespace {
-
-// Rows of a tile: as for the bf16 cache (rows_of_tile), but at most 48, beside
-// which there is room for the pieces' ring.
-int rows_of_tile4(int N, int64_t T, int H) {
-    const int64_t rows = T == N ? H : (T * H + N - 1) / N * 4 / 3;
-    const int64_t tiles = (rows + 47) / 48;
-    return (int)std::min<int64_t>(48, std::max<int64_t>(1, ((rows + tiles - 1) / tiles + 15) / 16) * 16);
-}
-
-}  // namespace
-
-size_t latent4_decode_workspace_bytes(int N, int64_t T, int H) { return pieces_bytes(rows_of_tile4(N, T, H)); }
+size_t latent4_decode_workspace_bytes(int N, int64_t T, int H) { return pieces_bytes(rows_of_tile(N, T, H)); }
 
 cudaError_t launch_latent4_decode(const void *q, const void *cache, const int32_t *table,
                                   const int32_t *seq_lens, const int32_t *cu, float scale, int exponent,
                                   void *o, float *lse, int N, int64_t T, int H, int64_t P, int page,
                                   int max_pages, void *ws, cudaStream_t stream) {
-    const int NR = rows_of_tile4(N, T, H);
+    const int NR = rows_of_tile(N, T, H);
     uint8_t *w = static_cast<uint8_t *>(ws);
     Args a;
     a.pages = paged_rows(table, P, page, max_pages);
@@ -698,7 +726,8 @@ cudaError_t launch_latent4_decode(const void *q, const void *cache, const int32_
     switch (NR) {
         case 16: return launch<16>(a, stream);
         case 32: return launch<32>(a, stream);
-        default: return launch<48>(a, stream);
+        case 48: return launch<48>(a, stream);
+        default: return launch<64>(a, stream);
     }
 }
 
