@@ -544,6 +544,8 @@ int kda_debug_latent_leave_out(unsigned int decode_tile, unsigned int prefill_ti
     const cudaError_t e = kda::latent_decode_leave_out(decode_tile);
     return cuda_status(e == cudaSuccess ? kda::latent_prefill_leave_out(prefill_tile) : e);
 }
+// The same for the decode kernel of the 4-bit cache.
+int kda_debug_latent4_leave_out(unsigned int tile) { return cuda_status(kda::latent4_decode_leave_out(tile)); }
 #endif
 
 }  // extern "C"

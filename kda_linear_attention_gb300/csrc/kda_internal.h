@@ -209,6 +209,7 @@ cudaError_t read_latent4_decode_error(unsigned int *code, bool reset);
 // The key tile whose arrival the kernel leaves out (latent_tc.cuh).
 cudaError_t latent_decode_leave_out(unsigned int tile);
 cudaError_t latent_prefill_leave_out(unsigned int tile);
+cudaError_t latent4_decode_leave_out(unsigned int tile);
 #endif
 
 // The conv prologue's arithmetic, shared by the prologue kernel and the

@@ -483,6 +483,7 @@ latent4_decode_kernel(const __grid_constant__ Args a) {
             }
             ++n_tile;
         }
+        copies_done();                                  // none is in flight when the block ends
     } else {
         // ================================================= softmax, output; warp 0 issues the products
         const Products<NR> mma(sm, M, tmem);
