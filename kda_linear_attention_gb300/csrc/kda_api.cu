@@ -412,6 +412,8 @@ int kda_latent_rotate(const void *x, int64_t x_token_stride, int64_t x_head_stri
     const int64_t e = dtype == KDA_BF16 ? 2 : 4;
     if (!row_strides(x_token_stride, x_head_stride, e) || !row_strides(out_token_stride, out_head_stride, e))
         return KDA_ERR_DIM;
+    // rows of x may be the same ones (broadcast), rows of out are written once
+    if ((T > 1 && out_token_stride < d) || (H > 1 && out_head_stride < d)) return KDA_ERR_DIM;
     const int r = rotation_status(amplitude, layout);
     if (r != KDA_OK) return r;
     if (inverse != 0 && inverse != 1) return KDA_ERR_VALUE;

@@ -19,7 +19,9 @@ namespace {
 // and c / scale are quotients of numbers of 8 and 4 significant bits, which meet a
 // border of e4m3 or e2m1 exactly or stay 2^-15 away from it, and both are exact
 // where they meet one.
-// Bound by HBM: 1,152 B in and 416 B out a token.
+// 1,152 B in and 416 B out a token; bound by its instructions, some 300 a token
+// (66,048 rows with rotation 29 us, 54 % of the measured copy; with divisions in
+// the Newton step's place 36).
 constexpr int kAppendThreads = 256;
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -95,7 +97,8 @@ latent4_append_kernel(const uint4 *__restrict__ x, uint8_t *__restrict__ cache, 
 // ---------------------------------------------------------------- gather
 // A warp takes four consecutive rows, all their loads in flight at once; a lane
 // turns four bytes of codes into 16 bytes of bf16, twice a row, so that both
-// sides are whole lines.  Bound by HBM: 416 B in and 1,152 B out a row.
+// sides are whole lines.  Bound by HBM: 416 B in and 1,152 B out a row (66,048
+// rows: 17 us, 90 % of the measured copy).
 constexpr int kGatherThreads = 256;
 constexpr int kGatherRows = 4;
 

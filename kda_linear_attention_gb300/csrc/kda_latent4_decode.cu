@@ -31,14 +31,36 @@
 //
 // A producer thread copies what it will read next into 64 bytes of its own
 // (cp.async, which needs no register and no line of the first-level cache:
-// beside 227 KB of shared memory that holds some 200, and plain loads a tile
-// ahead took two to three times as long), and reads it when its block's turn
-// comes; the rows are on their way from HBM to L2 a tile before.
+// beside 227 KB of shared memory that holds some 200), and reads it when its
+// block's turn comes; the rows are on their way from HBM to L2 a tile before.
+// Beside 64 rows' queries there is no room for that, and the next 64 bytes are
+// loaded into registers (64 sequences of 2,000-4,096 tokens at 96 heads, tiles of
+// 48 rows: 111 us so, 95 through shared memory; 128 of 8,000-8,192 at 64 heads:
+// two tiles of 32 rows through shared memory 356 us, one of 64 261 us).
 // The shared-memory writes of all roles are ordered before the tensor core's
 // reads by the warp that issues the products, between having seen the arrivals
-// and issuing: a fence in the writing threads would wait for their copies in
-// flight.  The roles' code is kept small for the instruction cache, and nothing
-// of a tile's is spilled.
+// and issuing: a fence in the writing threads waits for their copies in flight
+// (the same time within 1 %, and 400 to 600 cycles longer a softmax).
+//
+// What bounds it: the tile's chain, 5,700 cycles at 16 rows and 8,000 at 64:
+// softmax (450 and 1,400), the second product up to the slot that frees first
+// (900), a block's stores, the other block's conversion and stores (2,000), the
+// last scores (1,100).  Of these 2,200 are the products' reads of their operands
+// from shared memory, at 128 B a cycle, 1,000 the converted codes' writes and 500
+// a scheduler the conversions, 9 instructions a word.  The producers' own
+// instructions, some 1,000 a tile and warp at one in five cycles, are as long as
+// the chain.  Measured and not kept: codes turned into fp16 by shifts and masks
+// (19 instructions a word); the roles' loops unrolled (twice the time: the
+// instruction cache); rows brought by TMA in boxes of 64 bytes (900 rows' requests
+// a tile: 2,000 cycles from asking to arrival); all warps taking turns at the
+// softmax and the next tile (440 us where this takes 260: what comes next as
+// loads in 16 warps); sixteen producer warps (60 us where this takes 56); K as
+// the first product's operand in TMEM, which saves 1,000 cycles of shared-memory
+// reads a tile (92 us where this takes 95, 55 where 56).
+// Measured, a call with everything: 128 sequences of 8,000-8,192 tokens at 64
+// heads 261 us (the bf16 cache: 208); 64 of 2,000-4,096 at 96 heads 95 us (74);
+// 131,072 and 100,001 at 32 heads 56 us (60); 24 of 100-2,100 with drafts 27 us
+// (23); one of 1,000 at 16 heads 14 us (13).
 #include "latent4.cuh"
 #include "latent_walk.cuh"
 

@@ -177,6 +177,22 @@ def test_rotate_one_token_and_none():
     _clear()
 
 
+def test_rotate_a_row_for_all_heads():
+    """A broadcast input into a dense output; in place it is refused."""
+    torch, kda = _torch(), _kda()
+    turns, _ = kda.rotary_turns()
+    x, _ = _bf(_rng(9).normal(size=(5, 1, 64)))
+    lens, cu = _i32([40]), _i32([0, 5])
+    wide = x.expand(5, 7, 64)
+    got = kda.latent_rotate(wide, turns, lens, cu, out=torch.empty((5, 7, 64), dtype=x.dtype, device="cuda"))
+    _clear()
+    assert torch.equal(got, kda.latent_rotate(x.clone(), turns, lens, cu).expand(5, 7, 64))
+    before = x.clone()
+    with pytest.raises(kda.KDAError):
+        kda.latent_rotate(wide, turns, lens, cu)
+    assert torch.equal(x, before)
+
+
 def test_rotate_flags_bad_positions_and_offsets():
     torch, kda = _torch(), _kda()
     turns, _ = kda.rotary_turns()

@@ -74,7 +74,7 @@ def _decode4(L, **kw):
 @pytest.mark.parametrize("kw,status", BAD_ROTATION + [
     (dict(dtype=2), 5), (dict(N=0), 2), (dict(T=-1), 2), (dict(T=1 << 31), 2), (dict(T=1 << 62), 2), (dict(T=3), 2),
     (dict(H=0), 2), (dict(H=(1 << 24) + 1), 2), (dict(T=1 << 30, H=4, cu=GOOD), 2), (dict(d=0), 2), (dict(d=24), 2),
-    (dict(d=272), 2), (dict(xt=-8), 2), (dict(xt=4), 2), (dict(xh=1 << 31), 2), (dict(ot=100), 2), (dict(oh=-64), 2),
+    (dict(d=272), 2), (dict(xt=-8), 2), (dict(xt=4), 2), (dict(xh=1 << 31), 2), (dict(ot=100), 2), (dict(oh=-64), 2), (dict(ot=0), 2), (dict(oh=0), 2), (dict(oh=32), 2),
     (dict(dtype=1, xt=2), 2), (dict(inverse=2), 8), (dict(x=None), 1), (dict(out=None), 1), (dict(turns=None), 1),
     (dict(lens=None), 1), (dict(x=OFF4), 4), (dict(out=OFF4), 4), (dict(turns=OFF4), 4), (dict(cu=OFF4), 4)])
 def test_rotate_rejects_bad_arguments(L, kw, status):
