@@ -71,9 +71,10 @@ latent4_append_kernel(const uint4 *__restrict__ x, uint8_t *__restrict__ cache, 
     const float s = __low2float(scales2(s8)) / unit;
     // a scale of 0 has codes of 0 (signed); of NaN, any
     const float r = s > 0.f ? 1.f / s : 0.f;
-    if (top > tc::kHuge) {                          // infinities, which saturate
+    const float most = 8.f * s;
+    if (top > most && s > 0.f) {                    // past the last code (6), where c / s may be past fp32
 #pragma unroll
-        for (int i = 0; i < 16; ++i) c[i] = fmaxf(fminf(c[i], tc::kHuge), -tc::kHuge);
+        for (int i = 0; i < 16; ++i) c[i] = fmaxf(fminf(c[i], most), -most);
     }
     uint32_t code[2] = {0u, 0u};
 #pragma unroll

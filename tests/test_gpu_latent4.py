@@ -382,6 +382,27 @@ def test_append4_of_every_magnitude():
         assert _same_rows(cache.cpu().numpy()[0, :n], _quantised(rows))
 
 
+@pytest.mark.parametrize("exponent", [-32, -20, -9, 9, 32])
+def test_append4_of_every_magnitude_and_unit(exponent):
+    """Magnitudes far above and below the cache's unit saturate and vanish with
+    their signs."""
+    torch, kda = _torch(), _kda()
+    rng = _rng(52)
+    mags = torch.arange(0, 0x7F81, 7, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    n = -(-len(mags) // 32)
+    top = torch.zeros(n * 32, dtype=torch.bfloat16)
+    top[:len(mags)] = mags
+    share = torch.from_numpy(rng.choice([-1, 1], size=(n, 32, 16)) * rng.choice([0.0, 0.01, 0.3, 1.0], size=(n, 32, 16)))
+    x = torch.where(share == 0, share, top.view(n, 32, 1).double() * share).bfloat16()
+    rows = torch.cat([x.view(n, 512), torch.zeros((n, 64), dtype=torch.bfloat16)], 1).cuda()
+    page = 1 << (n - 1).bit_length()
+    cache = torch.zeros((1, page, 416), dtype=torch.uint8, device="cuda")
+    kda.latent4_append(rows, cache, _i32([[0]]), _i32([n]), _i32([0, n]), exponent=exponent)
+    _clear()
+    with np.errstate(invalid="ignore"):
+        assert _same_rows(cache.cpu().numpy()[0, :n], _quantised(rows, exponent))
+
+
 def test_append4_one_token_a_sequence_and_bad_places():
     torch, kda = _torch(), _kda()
     lens = [1, 16, 17, 100]
