@@ -36,7 +36,7 @@ latent_append_kernel(const uint4 *__restrict__ x, uint4 *__restrict__ cache, Pag
     // the row does not wait for the walk to its place
     const uint4 *src = x + (size_t)t * kRowChunks;
     uint4 a = __ldcs(src + lane), b = __ldcs(src + 32 + lane), c = make_uint4(0, 0, 0, 0);
-    float2 pe = make_float2(0.f, 0.f);
+    uint32_t pe = 0u;
     if (ROTATED) pe = load_pair(reinterpret_cast<const __nv_bfloat16 *>(src + 64), lane, rot.interleaved);
     else if (lane < 8) c = __ldcs(src + 64 + lane);
     const NewRow at = new_row(pages, seq_lens, cu, N, t, lane, &g_kda_latent_error);
@@ -52,7 +52,7 @@ latent_append_kernel(const uint4 *__restrict__ x, uint4 *__restrict__ cache, Pag
     dst[32 + lane] = b;
     if (ROTATED)
         store_pair(reinterpret_cast<__nv_bfloat16 *>(dst + 64), lane, rot.interleaved,
-                   rotated(pe.x, pe.y, rotation_of(rot, lane, at.pos)));
+                   turned_pair(pe, rotation_of(rot, lane, at.pos)));
     else if (lane < 8) dst[64 + lane] = c;
 }
 

@@ -44,7 +44,7 @@ latent4_append_kernel(const uint4 *__restrict__ x, uint8_t *__restrict__ cache, 
     // the row does not wait for the walk to its place
     const uint4 *src = x + (size_t)t * kRowChunks;
     uint4 a = __ldcs(src + 2 * lane), b = __ldcs(src + 2 * lane + 1);
-    float2 pe = load_pair(reinterpret_cast<const __nv_bfloat16 *>(src + 64), lane, rot.interleaved);
+    uint32_t pe = load_pair(reinterpret_cast<const __nv_bfloat16 *>(src + 64), lane, rot.interleaved);
     const NewRow at = new_row(pages, seq_lens, cu, N, t, lane, &g_kda_latent4_error);
     if (at.row < 0) return;
     if (norm_w) {
@@ -91,7 +91,7 @@ latent4_append_kernel(const uint4 *__restrict__ x, uint8_t *__restrict__ cache, 
     uint8_t *dst = cache + (size_t)at.row * kLatent4Row;
     reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(code[0], code[1]);
     dst[k4Scales + lane] = s8;
-    if (rot.turns) pe = rotated(pe.x, pe.y, rotation_of(rot, lane, at.pos));
+    if (rot.turns) pe = turned_pair(pe, rotation_of(rot, lane, at.pos));
     store_pair(reinterpret_cast<__nv_bfloat16 *>(dst + k4Pe), lane, rot.interleaved, pe);
 }
 

@@ -57,18 +57,25 @@ __device__ __forceinline__ float2 rotation_of(const Rotation &rot, int pair, int
 __device__ __forceinline__ float2 rotated(float a, float b, float2 cs) {
     return make_float2(a * cs.x - b * cs.y, b * cs.x + a * cs.y);
 }
-// The shared part of a row by one warp, a pair a lane: read ...
-__device__ __forceinline__ float2 load_pair(const __nv_bfloat16 *pe, int lane, bool interleaved) {
-    if (interleaved) return bf2_to_f2(reinterpret_cast<const uint32_t *>(pe)[lane]);
-    return make_float2(__bfloat162float(pe[lane]), __bfloat162float(pe[lane + kLatentPeDim / 2]));
+// The shared part of a row by one warp, a pair a lane (two bf16): read ...
+__device__ __forceinline__ uint32_t load_pair(const __nv_bfloat16 *pe, int lane, bool interleaved) {
+    if (interleaved) return reinterpret_cast<const uint32_t *>(pe)[lane];
+    const uint16_t *h = reinterpret_cast<const uint16_t *>(pe);
+    return h[lane] | (uint32_t)h[lane + kLatentPeDim / 2] << 16;
 }
-// ... and written with one rounding.
-__device__ __forceinline__ void store_pair(__nv_bfloat16 *pe, int lane, bool interleaved, float2 v) {
+// ... turned, with one rounding ...
+__device__ __forceinline__ uint32_t turned_pair(uint32_t pair, float2 cs) {
+    const float2 v = bf2_to_f2(pair);
+    return f2_to_bf2(rotated(v.x, v.y, cs));
+}
+// ... and written.
+__device__ __forceinline__ void store_pair(__nv_bfloat16 *pe, int lane, bool interleaved, uint32_t pair) {
     if (interleaved) {
-        reinterpret_cast<uint32_t *>(pe)[lane] = f2_to_bf2(v);
+        reinterpret_cast<uint32_t *>(pe)[lane] = pair;
     } else {
-        pe[lane] = __float2bfloat16_rn(v.x);
-        pe[lane + kLatentPeDim / 2] = __float2bfloat16_rn(v.y);
+        uint16_t *h = reinterpret_cast<uint16_t *>(pe);
+        h[lane] = (uint16_t)pair;
+        h[lane + kLatentPeDim / 2] = (uint16_t)(pair >> 16);
     }
 }
 static_assert(kLatentPeDim == 64, "a pair a lane");

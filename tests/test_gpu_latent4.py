@@ -403,6 +403,20 @@ def test_append4_of_every_magnitude_and_unit(exponent):
         assert _same_rows(cache.cpu().numpy()[0, :n], _quantised(rows, exponent))
 
 
+def test_append4_keeps_the_bits_of_the_shared_part():
+    """All 65,536 bit patterns, NaN's payloads among them."""
+    torch, kda = _torch(), _kda()
+    bits = torch.arange(-(1 << 15), 1 << 15, dtype=torch.int32).to(torch.int16).view(1024, 64)
+    rows = torch.cat([torch.zeros((1024, 512), dtype=torch.int16), bits], 1).view(torch.bfloat16).cuda()
+    cache = torch.zeros((16, 64, 416), dtype=torch.uint8, device="cuda")
+    where = (_i32(np.arange(16)[None]), _i32([1024]), _i32([0, 1024]))
+    kda.latent4_append(rows, cache, *where)
+    back = kda.latent4_gather(cache, where[0], where[2], total=1024)
+    _clear()
+    assert np.array_equal(cache.cpu().numpy().reshape(1024, 416)[:, 256:384].copy().view(np.int16), bits.numpy())
+    assert np.array_equal(back[:, 512:].contiguous().view(torch.int16).cpu().numpy(), bits.numpy())
+
+
 def test_append4_one_token_a_sequence_and_bad_places():
     torch, kda = _torch(), _kda()
     lens = [1, 16, 17, 100]
