@@ -863,24 +863,32 @@ def rotary_turns(d: int = LATENT_PE, base: float = 10000.0, method: Optional[str
         if method == "ntk":
             if d == 2:
                 raise ValueError("'ntk' needs d > 2")
-            base = base * factor ** (d / (d - 2))
+            try:
+                base = base * factor ** (d / (d - 2))
+            except OverflowError:
+                base = math.inf
+            if not 0 < base < math.inf:
+                raise ValueError("base and factor are out of range together")
         f = [base ** (-2.0 * i / d) for i in range(d // 2)]
         if method == "linear":
             f = [x / factor for x in f]
         elif method == "yarn":
-            if not trained_length or trained_length < 1:
+            if not trained_length or not 1 <= trained_length < math.inf:
                 raise ValueError("'yarn' needs trained_length")
-            if base == 1.0 or not beta_fast > beta_slow > 0:
-                raise ValueError("'yarn' needs a base other than 1 and beta_fast > beta_slow > 0")
+            if base <= 1.0 or not math.inf > beta_fast > beta_slow > 0:
+                raise ValueError("'yarn' needs a base above 1 and beta_fast > beta_slow > 0")
 
             def pair_of(turns):       # the (fractional) pair that makes so many turns in trained_length
                 return d * math.log(trained_length / (turns * 2 * math.pi)) / (2 * math.log(base))
 
             lo = max(0, math.floor(pair_of(beta_fast)))
             hi = min(d - 1, math.ceil(pair_of(beta_slow)))
-            ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3))) for i in range(d // 2)]
+            ramp = [1.0 if i >= pair_of(beta_slow) else min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3)))
+                    for i in range(d // 2)]
             f = [x / factor * r + x * (1 - r) for x, r in zip(f, ramp)]
             amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    if not all(abs(x) < 2.0 ** 900 for x in f):        # (whose turns fp64 holds)
+        raise ValueError("a frequency is out of range")
     whole = [round(x / (2 * math.pi) * 2.0 ** 64) & (2 ** 64 - 1) for x in f]
     turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in whole], dtype=_I64)
     return turns.to(device), amplitude

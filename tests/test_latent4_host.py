@@ -196,3 +196,22 @@ def test_turns_refuse_what_they_cannot_hold(kw):
     import kda_linear_attention_gb300 as kda
     with pytest.raises(ValueError):
         kda.rotary_turns(device="cpu", **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(method="yarn", trained_length=4096, base=0.5), dict(frequencies=[1e300] * 32),
+                                dict(method="yarn", trained_length=INF), dict(method="ntk", factor=1e300, base=1e300),
+                                dict(method="ntk", factor=1e305), dict(method="linear", factor=1e-305),
+                                dict(method="yarn", trained_length=64, beta_fast=INF)])
+def test_turns_refuse_what_is_out_of_range(kw):
+    pytest.importorskip("torch")
+    import kda_linear_attention_gb300 as kda
+    with pytest.raises(ValueError):
+        kda.rotary_turns(device="cpu", **kw)
+
+
+@pytest.mark.parametrize("length", [1, 4, 6])
+def test_yarn_divides_every_pair_of_a_context_below_a_turn(length):
+    pytest.importorskip("torch")
+    import kda_linear_attention_gb300 as kda
+    t, _ = kda.rotary_turns(64, method="yarn", factor=8.0, trained_length=length, device="cpu")
+    assert np.allclose(_radians(t), 10000.0 ** (-np.arange(32) / 32) / 8, rtol=1e-14, atol=WHOLE)
