@@ -529,7 +529,8 @@ size_t kda_latent_prefill_workspace_bytes(int N, int64_t Tq, int64_t Tk, int H, 
  *   x, out     T x H rows of d channels, a row's channels side by side; strides
  *              in elements between tokens and heads, multiples of 16 bytes.  A
  *              part of a head is given by its first channel's address.  x's may be
- *              0 (a row for all heads); out's rows lie apart.  out may be x (with
+ *              0 (a row for all heads); out's rows lie apart, all heads of a token
+ *              before the next token's or the other way round.  out may be x (with
  *              x's strides) and does not overlap it otherwise
  *   turns      [d / 2] int64
  *   seq_lens   [N] int32: lengths with the new tokens counted in

@@ -414,6 +414,15 @@ int kda_latent_rotate(const void *x, int64_t x_token_stride, int64_t x_head_stri
         return KDA_ERR_DIM;
     // rows of x may be the same ones (broadcast), rows of out are written once
     if ((T > 1 && out_token_stride < d) || (H > 1 && out_head_stride < d)) return KDA_ERR_DIM;
+    if (T > 1 && H > 1) {                     // the tokens' heads apart, or the heads' tokens
+        const bool by_token = out_token_stride >= out_head_stride;
+        const int64_t outer = by_token ? out_token_stride : out_head_stride;
+        const int64_t inner = by_token ? out_head_stride : out_token_stride;
+        if (outer < inner * ((by_token ? H : T) - 1) + d) return KDA_ERR_DIM;
+    }
+    // in place: each row where it was
+    if (x == out && ((T > 1 && x_token_stride != out_token_stride) || (H > 1 && x_head_stride != out_head_stride)))
+        return KDA_ERR_VALUE;
     const int r = rotation_status(amplitude, layout);
     if (r != KDA_OK) return r;
     if (inverse != 0 && inverse != 1) return KDA_ERR_VALUE;

@@ -215,3 +215,18 @@ def test_yarn_divides_every_pair_of_a_context_below_a_turn(length):
     import kda_linear_attention_gb300 as kda
     t, _ = kda.rotary_turns(64, method="yarn", factor=8.0, trained_length=length, device="cpu")
     assert np.allclose(_radians(t), 10000.0 ** (-np.arange(32) / 32) / 8, rtol=1e-14, atol=WHOLE)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(ot=64), 2), (dict(ot=64, oh=64), 2), (dict(ot=248), 2), (dict(ot=64, oh=120), 2),
+    (dict(xt=512), 8), (dict(xh=0), 8), (dict(ot=512), 8)])
+def test_rotate_rejects_outputs_that_overlap(L, kw, status):
+    assert _rotate(L, **kw) == status
+
+
+def test_rotate_takes_strides_in_either_order(L):
+    """Arguments that are right but for a pointer, which is looked at last."""
+    assert _rotate(L, ot=64, oh=128, turns=None) == 8       # in place with other strides
+    assert _rotate(L, xt=64, xh=128, ot=64, oh=128, turns=None) == 1
+    assert _rotate(L, ot=256, oh=64, turns=None) == 1
+    assert _rotate(L, xt=0, xh=0, T=1, N=1, H=1, turns=None) == 1
