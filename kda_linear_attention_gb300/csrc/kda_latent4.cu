@@ -13,12 +13,13 @@ namespace {
 
 // ---------------------------------------------------------------- append
 // A warp a token, a group of 16 channels a lane: the norm's sum is a warp
-// reduction, a group's maximum and codes are the lane's own.  The channels are
-// rounded to bf16 first, so that a row stands for what the bf16 cache would
-// hold; scale and codes then follow from it without a further rounding: max / 6
-// and c / scale are quotients of numbers of 8 and 4 significant bits, which meet a
-// border of e4m3 or e2m1 exactly or stay 2^-15 away from it, and both are exact
-// where they meet one.
+// reduction in the order of the bf16 append's (in another order a code or scale
+// moved in 9 of 524,288 rows), a group's maximum and codes are the lane's own.
+// The channels are rounded to bf16 first, so that a row stands for what the bf16
+// cache would hold; scale and codes then follow from it without a further
+// rounding: max / 6 and c / scale are quotients of numbers of 8 and 4 significant
+// bits, which meet a border of e4m3 or e2m1 exactly or stay 2^-15 away from it,
+// and both are exact where they meet one.
 // 1,152 B in and 416 B out a token; bound by its instructions, some 300 a token
 // (66,048 rows with rotation 29 us, 54 % of the measured copy; with divisions in
 // the Newton step's place 36).
@@ -48,7 +49,7 @@ latent4_append_kernel(const uint4 *__restrict__ x, uint8_t *__restrict__ cache, 
     const NewRow at = new_row(pages, seq_lens, cu, N, t, lane, &g_kda_latent4_error);
     if (at.row < 0) return;
     if (norm_w) {
-        const float ss = warp_sum(sumsq8(a) + sumsq8(b));
+        const float ss = warp_sum_of_neighbours(sumsq8(a), sumsq8(b), lane);
         const float n = 1.f / sqrtf(ss * (1.f / kLatent) + eps);
         a = scale8(a, n, norm_w + 16 * lane);
         b = scale8(b, n, norm_w + 16 * lane + 8);

@@ -12,6 +12,16 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
+// warp_sum of x_l + x_(32 + l) where lane l holds x_2l and x_(2l + 1): the same additions in the same
+// order, so the same bits.
+__device__ __forceinline__ float warp_sum_of_neighbours(float even, float odd, int lane) {
+    const bool up = lane & 16;            // the lower lanes go on with the even ones, the upper with the odd
+    float x = (up ? odd : even) + __shfl_xor_sync(0xffffffffu, up ? even : odd, 16);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
 // Block 0 raises bit 0 of its file's error word for offsets that decrease or leave [0, T] (the rest of
 // the kernel stays inside its buffers whatever they are).
 __device__ __forceinline__ void check_offsets(const int32_t *cu, int N, int T, unsigned int *error) {

@@ -775,3 +775,31 @@ def test_a_layer_in_chunks(interleaved):
         mag = SCALE * np.abs(_np(q)).max() * np.abs(kvr).max() * 192
         assert np.abs(_np(lse) - _np(plse)).max() <= 4 * HALF * mag
         _clear()
+
+
+def test_append4_of_many_normalised_rows_is_the_bf16_row_quantised():
+    """A sum of squares that is added in another order than the bf16 call's
+    rounds differently in a row of ten and moves a code in a row of tens of
+    thousands: half a million rows, plain and rotated, against the same rows
+    stored in bf16 and quantised as they lie there."""
+    torch, kda = _torch(), _kda()
+    N, L, page = 8, 1 << 16, 64
+    gen = torch.Generator(device="cuda").manual_seed(107)
+    x = (torch.randn((N * L, ol.ROW), generator=gen, device="cuda") * 3).bfloat16()
+    w = torch.randn(512, generator=gen, device="cuda")
+    table = torch.arange(N * L // page, dtype=torch.int32, device="cuda").view(N, -1)
+    where = (table, _i32([L] * N))
+    cu = _i32(np.arange(N + 1) * L)
+    turns, _ = kda.rotary_turns()
+    rows = torch.empty((N * L // page, page, ol.ROW), dtype=torch.bfloat16, device="cuda")
+    got, want = (torch.zeros((N * L // page, page, 416), dtype=torch.uint8, device="cuda") for _ in range(2))
+    for rot in (None, dict(amplitude=1.25, interleaved=False), dict(amplitude=1.0, interleaved=True)):
+        if rot is None:
+            kda.latent_append(x, rows, *where, cu, norm_w=w)
+        else:
+            kda.latent_append_rotated(x, rows, *where, turns, cu, norm_w=w, **rot)
+        kda.latent4_append(rows.view(-1, ol.ROW), want, *where, cu)
+        kda.latent4_append(x, got, *where, cu, norm_w=w, turns=None if rot is None else turns, **(rot or {}))
+        _clear()
+        off = (got != want).any(2).sum().item()
+        assert off == 0, "%d rows of %d differ" % (off, N * L)
