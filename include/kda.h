@@ -595,7 +595,10 @@ int kda_latent4_gather(const void *cache, const int32_t *block_table, const int3
 
 /*
  * kda_latent_decode over a 4-bit cache: the same arguments, outputs and rules,
- * with what the rows stand for in the rows' place.  workspace:
+ * with what the rows stand for in the rows' place.  The latent channels of a row
+ * of q are held to 2^-38 of the row's largest magnitude (at exponents above 0 the
+ * shared channels count 2^-exponent of theirs); shared channels of the cache are
+ * below 2^75 in magnitude (2^107 at exponents of 0 and above).  workspace:
  * kda_latent4_decode_workspace_bytes(N, T, H, ...) bytes.
  */
 int kda_latent4_decode(const void *q, const void *cache, const int32_t *block_table,

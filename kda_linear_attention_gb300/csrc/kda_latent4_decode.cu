@@ -7,13 +7,18 @@
 //   O^T [512 x rows]            += c^T [512 x 128] P^T         (4 blocks of 128 channels, 8 K-steps)
 // A code times its scale has 6 significant bits and lies in fp16's range, so
 // the latent operands are fp16, exactly what the cache stands for (but for its
-// unit 2^exponent, which goes into the factors of S and O).  The queries become
-// fp16 with a power of two a row that brings the row's largest magnitude to
-// 2^14: what fp16 then loses is below 2^-38 of that.  The shared channels stay
-// bf16 on both sides.  P is fp16 too: the running maximum is held at 2^7 and may
-// be passed by a factor 2^8 before O^T and the sums are rescaled, so P is below
-// 2^16, and what lies under fp16's normal numbers is below 2^-21 of the row's
-// largest weight.  Sums are fp32, of the unrounded probabilities.
+// unit 2^exponent, which goes into the factors of S and O).  The queries' latent
+// channels become fp16 with a power of two a row that brings the row's largest
+// magnitude to 2^14: what fp16 then loses is below 2^-38 of that.  The shared
+// channels stay bf16 on both sides, the queries' with 2^-exponent on top of that
+// power, so that their products are in the latent ones' unit.  At an exponent above
+// 0 they count among the row's magnitudes with it; below 0 without it, and then
+// reach 2^47, for which bf16 and fp32 have room (counted with it they took the row's
+// range: scores of rows whose two parts count alike were off by 0.01 at -32).
+// P is fp16 too: the running maximum is held at 2^7 and may be passed by a factor
+// 2^8 before O^T and the sums are rescaled, so P is below 2^16, and what lies under
+// fp16's normal numbers is below 2^-21 of the row's largest weight.  Sums are fp32,
+// of the unrounded probabilities.
 //
 // Work is dealt out and pieces are joined as latent_walk.cuh says.  Sixteen
 // warps, which leaves a thread 128 registers:
@@ -435,9 +440,10 @@ latent4_decode_kernel(const __grid_constant__ Args a) {
                     }
                     int top = (int)max(top8(u[0]), top8(u[1]));
                     const int tp = (int)top8(u[2]);
-                    if (tp > 0) top = max(top, tp == 255 ? 255 : tp - a.exponent);
+                    if (tp > 0) top = max(top, tp == 255 ? 255 : tp - max(a.exponent, 0));
                     top = __reduce_max_sync(0xffffffffu, top);
-                    // 2^e brings the row's largest magnitude to [2^14, 2^15); tiny rows to less
+                    // 2^e brings the row's largest magnitude to [2^14, 2^15); tiny rows to less.  The shared
+                    // part at 2^er stays below 2^(15 - min(0, exponent))
                     const int e = 141 - max(20, min(255, top));
                     const float f = pow2(e);
                     const int er = e - a.exponent, er1 = er / 2;

@@ -803,3 +803,22 @@ def test_append4_of_many_normalised_rows_is_the_bf16_row_quantised():
         _clear()
         off = (got != want).any(2).sum().item()
         assert off == 0, "%d rows of %d differ" % (off, N * L)
+
+
+@pytest.mark.parametrize("more", [0, 10])
+@pytest.mark.parametrize("exponent", [-32, -28, -24, -20, 0, 20, 32])
+def test_decode4_units_with_queries_of_one_size(exponent, more):
+    """Latents and shared channels of the cache's unit, or the shared ones 2^10
+    below it, under queries that balance them: both parts count alike in a
+    score, whatever the unit."""
+    c = Paged4(108, [300, 77], 32, exponent)
+    pe = (c.rng.normal(size=(c.P, 32, 64)) * 2.0 ** (exponent - more)).astype(np.float32)
+    c.rows[..., 256:384] = (pe.view(np.uint32) >> 16).astype(np.uint16).view(np.uint8)
+    dirty = c.rows.copy()
+    dirty[~c.held] = 0xFF
+    c.dev, c.ref = _torch().from_numpy(dirty).cuda(), o4.unpack(c.rows, exponent)
+    part = np.concatenate([np.ones(512), np.full(64, 2.0 ** more)])
+    q, qr = _bf(c.rng.normal(size=(2, 20, ol.ROW)) * part * 2.0 ** -exponent)
+    o, lse = c.decode(q, None)
+    _clear()
+    check(o, lse, c.want(qr, None), "exponent %d" % exponent)
