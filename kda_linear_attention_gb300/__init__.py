@@ -912,7 +912,15 @@ def latent_rotate(x: torch.Tensor, turns: torch.Tensor, seq_lens: torch.Tensor,
     opposite angles, which takes the gradient of out to that of x.  Writes and
     returns out (a tensor like x that shares no memory with it), or x itself
     where none is given.
+
+    No gradient is recorded: with gradients enabled, tensors that require one are
+    refused (call it from an autograd function, or under ``torch.no_grad()``).  A
+    rotation counts as a change of the tensor in place, so that a backward pass
+    that saved it before says so.
     """
+    if torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(out, "requires_grad", False)):
+        raise ValueError("latent_rotate records no gradient: call it under torch.no_grad(), and with inverse=True on "
+                         "the gradient of its output")
     dev = _device(x)
     if dev != _current_device():       # a launch goes to the current device
         with torch.cuda.device(dev):
@@ -942,6 +950,7 @@ def latent_rotate(x: torch.Tensor, turns: torch.Tensor, seq_lens: torch.Tensor,
         1 if inverse else 0, N, T, H, d, KDA_BF16 if x.dtype is _BF16 else KDA_F32, _raw_stream(dev, stream))
     if rc != 0:
         raise KDAError(rc, "kda_latent_rotate")
+    torch.autograd.graph.increment_version(out)
     return out
 
 

@@ -822,3 +822,47 @@ def test_decode4_units_with_queries_of_one_size(exponent, more):
     o, lse = c.decode(q, None)
     _clear()
     check(o, lse, c.want(qr, None), "exponent %d" % exponent)
+
+
+def test_rotate_and_autograd():
+    """A rotation raises the version of the tensor that it writes, and no other:
+    a backward pass over a tensor that was rotated after it was saved is an error
+    and not a wrong gradient.  Inside an autograd function it is differentiable."""
+    torch, kda = _torch(), _kda()
+    rng = _rng(112)
+    turns, amplitude = kda.rotary_turns(64, method="yarn", factor=8.0, trained_length=1024)
+    lens, cu = _i32([40]), _i32([0, 5])
+    x, xr = _to(rng.normal(size=(5, 3, 192)), torch.float32)
+    with pytest.raises(ValueError, match="gradient"):
+        kda.latent_rotate(x.clone().requires_grad_()[..., 128:], turns, lens, cu)
+    leaf = x.clone().requires_grad_()
+    y = leaf * 2
+    z = (y * y).sum()
+    with torch.no_grad():
+        kda.latent_rotate(y[..., 128:], turns, lens, cu)
+    with pytest.raises(RuntimeError, match="inplace"):
+        z.backward()
+    out = torch.empty_like(x[..., 128:])
+    before = x._version, out._version
+    kda.latent_rotate(x[..., 128:], turns, lens, cu, out=out)
+    assert x._version == before[0] and out._version > before[1]
+    with torch.inference_mode():
+        assert torch.equal(kda.latent_rotate(x[..., 128:].clone(), turns, lens, cu), out)
+
+    class Rotate(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a):
+            return kda.latent_rotate(a, turns, lens, cu, out=torch.empty_like(a), amplitude=amplitude)
+
+        @staticmethod
+        def backward(ctx, g):
+            return kda.latent_rotate(g, turns, lens, cu, out=torch.empty_like(g), amplitude=amplitude, inverse=True)
+
+    leaf = x.clone().requires_grad_()
+    g, gr = _to(rng.normal(size=(5, 3, 64)), torch.float32)
+    (Rotate.apply(leaf[..., 128:]) * g).sum().backward()
+    _clear()
+    freq = np.array([float(t) * 2.0 ** -64 * 2 * np.pi for t in turns.cpu().numpy().astype(np.uint64)])
+    want = o4.rotate(gr, np.arange(35, 40), freq, amplitude, inverse=True)
+    assert (np.abs(_np(leaf.grad[..., 128:]) - want) <= _rotation_limit(gr, want, amplitude, 2.0 ** -24, False)).all()
+    assert (leaf.grad[..., :128] == 0).all()

@@ -230,3 +230,19 @@ def test_rotate_takes_strides_in_either_order(L):
     assert _rotate(L, xt=64, xh=128, ot=64, oh=128, turns=None) == 1
     assert _rotate(L, ot=256, oh=64, turns=None) == 1
     assert _rotate(L, xt=0, xh=0, T=1, N=1, H=1, turns=None) == 1
+
+
+@pytest.mark.parametrize("which", ["x", "out", "view"])
+def test_rotate_refuses_tensors_that_require_a_gradient(which):
+    torch = pytest.importorskip("torch")
+    import kda_linear_attention_gb300 as kda
+    x, out = torch.zeros(1, 2, 64), torch.zeros(1, 2, 64)
+    turns, lens = torch.zeros(32, dtype=torch.int64), torch.ones(1, dtype=torch.int32)
+    if which == "view":
+        x = torch.zeros(1, 2, 80, requires_grad=True)[..., 16:]
+    else:
+        {"x": x, "out": out}[which].requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        kda.latent_rotate(x, turns, lens, out=out)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):     # goes on to the next check
+        kda.latent_rotate(x, turns, lens, out=out)
