@@ -527,11 +527,12 @@ size_t kda_latent_prefill_workspace_bytes(int N, int64_t Tq, int64_t Tk, int H, 
  * Rotate the d channels that x's rows point at.
  *
  *   x, out     T x H rows of d channels, a row's channels side by side; strides
- *              in elements between tokens and heads, multiples of 16 bytes.  A
- *              part of a head is given by its first channel's address.  x's may be
- *              0 (a row for all heads); out's rows lie apart, all heads of a token
- *              before the next token's or the other way round.  out may be x (with
- *              x's strides) and does not overlap it otherwise
+ *              in elements between tokens and heads, multiples of 16 bytes below
+ *              2^31, all rows within 2^60 elements.  A part of a head is given by
+ *              its first channel's address.  x's strides may be 0 (a row for all
+ *              heads); out's rows lie apart, all heads of a token before the next
+ *              token's or the other way round.  out may be x (with x's strides)
+ *              and does not overlap it otherwise
  *   turns      [d / 2] int64
  *   seq_lens   [N] int32: lengths with the new tokens counted in
  *   cu_seqlens [N + 1] int32, or NULL: one new token a sequence (then T = N)

@@ -40,11 +40,12 @@ int exponent_status(int exponent) {
     return exponent < -kda::kLatent4Exponent || exponent > kda::kLatent4Exponent ? KDA_ERR_VALUE : KDA_OK;
 }
 
-// Strides of rows of d elements of e bytes: rows apart by whole 16 bytes, and
-// all of T x H rows within 63 bits of bytes.
-bool row_strides(int64_t token, int64_t head, int64_t e) {
-    const int64_t most = int64_t(1) << 31;
-    return token >= 0 && head >= 0 && token < most && head < most && token * e % 16 == 0 && head * e % 16 == 0;
+// Strides of T x H rows of d elements of e bytes: whole 16 bytes, and all the
+// rows within 2^60 elements, so that a row's place in bytes fits 63 bits.
+bool row_strides(int64_t token, int64_t head, int64_t T, int H, int d, int64_t e) {
+    const int64_t most = int64_t(1) << 31;    // T and H are below it too: no product passes 62 bits
+    if (token < 0 || head < 0 || token >= most || head >= most || token * e % 16 != 0 || head * e % 16 != 0) return false;
+    return T == 0 || (T - 1) * token + (H - 1) * head + d <= (int64_t(1) << 60);
 }
 
 }  // namespace
@@ -410,7 +411,8 @@ int kda_latent_rotate(const void *x, int64_t x_token_stride, int64_t x_head_stri
     if (N < 1 || T < 0 || H < 1 || H > (1 << 24) || !rows_in_32_bits(T, H)) return KDA_ERR_DIM;
     if (d < 16 || d > 256 || d % 16 != 0 || (!cu_seqlens && T != N)) return KDA_ERR_DIM;
     const int64_t e = dtype == KDA_BF16 ? 2 : 4;
-    if (!row_strides(x_token_stride, x_head_stride, e) || !row_strides(out_token_stride, out_head_stride, e))
+    if (!row_strides(x_token_stride, x_head_stride, T, H, d, e) ||
+        !row_strides(out_token_stride, out_head_stride, T, H, d, e))
         return KDA_ERR_DIM;
     // rows of x may be the same ones (broadcast), rows of out are written once
     if ((T > 1 && out_token_stride < d) || (H > 1 && out_head_stride < d)) return KDA_ERR_DIM;

@@ -246,3 +246,17 @@ def test_rotate_refuses_tensors_that_require_a_gradient(which):
         kda.latent_rotate(x, turns, lens, out=out)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):     # goes on to the next check
         kda.latent_rotate(x, turns, lens, out=out)
+
+
+MOST = (1 << 31) - 1
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(xt=MOST - 7), 2), (dict(ot=MOST - 7), 2), (dict(xt=MOST - 7, dtype=1), 2), (dict(xt=1 << 30), 2),
+    (dict(xt=1 << 29), 1), (dict(ot=1 << 29), 1), (dict(xt=0), 1), (dict(T=1, xt=MOST - 7), 1),
+    (dict(T=0, xt=MOST - 7), 0)])
+def test_rotate_rejects_rows_past_2_to_the_60_elements(L, kw, status):
+    """Two numbers below 2^31 can multiply to more bytes than 63 bits count; all is
+    right but for that and a pointer, which is looked at later."""
+    a = dict(dict(out=ctypes.c_void_p(0x20000), xt=64, xh=64, ot=64, oh=64, T=MOST, N=1, H=1, cu=GOOD, turns=None), **kw)
+    assert _rotate(L, **a) == status
