@@ -866,3 +866,70 @@ def test_rotate_and_autograd():
     want = o4.rotate(gr, np.arange(35, 40), freq, amplitude, inverse=True)
     assert (np.abs(_np(leaf.grad[..., 128:]) - want) <= _rotation_limit(gr, want, amplitude, 2.0 ** -24, False)).all()
     assert (leaf.grad[..., :128] == 0).all()
+
+
+def _forms_limits(qr, rows, wk, wv, o):
+    """For one (token, head): how far lse and the value-expanded output of the
+    absorbed form may be from the expanded form's, over the rows it sees.
+
+    With q' = Wk q, k = c Wk and v = c Wv: the absorbed form rounds q' to bf16,
+    the expanded one k and v, each by HALF of its size at most and independently.
+    So a score is off by scale sum_j e_j q'_j c_pj there and by scale sum_j e_pj
+    q_j k_pj here; 7 times the root of the summed squares (Hoeffding, as in
+    check) bounds these sums, Da and De their largest over p, and also what they
+    come to, to first order, in lse (weights p) and in an output (weights
+    p (v - vm), vm = sum p v).  Second order: Da^2 / 2 in lse, 4 Da^2 e^2Da sum p
+    |v - vm| in an output (the third cumulant of weights changed by e^2Da), and
+    the same of De.  An output has the roundings of P (fp16 absorbed, bf16
+    expanded), of v, of the absorbed o (each channel, through Wv) and of the
+    expanded one besides, both the kernels' own fp32 as in check."""
+    q, c, r = qr[:128], rows[:, :512], rows[:, 512:]
+    k, v, qa = c @ wk, c @ wv, wk @ q
+    s = SCALE * (k @ q + r @ qr[128:])
+    p = np.exp(s - s.max())
+    p /= p.sum()
+    lse = s.max() + np.log(np.exp(s - s.max()).sum())
+    a, e = 7 * HALF * SCALE * qa, 7 * HALF * SCALE * np.sqrt((q * q) @ (k * k).T)      # e: of each score
+    da, de = np.sqrt((a * a) @ (c * c).T).max(), e.max()
+    mag = SCALE * ((np.abs(c) @ np.abs(qa)).max() + (np.abs(k) @ np.abs(q)).max() + 2 * (np.abs(r) @ np.abs(qr[128:])).max())
+    d = 80 * 2.0 ** -23 * mag                                       # of both kernels
+    lim_lse = np.sqrt(((a * (p @ c)) ** 2).sum()) + np.sqrt(((p * e) ** 2).sum()) + (da * da + de * de) / 2
+    lim_lse += d + 2 * 2.0 ** -20 * (1 + np.abs(lse))
+    dev = v - p @ v
+    first = np.sqrt((a * a) @ ((p[:, None] * c).T @ dev) ** 2) + np.sqrt((p * e) ** 2 @ dev ** 2)
+    second = 4 * (da * da * np.exp(2 * da) + de * de * np.exp(2 * de)) * (p @ np.abs(dev))
+    lim = first + second + 7 * (HALF16 + 2 * HALF) * np.sqrt((p * p) @ (v * v)) + (2 * d + 2 * 2.0 ** -20) * (p @ np.abs(v))
+    lim += 7 * HALF * np.sqrt((o * o) @ (wv * wv)) + HALF * np.abs(p @ v) + 2.0 ** -20 * ((p @ np.abs(c)) @ np.abs(wv))
+    return lim_lse, lim * (1 + 4 * HALF) + 2.0 ** -32 * len(rows) * 16 * np.abs(v).max()
+
+
+@pytest.mark.parametrize("news", [[40, 130], [3, 20], [1, 1]])
+def test_both_forms_over_the_same_rows(news):
+    """The absorbed form over 4-bit pages and the expanded form over the gathered
+    rows: each against the oracle, and the absorbed output, its values expanded,
+    against the expanded output."""
+    from test_gpu_latent import check as check_prefill
+    torch, kda = _torch(), _kda()
+    lens, H, page = [40, 163], 3, 16
+    c = Paged4(109, lens, page)
+    wk, wv = (c.rng.normal(size=(H, 512, 128)) / 16 for _ in range(2))
+    cu, cu_k = np.cumsum([0] + news), np.cumsum([0] + lens)
+    q, qr = _bf(c.rng.normal(size=(int(cu[-1]), H, 192)))
+    rows = kda.latent4_gather(c.dev, c.table_dev, _i32(cu_k), total=int(cu_k[-1]))
+    ref = [ol.sequence_rows(c.ref, c.table[b], 0, n) for b, n in enumerate(lens)]
+    assert np.array_equal(_np(rows), np.concatenate(ref))
+    qa, qar = _bf(ol.absorb(qr, wk))
+    o, lse = c.decode(qa, cu)
+    kv, kvr = _bf(ol.expand(_np(rows), wk, wv)[0])
+    po, plse = kda.latent_prefill(q, kv, rows[:, 512:], _i32(cu), _i32(cu_k))
+    _clear()
+    check(o, lse, c.want(qar, cu), "absorbed")
+    check_prefill(po, plse, ol.prefill(qr, kvr, _np(rows[:, 512:]), cu, cu_k, SCALE), "expanded")
+    o, lse, po, plse = (_np(t) for t in (o, lse, po, plse))
+    for b, (n, m) in enumerate(zip(news, lens)):
+        for i in range(n):
+            for h in range(H):
+                t = cu[b] + i
+                lim_lse, lim = _forms_limits(qr[t, h], ref[b][:m - n + i + 1], wk[h], wv[h], o[t, h])
+                assert abs(lse[t, h] - plse[t, h]) <= lim_lse, (b, i, h)
+                assert (np.abs(o[t, h] @ wv[h] - po[t, h]) <= lim).all(), (b, i, h)
