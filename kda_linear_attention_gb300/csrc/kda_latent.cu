@@ -15,10 +15,12 @@ namespace {
 // A warp a token: the row's 72 16-byte pieces are read once (lane l holds
 // latent pieces l and 32 + l, lanes 0..7 one of the shared part), the sum of
 // squares is a warp reduction in fp32, each value is rounded to bf16 once.
-// Bound by HBM: 1,152 B in and out a token (66,048 tokens: 30 us, 75 % of the
-// measured copy; two or four tokens a warp, and a grid that stays with the
-// weights in registers, measured 31 to 34 us; with the shared part rotated, a
-// pair a lane, 33).
+// 1,152 B in and out a token (66,048 tokens: 30 us, 75 % of the measured copy;
+// two or four tokens a warp, and a grid that stays with the weights in registers,
+// measured 31 to 34 us).  With the shared part rotated, a pair a lane, 32 us: no
+// limit is reached (325 instructions a token fill 66 % of the issue slots, DRAM is
+// at 53 %, the first-level cache, which has the norm's weights for every token, at
+// 64 %), and half of a warp's waiting is for its loads.
 constexpr int kAppendThreads = 256;
 
 template <bool ROTATED>

@@ -20,9 +20,11 @@ namespace {
 // rounding: max / 6 and c / scale are quotients of numbers of 8 and 4 significant
 // bits, which meet a border of e4m3 or e2m1 exactly or stay 2^-15 away from it,
 // and both are exact where they meet one.
-// 1,152 B in and 416 B out a token; bound by its instructions, some 300 a token
-// (66,048 rows with rotation 29 us, 54 % of the measured copy; with divisions in
-// the Newton step's place 36).
+// 1,152 B in and 416 B out a token; bound by its instructions: 358 a token with
+// rotation, 478 with the norm too, which fill 77 % of the issue slots while the SMs
+// are active (DRAM 37 % and 28 %).  66,048 rows: 25 us, 28 with rotation (54 % of the
+// measured copy), 35 with the norm, 37 with both (41 %); with divisions in the Newton
+// step's place 36 where it is 28.
 constexpr int kAppendThreads = 256;
 
 __device__ __forceinline__ float max_nan(float a, float b) {

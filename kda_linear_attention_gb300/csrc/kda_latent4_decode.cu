@@ -47,14 +47,18 @@
 // and issuing: a fence in the writing threads waits for their copies in flight
 // (the same time within 1 %, and 400 to 600 cycles longer a softmax).
 //
-// What bounds it: the tile's chain, 5,700 cycles at 16 rows and 8,000 at 64:
-// softmax (450 and 1,400), the second product up to the slot that frees first
-// (900), a block's stores, the other block's conversion and stores (2,000), the
-// last scores (1,100).  Of these 2,200 are the products' reads of their operands
-// from shared memory, at 128 B a cycle, 1,000 the converted codes' writes and 500
-// a scheduler the conversions, 9 instructions a word.  The producers' own
-// instructions, some 1,000 a tile and warp at one in five cycles, are as long as
-// the chain.  Measured and not kept: codes turned into fp16 by shifts and masks
+// What bounds it: a tile's chain.  By one block's clock, from scores to scores,
+// 5,600 cycles at 16 rows, 6,200 at 32, 6,800 at 48 and 8,400 at 64: softmax up to
+// its arrival (840 at 16 rows, 1,750 at 64), the second product up to the slot that
+// frees first (920, 1,270), its block's stores (1,030, 1,400), the other blocks'
+// conversion and stores (1,880, 2,700), the last scores (920, 1,330).  Of these
+// 2,200 are the products' reads of their operands from shared memory, at 128 B a
+// cycle, 1,000 the converted codes' writes and 500 a scheduler the conversions, 9
+// instructions a word.  The producers' own instructions, some 1,000 a tile and warp
+// at one in five cycles, are as long as the chain.  Over whole calls (152 sequences
+// of 512 to 8,192 tokens, in a graph) a tile comes to 3.0, 3.2, 3.5 and 4.5 us, and
+// 13, 18, 21 and 22 us are beside the tiles: launches, page lookups, first rows and
+// queries, pieces out and joined.  Measured and not kept: codes turned into fp16 by shifts and masks
 // (19 instructions a word); the roles' loops unrolled (twice the time: the
 // instruction cache); rows brought by TMA in boxes of 64 bytes (900 rows' requests
 // a tile: 2,000 cycles from asking to arrival); all warps taking turns at the
@@ -200,7 +204,7 @@ __device__ __forceinline__ uint4 to_half8(uint4 u, float f) {
 // The codes of a word times their scale.  The conversions take a word's bytes as
 // they are: with the multiplications a word costs 9 instructions (shifts and masks
 // that build fp16 numbers: 19).
-__device__ __forceinline__ uint4 values8(uint32_t w, __half2 s) {
+__device__ __forceinline__ uint4 halves8(uint32_t w, __half2 s) {
     uint32_t a, b, c, d;
     asm("{\n\t.reg .b8 p, q, r, t;\n\t"
         "mov.b32 {p, q, r, t}, %4;\n\t"
@@ -475,10 +479,10 @@ latent4_decode_kernel(const __grid_constant__ Args a) {
                     const uint4 c = next[k];
                     const __half2 s = scales2(scales[k]);
                     const __half2 s0 = turn ? __high2half2(s) : __low2half2(s), s1 = turn ? __low2half2(s) : __high2half2(s);
-                    v[k][0] = values8(turn ? c.z : c.x, s0);
-                    v[k][1] = values8(turn ? c.w : c.y, s0);
-                    v[k][2] = values8(turn ? c.x : c.z, s1);
-                    v[k][3] = values8(turn ? c.y : c.w, s1);
+                    v[k][0] = halves8(turn ? c.z : c.x, s0);
+                    v[k][1] = halves8(turn ? c.w : c.y, s0);
+                    v[k][2] = halves8(turn ? c.x : c.z, s1);
+                    v[k][3] = halves8(turn ? c.y : c.w, s1);
                 }
                 if constexpr (F::STAGED) {
                     take();                             // the other block, then a half of the shared channels

@@ -157,7 +157,7 @@ cudaError_t launch_latent_rotate(const void *x, int64_t x_token, int64_t x_head,
                                  const int32_t *cu, int N, int64_t T, int H, int d, bool bf16,
                                  cudaStream_t stream) {
     const int64_t e = bf16 ? 2 : 4;
-    // enough tokens for kUnits a thread, few enough for their angles and for a grid over all SMs
+    // enough tokens for kUnits a thread, few enough for their angles and for two blocks on each of 152 SMs
     const int64_t units = (int64_t)H * (d / 16);
     const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kUnits * kRotateThreads / units, T / 304));
     const int tokens = (int)std::min<int64_t>(std::min<int64_t>(want, kMaxTokens), kMaxPairs / (d / 2));
